@@ -58,7 +58,8 @@
 extern "C" {
 #endif
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
+/* SPEC_F16 only in the calls around the verify step that say so. */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype;
 
 typedef enum {
     SPEC_OK = 0,
@@ -84,7 +85,13 @@ enum {
     SPEC_ROW_BAD_PARENT = 5,           /* tree: parents[b,i] is not in [-1, i) */
     SPEC_ROW_OUTPUT_OVERFLOW = 6,      /* tree: accepted path + bonus does not fit in max_out */
     SPEC_ROW_BAD_UNIFORM = 7,          /* a uniform of the request is not in [0, 1) */
-    SPEC_ROW_BAD_PROPOSAL_ROW = 8      /* tree_verify_sample: qrow[b,i] is not in [0, Nq) */
+    SPEC_ROW_BAD_PROPOSAL_ROW = 8,     /* tree_verify_sample: qrow[b,i] is not in [0, Nq) */
+    SPEC_ROW_BAD_PAGE = 9,             /* cache calls: a page-table entry that the request needs is not
+                                          in [0, pages) */
+    SPEC_ROW_BAD_LENGTH = 10,          /* cache calls: lens[b] (or the length after the write) is
+                                          negative or more than the page table's row holds, or more
+                                          rows are to be written than there are */
+    SPEC_ROW_BAD_NODE = 11             /* kv_cache_write: a node of the accepted path has no row */
 };
 
 /*
@@ -374,6 +381,129 @@ spec_status spec_verify_noalloc(const void* target_logits, const void* draft_log
                                 int32_t* accepted_len, int32_t* out_tokens, int32_t* row_status,
                                 float* aux_lse_p, float* aux_lse_q, float* aux_accept,
                                 void* stream);
+
+/* ------------------------------------------------------------------ around the verify step
+ *
+ * What the target runs next to the verify calls in a speculative round: attention of the round's rows
+ * over the committed context (verify_attention), the processors that depend on what was generated
+ * (process_logits), and the commit of the accepted rows ("Exact speculative and assisted decoding for
+ * TinyRustLM", cache transactions: a round's keys and values are provisional until the verify step has
+ * accepted them).
+ *
+ * The key/value cache is paged and held in 8 bits:
+ *   k_cache, v_cache [pages, Hkv, page_size, D]  e4m3 codes; page_size 16, 32, 64 or 128; D 64 or 128;
+ *                                                16-byte aligned
+ *   k_scale, v_scale [pages, Hkv]                fp32, a power of two 2^e with e in [-60, 60] per page and head;
+ *                                                a code stands for code * scale
+ *   page_table [B, table_width]                  int32: token i of request b is in slot i mod page_size of
+ *                                                page page_table[b, i / page_size]
+ *   lens [B]                                     int32: committed tokens of each request
+ * Requests may share pages that no call writes.  Slots past a request's length are never interpreted: they
+ * may hold anything, and so may the scale of a page without tokens.
+ * Strides arguments (NULL: dense) are in elements, of the leading dimensions; the last one is contiguous.
+ */
+
+/*
+ * Logit processors of a round that depend on the request's history: penalties for repeated tokens, then
+ * biases, then a grammar mask ("M7.1" 0x03: p and q are the post-processor distributions, so the same
+ * call serves the target's rows and the draft's).
+ *
+ *   logits, out [B, R, V]   fp32 or bf16; strides[0..1] of each (request, row).  out may be logits itself
+ *                           (with equal strides) but must not overlap it otherwise
+ *   tokens  [B, N]          int32 drafted tokens, R <= N + 1, N <= 4096 (NULL when N == 0)
+ *   parents [B, N]          int32 in [-1, i), as the tree calls take it; NULL: a chain
+ *   history [B, H]          int32: tokens before the round (prompt, then output); entries outside [0, V) are
+ *                           ignored.  history_len [B] (NULL: H) of them count, the first prompt_len [B]
+ *                           (NULL: 0) are the prompt
+ *   repetition, presence, frequency [B]   fp32 (NULL: 1, 0, 0); repetition > 0
+ *   bias_tokens, bias_values [B, nb]      int32, fp32; entries outside [0, V) are ignored; of entries that
+ *                                         name one token the last holds
+ *   allowed [B, R, ceil(V/32)]            uint32 bits as in spec_verify_masked, NULL: no mask
+ *
+ * Row r follows the path to it: tokens 0..r-1 of a chain, the token of node r-1 and of its ancestors in a
+ * tree.  With c(v) the output tokens of the history and the path that are v, and seen(v) when c(v) > 0 or v is
+ * in the prompt, in fp32 and rounded once:
+ *   x = logits[b,r,v];  seen(v): x = x > 0 ? x / repetition : x * repetition
+ *   c(v) > 0: x = x - (frequency * c(v) + presence);  x = x + bias(v);  not allowed: x = -inf
+ * row_status [B] (nullable): SPEC_ROW_BAD_PARENT when a parent is out of range (a path ends at such a node), else OK.
+ */
+spec_status process_logits(const void* logits, void* out, spec_dtype dtype, int B, int R, int V,
+                           const int64_t* in_strides, const int64_t* out_strides, const int32_t* tokens,
+                           const int32_t* parents, int N, const int32_t* history, int H,
+                           const int32_t* prompt_len, const int32_t* history_len, const float* repetition,
+                           const float* presence, const float* frequency, const int32_t* bias_tokens,
+                           const float* bias_values, int nb, const uint32_t* allowed, int32_t* row_status,
+                           void* stream);
+
+/*
+ * Appends rows to the requests' caches, quantised as they are written.
+ *
+ *   k, v [B, T, Hkv, D]     fp32, bf16 or fp16; strides[0..2] of each
+ *   accepted_len [B]        rows 0 .. accepted_len[b] are written, as a verify call returns it: row 0 is the
+ *                           token that the round started from, row i + 1 draft i.  -1 (an abandoned request)
+ *                           writes nothing.  NULL: all T rows (a prompt)
+ *   out_nodes [B, nodes_width]  the accepted path of a tree call: the rows written are 0, then
+ *                           out_nodes[b,i] + 1 for i < accepted_len[b].  NULL: a chain
+ *   lens_out [B]            the lengths after the call (nullable; not lens itself)
+ *
+ * Tokens lens[b], lens[b] + 1, ... take the slots that the page table names.  Of the rows that the call puts
+ * into one page, A is the largest magnitude of a head's keys (values): the scale becomes the smallest
+ * 2^e with A <= 448 2^e; where the page holds earlier tokens of the request (lens[b] is inside it), the larger of that
+ * and the old scale, and the earlier codes are requantised (exact, but for codes that become e4m3 subnormals).  A code
+ * is x / scale rounded to nearest even.  NaN, infinities and magnitudes above 448 2^60 are stored as NaN and
+ * take no part in A.
+ * row_status [B] (nullable): SPEC_ROW_BAD_LENGTH, BAD_PAGE, BAD_NODE; nothing of such a request is written and
+ * lens_out[b] = lens[b].  No two requests may write into one page.
+ */
+spec_status kv_cache_write(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                           spec_dtype dtype, int B, int T, int Hkv, int D, void* k_cache, void* v_cache,
+                           float* k_scale, float* v_scale, int pages, int page_size, const int32_t* page_table,
+                           int table_width, const int32_t* lens, const int32_t* accepted_len,
+                           const int32_t* out_nodes, int nodes_width, int32_t* lens_out, int32_t* row_status,
+                           void* stream);
+
+/*
+ * Reads tokens start[b] .. start[b] + max_len - 1 (start NULL: 0) back as fp32, bf16 or fp16 (rounded once):
+ * k_out, v_out [B, max_len, Hkv, D], dense, 16-byte aligned; tokens past lens[b] read as zero.
+ * row_status [B] (nullable): SPEC_ROW_BAD_LENGTH (all of the request's output is NaN; also for a negative start),
+ * SPEC_ROW_BAD_PAGE (that page's tokens are NaN).
+ */
+spec_status kv_cache_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                          int pages, int page_size, int Hkv, int D, const int32_t* page_table, int table_width,
+                          const int32_t* lens, const int32_t* start, int B, int max_len, void* k_out, void* v_out,
+                          spec_dtype dtype, int32_t* row_status, void* stream);
+
+/* Bytes of workspace of a verify_attention call; 0 for sizes that it refuses. */
+size_t verify_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
+
+/*
+ * The target's attention over one round ("M7.7" 0x07E: the candidate rows of a tree share the prefix and see
+ * their ancestors): T rows per request against the committed tokens in the cache and the round's own rows,
+ * which are not in the cache yet.  T = 1 is a plain decoding step.
+ *
+ *   q    [B, T, Hq, D]      bf16 or fp16; strides[0..2].  Hq a multiple of Hkv: query head h reads key/value head
+ *                           h / (Hq / Hkv).  T <= 256
+ *   k, v [B, T, Hkv, D]     the round's keys and values, same type; both NULL: the cache alone
+ *   parents [B, T-1]        as the tree calls take it (row 0 the frontier, row i + 1 node i); NULL: a chain
+ *   n_rows [B]              live rows of each request (NULL: T); the others give zeros and lse = -inf
+ *   scale                   factor of the scores, > 0
+ *
+ *   s_j = scale * (q . k_j) over tokens 0 .. lens[b]-1 and, in a chain, rows 0 .. t; in a tree row 0, the
+ *   ancestors of row t and row t itself
+ *   out [B, T, Hq, D] = sum_j softmax(s)_j v_j, dense, 16-byte aligned;  lse [B, T, Hq] (nullable, fp32) = log sum_j exp(s_j)
+ * A row that sees nothing gives zeros and -inf.  What a row does not see has no effect on it, whatever it
+ * holds.  Scores, softmax and sums are fp32; out is rounded once.  A row of q that holds a NaN or an infinity gives
+ * NaN.
+ * row_status [B] (nullable): SPEC_ROW_BAD_LENGTH, BAD_PAGE, BAD_PARENT; the request's out and lse are NaN.
+ * workspace: verify_attention_workspace_bytes(...), 16-byte aligned, no initialisation needed.
+ */
+spec_status verify_attention(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                             const void* v, const int64_t* v_strides, spec_dtype dtype, int B, int T, int Hq,
+                             int Hkv, int D, const void* k_cache, const void* v_cache, const float* k_scale,
+                             const float* v_scale, int pages, int page_size, const int32_t* page_table,
+                             int table_width, const int32_t* lens, const int32_t* parents, const int32_t* n_rows,
+                             float scale, void* out, float* lse, int32_t* row_status, void* workspace,
+                             size_t workspace_bytes, void* stream);
 
 /*
  * Measurement aid.  With both events non-NULL (cudaEvent_t created by the caller), every later

@@ -6,10 +6,15 @@ no CPU fallback.
 """
 from .binding import (  # noqa: F401
     EXPORTS,
+    KVCache,
     NOALLOC_SCRATCH_BYTES,
     SpecVerifyError,
     Workspace,
+    kv_cache,
+    kv_cache_read,
+    kv_cache_write,
     load,
+    process_logits,
     set_kernel_events,
     set_tree_sample_cluster,
     set_wait_limit,
@@ -23,5 +28,6 @@ from .binding import (  # noqa: F401
     tree_verify_greedy,
     tree_verify_sample,
     tree_verify_typical,
+    verify_attention,
     workspace_bytes,
 )

@@ -8,21 +8,25 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
 from . import build_ext
 
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_F16 = 0, 1, 2
 ROW_OK, ROW_NONFINITE, ROW_DEGENERATE, ROW_BAD_TOKEN, ROW_TIMEOUT = 0, 1, 2, 3, 4
 ROW_BAD_PARENT, ROW_OVERFLOW, ROW_BAD_UNIFORM, ROW_BAD_QROW = 5, 6, 7, 8
+ROW_BAD_PAGE, ROW_BAD_LENGTH, ROW_BAD_NODE = 9, 10, 11
 
 # every symbol the header declares
 EXPORTS = ("spec_workspace_bytes", "spec_verify", "spec_verify_topk", "spec_verify_topp",
            "spec_verify_masked",
            "tree_verify_greedy", "spec_verify_greedy",
            "tree_verify_sample", "tree_verify_typical", "smc_verify", "spec_verify_noalloc", "spec_set_kernel_events", "spec_set_wait_limit",
-           "spec_set_tree_sample_cluster", "spec_status_string")
+           "spec_set_tree_sample_cluster", "spec_status_string",
+           "process_logits", "kv_cache_write", "kv_cache_read", "verify_attention",
+           "verify_attention_workspace_bytes")
 
 # fixed scratch of spec_verify_noalloc (SPEC_NOALLOC_SCRATCH_BYTES in the header)
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -68,6 +72,17 @@ def load(path: str | None = None):
     lib.smc_verify.restype = I
     lib.spec_verify_noalloc.argtypes = [P, P, I, P, P, I, I, I, F, P, P, P, P, P, P, P]
     lib.spec_verify_noalloc.restype = I
+    lib.process_logits.argtypes = [P, P, I, I, I, I, P, P, P, P, I, P, I, P, P, P, P, P, P, P, I, P, P, P]
+    lib.process_logits.restype = I
+    lib.kv_cache_write.argtypes = [P, P, P, P, I, I, I, I, I, P, P, P, P, I, I, P, I, P, P, P, I, P, P, P]
+    lib.kv_cache_write.restype = I
+    lib.kv_cache_read.argtypes = [P, P, P, P, I, I, I, I, P, I, P, P, I, I, P, P, I, P, P]
+    lib.kv_cache_read.restype = I
+    lib.verify_attention.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, P, P, P, P, I, I, P, I, P, P, P, F,
+                                     P, P, P, P, Z, P]
+    lib.verify_attention.restype = I
+    lib.verify_attention_workspace_bytes.argtypes = [I, I, I, I, I]
+    lib.verify_attention_workspace_bytes.restype = Z
     lib.spec_set_kernel_events.argtypes = [P, P]
     lib.spec_set_kernel_events.restype = None
     lib.spec_set_wait_limit.argtypes = [I]
@@ -425,4 +440,241 @@ def spec_verify_greedy(target, draft_tokens, *, out=None, workspace: Workspace |
                                 _ptr(out["accepted_len"]), _ptr(out["out_tokens"]),
                                 _ptr(out.get("row_status")), _ptr(ws), ws.numel(), _stream(stream))
     _check(rc)
+    return out
+
+
+# ------------------------------------------------------------------ around the verify step
+
+class KVCache(NamedTuple):
+    """The 8-bit paged cache: e4m3 codes [pages, heads, page_size, head_dim] of keys and values, and one fp32
+    scale, a power of two, per page and head.  The calls take any four such tensors in this order."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def kv_cache(pages: int, heads: int, page_size: int, head_dim: int, device="cuda") -> KVCache:
+    """An empty cache (page_size 16, 32, 64 or 128; head_dim 64 or 128)."""
+    shape = (pages, heads, page_size, head_dim)
+    return KVCache(*(torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)),
+                   *(torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def _new(shape, dtype, device, stream):
+    """A new output, safe to be written on `stream` when that is not the current one."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _round_workspace(ws, device, stream, nbytes):
+    """The call's workspace; by default one per device and stream, as calls on two streams may overlap."""
+    if ws is not None:
+        return ws.get(nbytes)
+    key = (str(device), (stream or torch.cuda.current_stream()).cuda_stream)
+    if key not in _default_ws:
+        _default_ws[key] = Workspace(device)
+    buf = _default_ws[key].get(nbytes)
+    if stream is not None:
+        buf.record_stream(stream)
+    return buf
+
+
+def _round_dtype(t: torch.Tensor, what: str, allowed) -> int:
+    code = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}.get(t.dtype)
+    if code not in allowed:
+        raise TypeError(f"{what} has an unsupported dtype {t.dtype}")
+    return code
+
+
+def _strides(t, n):
+    """The strides of the n leading dimensions for the C ABI; the last one must be contiguous.  A dimension of size 1
+    has no stride that matters, and torch may give it any."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("the last dimension must be contiguous")
+    dense = [1] * (t.dim())
+    for i in range(t.dim() - 2, -1, -1):
+        dense[i] = dense[i + 1] * t.shape[i + 1]
+    s = [t.stride(i) if t.shape[i] > 1 else dense[i] for i in range(n)]
+    return (ctypes.c_int64 * n)(*s)
+
+
+def _ints(t, shape, what, optional=False):
+    """A contiguous CUDA int32 tensor of this shape (its pointer)."""
+    if t is None and optional:
+        return None
+    if t is None or t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)}")
+    _need_cuda(t)
+    return _ptr(t)
+
+
+def _floats(t, shape, what):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float32 tensor of shape {tuple(shape)}")
+    _need_cuda(t)
+    return _ptr(t)
+
+
+def _cache_args(cache, page_table, lens, B):
+    k, v, ks, vs = cache
+    if k.dim() != 4 or k.shape != v.shape or not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("the cache's codes must be contiguous [pages, heads, page_size, head_dim]")
+    if k.element_size() != 1 or v.element_size() != 1:
+        raise TypeError("the cache's codes must be e4m3 (one byte each)")
+    pages, heads, page, dim = k.shape
+    _need_cuda(k, v)
+    if page_table is None or page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be [{B}, width]")
+    width = page_table.shape[1]
+    return (pages, heads, page, dim, width,
+            [_ptr(k), _ptr(v), _floats(ks, (pages, heads), "k_scale"), _floats(vs, (pages, heads), "v_scale")],
+            _ints(page_table, (B, width), "page_table"), _ints(lens, (B,), "lens"))
+
+
+def process_logits(logits, *, tokens=None, parents=None, history=None, prompt_len=None, history_len=None,
+                   repetition=None, presence=None, frequency=None, bias_tokens=None, bias_values=None,
+                   allowed=None, out=None, stream=None):
+    """Penalties for repeated tokens, biases and a grammar mask on the rows of a round.
+
+    logits [B, R, V] (bf16 or fp32, CUDA; any request and row stride).  Row r follows the drafted ``tokens``
+    [B, N] on its path: tokens 0..r-1, or, with ``parents`` [B, N], node r-1 and its ancestors (R <= N + 1).
+    ``history`` [B, H]: the tokens before the round, ``history_len`` [B] of them valid, the first
+    ``prompt_len`` [B] the prompt (which counts for the repetition penalty alone).  ``repetition``, ``presence``,
+    ``frequency`` [B] float32; ``bias_tokens`` / ``bias_values`` [B, nb]; ``allowed`` [B, R, ceil(V/32)] 32-bit
+    words as in spec_verify_masked.  ``out`` = dict(logits=..., row_status=...); out["logits"] may be ``logits``.
+    Returns that dict.
+    """
+    lib = load()
+    _need_cuda(logits)
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, R, V]")
+    B, R, V = logits.shape
+    dt = _round_dtype(logits, "logits", (SPEC_F32, SPEC_BF16))
+    N = 0 if tokens is None else tokens.shape[-1]
+    H = 0 if history is None else history.shape[-1]
+    nb = 0 if bias_tokens is None else bias_tokens.shape[-1]
+    if nb and bias_values is None:
+        raise ValueError("bias_tokens need bias_values")
+    if parents is not None and tokens is None:
+        raise ValueError("parents need tokens")
+    if R > N + 1:
+        raise ValueError(f"{R} rows need at least {R - 1} drafted tokens")
+    if out is None:
+        out = dict(logits=_new((B, R, V), logits.dtype, logits.device, stream),
+                   row_status=_new(B, torch.int32, logits.device, stream))
+    y = out["logits"]
+    if y.shape != logits.shape or y.dtype != logits.dtype:
+        raise ValueError("out['logits'] must have the logits' shape and dtype")
+    W = (V + 31) // 32
+    if allowed is not None:
+        _need_cuda(allowed)
+        if tuple(allowed.shape) != (B, R, W) or allowed.element_size() != 4 or not allowed.is_contiguous():
+            raise ValueError(f"allowed must be a contiguous 32-bit [B, R, {W}] tensor")
+    _check(lib.process_logits(
+        _ptr(logits), _ptr(y), dt, B, R, V, _strides(logits, 2), _strides(y, 2),
+        _ints(tokens, (B, N), "tokens", True) if N else None, _ints(parents, (B, N), "parents", True) if N else None, N,
+        _ints(history, (B, H), "history", True) if H else None, H, _ints(prompt_len, (B,), "prompt_len", True),
+        _ints(history_len, (B,), "history_len", True), _floats(repetition, (B,), "repetition"),
+        _floats(presence, (B,), "presence"), _floats(frequency, (B,), "frequency"),
+        _ints(bias_tokens, (B, nb), "bias_tokens", True) if nb else None,
+        _floats(bias_values, (B, nb), "bias_values") if nb else None, nb, _ptr(allowed),
+        _ptr(out.get("row_status")), _stream(stream)))
+    return out
+
+
+def kv_cache_write(k, v, cache, page_table, lens, *, accepted_len=None, out_nodes=None, out=None, stream=None):
+    """Appends rows to the requests' 8-bit caches, one scale per page and head.
+
+    k, v [B, T, Hkv, D] (fp32, bf16 or fp16; any strides but the last), ``cache`` a KVCache (written in place),
+    page_table [B, width] and lens [B] int32.  ``accepted_len`` [B] and ``out_nodes`` [B, >= T-1], as a verify call
+    returns them, choose the rows: 0 .. accepted_len, or row 0 and the accepted path's nodes; without them
+    all T rows are written.  Returns dict(lens, row_status): the lengths after the write.
+    """
+    lib = load()
+    _need_cuda(k, v)
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must be [B, T, heads, head_dim] of one dtype")
+    B, T, heads, dim = k.shape
+    dt = _round_dtype(k, "k", (SPEC_F32, SPEC_BF16, SPEC_F16))
+    pages, h, page, d, width, ptrs, table, ln = _cache_args(cache, page_table, lens, B)
+    if (h, d) != (heads, dim):
+        raise ValueError(f"the cache holds {h} heads of {d}, the rows {heads} of {dim}")
+    if out_nodes is not None and accepted_len is None:
+        raise ValueError("out_nodes need accepted_len")
+    nw = 0 if out_nodes is None else out_nodes.shape[-1]
+    if out is None:
+        out = dict(lens=_new(B, torch.int32, k.device, stream),
+                   row_status=_new(B, torch.int32, k.device, stream))
+    _check(lib.kv_cache_write(
+        _ptr(k), _strides(k, 3), _ptr(v), _strides(v, 3), dt, B, T, heads, dim, *ptrs, pages, page, table, width, ln,
+        _ints(accepted_len, (B,), "accepted_len", True),
+        _ints(out_nodes, (B, nw), "out_nodes", True) if nw else None, nw,
+        _ptr(out.get("lens")), _ptr(out.get("row_status")), _stream(stream)))
+    return out
+
+
+def kv_cache_read(cache, page_table, lens, *, max_len: int, start=None, dtype=torch.bfloat16, out=None, stream=None):
+    """Reads tokens start .. start + max_len - 1 of every request back as ``dtype``: dict(k, v [B, max_len, heads,
+    head_dim], row_status).  Tokens past a request's length read as zero."""
+    lib = load()
+    B = lens.shape[0]
+    pages, heads, page, dim, width, ptrs, table, ln = _cache_args(cache, page_table, lens, B)
+    dev = cache[0].device
+    if out is None:
+        out = {n: _new((B, max_len, heads, dim), dtype, dev, stream) for n in ("k", "v")}
+        out["row_status"] = _new(B, torch.int32, dev, stream)
+    for n in ("k", "v"):
+        if tuple(out[n].shape) != (B, max_len, heads, dim) or not out[n].is_contiguous() or out[n].dtype != out["k"].dtype:
+            raise ValueError(f"out[{n!r}] must be contiguous [B, max_len, heads, head_dim]")
+    dt = _round_dtype(out["k"], "out", (SPEC_F32, SPEC_BF16, SPEC_F16))
+    _check(lib.kv_cache_read(*ptrs, pages, page, heads, dim, table, width, ln, _ints(start, (B,), "start", True), B,
+                             max_len, _ptr(out["k"]), _ptr(out["v"]), dt, _ptr(out.get("row_status")), _stream(stream)))
+    return out
+
+
+def verify_attention(q, cache, page_table, lens, *, k=None, v=None, parents=None, n_rows=None,
+                     scale: float | None = None, lse: bool = False, out=None, workspace: Workspace | None = None,
+                     stream=None):
+    """Attention of a round's rows over the 8-bit cache and the round's own keys and values.
+
+    q [B, T, Hq, D] and k, v [B, T, Hkv, D] (bf16 or fp16; any strides but the last), T <= 256, Hq a multiple of
+    Hkv; without k and v the rows see the cache alone.  Every row sees the committed tokens; of the round's rows, row t sees
+    0..t, or with ``parents`` [B, T-1] (as the tree calls take it) row 0, its ancestors and itself.  ``n_rows`` [B]:
+    live rows of each request.  ``scale`` defaults to D ** -0.5.  Returns dict(out [B, T, Hq, D], row_status and,
+    with ``lse``, lse [B, T, Hq] in fp32).
+    """
+    lib = load()
+    _need_cuda(q, k, v)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, Hq, D]")
+    B, T, hq, dim = q.shape
+    dt = _round_dtype(q, "q", (SPEC_BF16, SPEC_F16))
+    pages, hkv, page, d, width, ptrs, table, ln = _cache_args(cache, page_table, lens, B)
+    if d != dim or hq % hkv:
+        raise ValueError(f"q has {hq} heads of {dim}, the cache {hkv} of {d}")
+    if (k is None) != (v is None):
+        raise ValueError("k and v come together")
+    if k is not None and not (k.shape == v.shape == (B, T, hkv, dim) and k.dtype == v.dtype == q.dtype):
+        raise ValueError("k and v must be [B, T, Hkv, D] of q's dtype")
+    if out is None:
+        out = dict(out=_new((B, T, hq, dim), q.dtype, q.device, stream),
+                   row_status=_new(B, torch.int32, q.device, stream))
+        if lse:
+            out["lse"] = _new((B, T, hq), torch.float32, q.device, stream)
+    if out["out"].shape != q.shape or out["out"].dtype != q.dtype or not out["out"].is_contiguous():
+        raise ValueError("out['out'] must be contiguous, with q's shape and dtype")
+    nbytes = int(lib.verify_attention_workspace_bytes(B, T, hq, hkv, dim))
+    ws = _round_workspace(workspace, q.device, stream, nbytes)
+    s = float(dim) ** -0.5 if scale is None else float(scale)
+    _check(lib.verify_attention(
+        _ptr(q), _strides(q, 3), _ptr(k), None if k is None else _strides(k, 3), _ptr(v),
+        None if v is None else _strides(v, 3), dt, B, T, hq, hkv, dim, *ptrs, pages, page, table, width, ln,
+        _ints(parents, (B, T - 1), "parents", True) if T > 1 else None, _ints(n_rows, (B,), "n_rows", True), s,
+        _ptr(out["out"]), _floats(out.get("lse"), (B, T, hq), "lse"), _ptr(out.get("row_status")), _ptr(ws),
+        ws.numel(), _stream(stream)))
     return out

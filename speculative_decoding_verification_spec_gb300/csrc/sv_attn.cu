@@ -1,0 +1,749 @@
+// sv_attn.cu -- verify_attention for few rows: attention of a round's rows over the 8-bit paged cache
+// and over the round's own rows.
+//
+// For row t and query head h, with g the key/value head that h shares and s_j = scale * (q . k_j),
+//   o = sum_j p_j v_j,  p_j = exp(s_j - lse),  lse = log sum_j exp(s_j)
+// over the committed tokens and the rows of the round that t sees (a chain: 0 .. t; a tree: row 0, the
+// ancestors' rows and itself).  The rows of the round are not quantised.
+//
+// Arithmetic.  An e4m3 code is exact as a half, so products are half x half, summed in fp32.  A row of q is scaled by a
+// power of two so that its largest element lies in [2^14, 2^15): a bf16 or half element is then exact as a
+// half unless it is 2^-28 of the largest or less, and off by at most 2^-39 of it.  With u_j = log2(e) s_j + e_j, 2^(e_j) the scale of
+// v_j's page (a power of two), the kernel keeps a reference m per row, within 2^8 of the running maximum of
+// u, and sums p'_j = 2^(u_j - m):
+//   o = (sum_j p'_j c_j) / (sum_j p'_j 2^(-e_j)),   c_j the codes of v_j,
+// so pages with different scales need no second scaling of the sums.  p' <= 2^15 is rounded to a half for the
+// product (half a step, 2^-11, under the output's own rounding; what lies under 2^-14 is off by 2^-25 absolute, 2^-32 of
+// the row's largest term); the denominator takes it in fp32.
+//
+// Schedule.  The work is cut into tiles of 64 tokens; every CTA takes an equal run of the tiles of all (request,
+// head, row tile) groups in a row, so ragged lengths balance and one long request spreads over the GPU.  A
+// group that one CTA covers is written out directly; otherwise its parts (m, l, o) go to the workspace and
+// attn_merge_kernel joins them in a fixed order.  Each of a CTA's four warps streams its own 16 tokens of a
+// tile through a private ring of cp.async stages, so the loop has no barrier; the warps join at the end.
+#include "sv_round.cuh"
+
+namespace sv {
+
+namespace {
+
+constexpr int AW = 4;           // warps per CTA
+constexpr int ANT = AW * 32;
+constexpr int SLICE = 16;       // tokens of a warp per tile
+constexpr int TILE = AW * SLICE;
+constexpr int ASTAGES = 4;
+constexpr int MR_MAX = 32;      // rows of the largest row tile
+constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
+
+// a part of a group in the workspace: o [MR_MAX][D], then m, l [MR_MAX], then the status
+__host__ __device__ constexpr size_t part_floats(int D) { return (size_t)MR_MAX * D + 2 * MR_MAX + 32; }
+
+__device__ __forceinline__ uint32_t swz_off(int D, int row, int chunk)
+{
+    // byte offset of 16-byte chunk `chunk` of token `row`: spread so that the 8 (row, chunk) pairs that one
+    // phase of a fragment load touches fall into different banks
+    if (D == 128) return row * 128 + ((chunk ^ (row & 7)) << 4);
+    const int line = row >> 1;
+    return line * 128 + (((((row & 1) << 2) | chunk) ^ (((line & 1) << 2) | (line & 2))) << 4);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int DT>
+__device__ __forceinline__ float load_elem(const void* p, int64_t i)
+{
+    if constexpr (DT == DT_BF16)
+        return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + i) << 16);
+    else
+        return __half2float(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(p) + i)));
+}
+
+// the exponent x of a finite a >= 0, a = f * 2^x with f in [1, 2), -127 below the normal range
+__device__ __forceinline__ int exponent_of(float a) { return (int)(__float_as_uint(a) >> 23) - 127; }
+
+// ---------------------------------------------------------------- schedule
+
+struct ReqInfo {
+    int len;     // committed tokens (0 when the length is bad)
+    int rows;    // live rows
+    int ncache;  // tiles of the cache
+    int n;       // tiles of a group, at least one: a group without tokens still writes its outputs
+    int status;
+};
+
+__device__ __forceinline__ ReqInfo req_info(const AttnParams& P, int b)
+{
+    ReqInfo q;
+    q.len = __ldg(P.lens + b);
+    q.rows = P.n_rows ? min(max(__ldg(P.n_rows + b), 0), P.T) : P.T;
+    q.status = ROW_OK;
+    if (q.len < 0 || (long long)q.len > (long long)P.table_width * P.page) {
+        q.len = 0;
+        q.status = ROW_BAD_LENGTH;
+    }
+    q.ncache = (q.len + TILE - 1) / TILE;
+    const int fresh = P.kn ? (q.rows + TILE - 1) / TILE : 0;
+    q.n = max(1, q.ncache + fresh);
+    return q;
+}
+
+// total units (tiles of all groups), and the request that unit `u0(total)` falls into; every thread of the CTA calls
+// it, warp 0 works
+struct Place {
+    long long total, pre;  // pre: units of the requests before b
+    int b;
+};
+
+__device__ Place find_place(const AttnParams& P, int cta, int ctas, Place* sh)
+{
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        const long long per = (long long)P.Hkv * P.RT;
+        long long total = 0;
+        for (int b0 = 0; b0 < P.B; b0 += 32) {
+            long long v = b0 + lane < P.B ? req_info(P, b0 + lane).n * per : 0;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            total += v;
+        }
+        const long long u0 = total * cta / ctas;
+        long long pre = 0;
+        int found = P.B;
+        for (int b0 = 0; b0 < P.B; b0 += 32) {
+            long long v = b0 + lane < P.B ? req_info(P, b0 + lane).n * per : 0, s = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long x = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += x;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, u0 < pre + s);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                pre += __shfl_sync(0xffffffffu, s - v, l);
+                found = b0 + l;
+                break;
+            }
+            pre += __shfl_sync(0xffffffffu, s, 31);
+        }
+        if (lane == 0) {
+            sh->total = total;
+            sh->pre = pre;
+            sh->b = found;
+        }
+    }
+    __syncthreads();
+    return *sh;
+}
+
+// ---------------------------------------------------------------- outputs of a row
+
+template <int DT>
+__device__ __forceinline__ void store_out4(const AttnParams& P, int b, int t, int hq, int d, float4 o)
+{
+    uint32_t lo, hi;
+    if constexpr (DT == DT_BF16) {
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(o.y), "f"(o.x));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(o.w), "f"(o.z));
+    } else {
+        lo = pack_half2(o.x, o.y);
+        hi = pack_half2(o.z, o.w);
+    }
+    uint16_t* p = reinterpret_cast<uint16_t*>(P.out) + (((size_t)b * P.T + t) * P.Hq + hq) * P.D + d;
+    *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+}
+
+// o = O / l and lse of row r of (b, h); rows past the live ones, and rows that see nothing, give 0 and -inf
+template <int DT>
+__device__ __forceinline__ void finish_row4(const AttnParams& P, int b, int h, int r, int rows, int status, int d,
+                                            float4 O, float m, float l)
+{
+    const int t = r / P.G, hq = h * P.G + r % P.G;
+    const bool live = t < rows && l != 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float lse = NEG_INF;
+    if (live) {
+        o = make_float4(O.x / l, O.y / l, O.z / l, O.w / l);
+        lse = (m + log2f(l)) * LN2;
+    }
+    if (status != ROW_OK) {
+        lse = __int_as_float(0x7fc00000);
+        o = make_float4(lse, lse, lse, lse);
+    }
+    store_out4<DT>(P, b, t, hq, d, o);
+    if (d == 0 && P.lse) P.lse[((size_t)b * P.T + t) * P.Hq + hq] = lse;
+}
+
+// ---------------------------------------------------------------- the streaming kernel
+
+template <int D, int MT>
+struct RowState {
+    float o[MT][D / 8][4];
+    float m[MT][2], l[MT][2];
+};
+
+// One slice of 16 tokens against the CTA's rows.  kf(nt, c, w): the four halves-pairs ... see the two callers.
+// u_scale(nt, j), u_add(nt, j), l_scale(nt, j): per token column (2t + j of n-tile nt); see(mt, hi, nt, j): whether row g
+// (+ 8 hi) of m-tile mt sees the column.
+template <int D, int MT, class KFrag, class VFrag, class Scale, class Add, class LScale, class See>
+__device__ __forceinline__ void slice_step(RowState<D, MT>& S, const uint32_t (&qf)[MT][D / 16][4], const float (&F)[MT][2],
+                                           KFrag kfrag, VFrag vfrag, Scale u_scale, Add u_add, LScale l_scale, See see)
+{
+    float s[MT][2][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+        for (int cc = 0; cc < D / 64; ++cc) {
+            uint32_t kb[4][2];
+            kfrag(nt, cc, kb);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) mma_f16(s[mt][nt], qf[mt][cc * 4 + k], kb[k][0], kb[k][1]);
+        }
+    }
+    uint32_t pf[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int hi = 0; hi < 2; ++hi) {
+            float u[2][2], top = NEG_INF;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float x = fmaf(s[mt][nt][2 * hi + j], F[mt][hi] * u_scale(nt, j), u_add(nt, j));
+                    u[nt][j] = see(mt, hi, nt, j) ? x : NEG_INF;
+                    top = fmaxf(top, u[nt][j]);
+                }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            float m = S.m[mt][hi];
+            // the reference moves only when the maximum has left its 2^8 window, so the sums are rarely rescaled
+            const bool move = top > m + 15.0f;
+            if (__any_sync(0xffffffffu, move)) {
+                const float now = move ? top - 7.0f : m;
+                const float f = move ? (m == NEG_INF ? 0.0f : ex2(m - now)) : 1.0f;
+                S.m[mt][hi] = m = now;
+                S.l[mt][hi] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    S.o[mt][i][2 * hi] *= f;
+                    S.o[mt][i][2 * hi + 1] *= f;
+                }
+            }
+            const float ref = m == NEG_INF ? 0.0f : m;
+            float p[2][2];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    p[nt][j] = ex2(u[nt][j] - ref);
+                    S.l[mt][hi] = fmaf(p[nt][j], l_scale(nt, j), S.l[mt][hi]);
+                }
+            pf[mt][hi] = pack_half2(p[0][0], p[0][1]);
+            pf[mt][2 + hi] = pack_half2(p[1][0], p[1][1]);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < D / 32; ++q) {  // four n-tiles (four channels of the thread's run) at a time
+        uint32_t vb[4][2];
+        vfrag(q, vb);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) mma_f16(S.o[mt][4 * q + i], pf[mt], vb[i][0], vb[i][1]);
+    }
+}
+
+// token (row of the slice's n-tile) that column n of an n-tile stands for; with it, the rows that one
+// phase of a fragment load reads lie in different banks for keys and values alike
+__device__ __forceinline__ int col_token(int n) { return n & 1 ? (n - 1) ^ 5 : n; }
+
+template <int DT, int D, int MT>
+__global__ void __launch_bounds__(ANT, MT == 1 ? 3 : 2) attn_rows_kernel(AttnParams P)
+{
+    constexpr int MR = MT * 16;
+    constexpr int KB = SLICE * D;        // bytes of a slice's keys (or values)
+    constexpr int STAGE = 2 * KB;
+    extern __shared__ __align__(128) uint8_t ring[];  // [AW][ASTAGES][STAGE]; at a group's end [AW][MR][D] floats
+    __shared__ float2 scales[AW][ASTAGES];            // of the stage's page: keys, values
+    __shared__ __half sq[MR][D + 8];
+    __shared__ float sf[MR], wm[AW][MR], wl[AW][MR];
+    __shared__ uint64_t smask[MR];
+    __shared__ float fks[AW][SLICE], fve[AW][SLICE];
+    __shared__ int sstatus;
+    __shared__ Place place;
+
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const Place at = find_place(P, blockIdx.x, gridDim.x, &place);
+    long long u = at.total * blockIdx.x / gridDim.x;
+    const long long u1 = at.total * (blockIdx.x + 1) / gridDim.x;
+    if (u >= u1) return;
+    int b = at.b;
+    long long pre = at.pre;
+    ReqInfo rq = req_info(P, b);
+    uint8_t* my = ring + w * ASTAGES * STAGE;
+    const uint32_t my_a = smem_addr(my), sc_a = smem_addr(&scales[w][0]);
+    int ltok[2];  // this lane's key token of each n-tile
+    ltok[0] = col_token(g);
+    ltok[1] = 8 + col_token(g);
+    const bool first_cont = ((u - pre) % rq.n) != 0;
+    bool first = true;
+
+    while (u < u1) {
+        const long long rem = u - pre;
+        const int grp = (int)(rem / rq.n), tile0 = (int)(rem % rq.n);
+        const int h = grp / P.RT, rt = grp % P.RT;
+        const int tile1 = (int)min((long long)rq.n, tile0 + (u1 - u));
+        const bool whole = tile0 == 0 && tile1 == rq.n;
+
+        // ---- the rows of q
+        __syncthreads();  // the previous group's use of the shared arrays is over
+        if (tid == 0) sstatus = rq.status;
+        for (int i = w; i < MR; i += AW) {
+            const int r = rt * MR + i, t = r / P.G;
+            float x[D / 32], amax = 0.0f;
+            const bool live = r < P.R && t < rq.rows;
+            const int64_t base = live ? (int64_t)b * P.qb + (int64_t)t * P.qt + (int64_t)(h * P.G + r % P.G) * P.qh : 0;
+            bool fin = true;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                x[k] = live ? load_elem<DT>(P.q, base + lane + 32 * k) : 0.0f;
+                fin = fin && fabsf(x[k]) < __int_as_float(0x7f800000);
+                amax = fmaxf(amax, fabsf(x[k]));
+            }
+            fin = __all_sync(0xffffffffu, fin);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const int e = fin ? min(max(14 - exponent_of(amax), -113), 126) : 0;
+            const float mul = exp2_int(e);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) sq[i][lane + 32 * k] = __float2half_rn(x[k] * mul);
+            // a row of q with a NaN or an infinity has no scores
+            if (lane == 0) sf[i] = fin ? P.scale * LOG2E * exp2_int(-e) : __int_as_float(0x7fc00000);
+        }
+        __syncthreads();
+        uint32_t qf[MT][D / 16][4];
+        float F[MT][2];
+        RowState<D, MT> S;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                F[mt][hi] = sf[mt * 16 + 8 * hi + g];
+                S.m[mt][hi] = NEG_INF;
+                S.l[mt][hi] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) S.o[mt][i][k] = 0.0f;
+            // product step cc * 4 + k takes channels 16 (t4 + 4 cc) + 4 k .. + 3 of this lane's rows
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+                for (int hi = 0; hi < 2; ++hi) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(&sq[mt * 16 + 8 * hi + g][16 * (t4 + 4 * (c >> 2)) + 4 * (c & 3)]);
+                    qf[mt][c][hi] = v.x;
+                    qf[mt][c][2 + hi] = v.y;
+                }
+        }
+
+        // ---- the cache
+        const int c0 = min(tile0, rq.ncache), c1 = min(tile1, rq.ncache), nc = c1 - c0;
+        const int32_t* table = P.page_table + (size_t)b * P.table_width;
+        int page_reg = 0;  // lane k holds the page of the slice c0 + 32 i + k
+        auto fetch = [&](int i) {
+            if (i < nc) {
+                const int base = (c0 + i) * TILE + w * SLICE;
+                if ((i & 31) == 0) {
+                    const long long tk = (long long)(c0 + i + lane) * TILE + w * SLICE;
+                    page_reg = tk < rq.len ? __ldg(table + (tk >> P.page_shift)) : 0;
+                    if (tk < rq.len && c0 + i + lane < c1 && (unsigned)page_reg >= (unsigned)P.pages) sstatus = ROW_BAD_PAGE;
+                }
+                const int page = __shfl_sync(0xffffffffu, page_reg, i & 31);
+                if (base < rq.len) {
+                    const bool good = (unsigned)page < (unsigned)P.pages;
+                    const size_t blk = good ? (size_t)page * P.Hkv + h : 0;
+                    const int valid = good ? rq.len - base : 0;
+                    const size_t off = (blk * P.page + (good ? (base & (P.page - 1)) : 0)) * D;
+                    const uint32_t st = my_a + (i % ASTAGES) * STAGE;
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        const int q = lane + 32 * k, row = q / (D / 16), ch = q % (D / 16);
+                        const int bytes = row < valid ? 16 : 0;  // tokens past the length are filled with zeros
+                        const uint32_t o = swz_off(D, row, ch);
+                        const size_t from = bytes ? off + (size_t)row * D + ch * 16 : 0;
+                        cp_async16(st + o, P.kc + from, bytes);
+                        cp_async16(st + KB + o, P.vc + from, bytes);
+                    }
+                    if (lane < 2) cp_async4(sc_a + (i % ASTAGES) * 8 + lane * 4, (lane ? P.vs : P.ks) + blk, good ? 4 : 0);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int i = 0; i < ASTAGES - 1; ++i) fetch(i);
+        for (int i = 0; i < nc; ++i) {
+            asm volatile("cp.async.wait_group %0;" :: "n"(ASTAGES - 2) : "memory");
+            __syncwarp();  // every lane's copies of stage i have landed, and stage i - 1 is read to the end
+            fetch(i + ASTAGES - 1);
+            const int base = (c0 + i) * TILE + w * SLICE;
+            if (base >= rq.len) continue;
+            const uint8_t* st = my + (i % ASTAGES) * STAGE;
+            const float2 sc = scales[w][i % ASTAGES];
+            const float ve = (float)exponent_of(sc.y);
+            const float inv = exp2_int(min(max(-exponent_of(sc.y), -126), 127));
+            const int left = rq.len - base;
+            auto kfrag = [&](int nt, int cc, uint32_t (&kb)[4][2]) {
+                const uint4 x = *reinterpret_cast<const uint4*>(st + swz_off(D, ltok[nt], t4 + 4 * cc));
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    kb[k][0] = e4m3x2_to_half2((uint16_t)xs[k]);
+                    kb[k][1] = e4m3x2_to_half2((uint16_t)(xs[k] >> 16));
+                }
+            };
+            // channels (D / 8) g .. of the four tokens that this lane's columns 2 t4, 2 t4 + 1 of both n-tiles name
+            constexpr int VW = D / 32;  // 32-bit words per token
+            uint32_t vw[4][VW];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int row = (k >> 1) * 8 + (k & 1 ? (2 * t4) ^ 5 : 2 * t4);
+                if constexpr (D == 128) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(st + KB + swz_off(D, row, g));
+                    vw[k][0] = x.x; vw[k][1] = x.y; vw[k][2] = x.z; vw[k][3] = x.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2*>(st + KB + swz_off(D, row, g >> 1) + (g & 1) * 8);
+                    vw[k][0] = x.x; vw[k][1] = x.y;
+                }
+            }
+            auto vfrag = [&](int q, uint32_t (&vb)[4][2]) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t a = vw[2 * half][q], c = vw[2 * half + 1][q];
+                    const uint32_t lo = __byte_perm(a, c, 0x5140), hi = __byte_perm(a, c, 0x7362);
+                    vb[0][half] = e4m3x2_to_half2((uint16_t)lo);
+                    vb[1][half] = e4m3x2_to_half2((uint16_t)(lo >> 16));
+                    vb[2][half] = e4m3x2_to_half2((uint16_t)hi);
+                    vb[3][half] = e4m3x2_to_half2((uint16_t)(hi >> 16));
+                }
+            };
+            auto uscale = [&](int, int) { return sc.x; };
+            auto uadd = [&](int, int) { return ve; };
+            auto lscale = [&](int, int) { return inv; };
+            if (left >= SLICE)
+                slice_step<D, MT>(S, qf, F, kfrag, vfrag, uscale, uadd, lscale, [](int, int, int, int) { return true; });
+            else
+                slice_step<D, MT>(S, qf, F, kfrag, vfrag, uscale, uadd, lscale, [&](int, int, int nt, int j) {
+                    return nt * 8 + (j ? (2 * t4) ^ 5 : 2 * t4) < left;
+                });
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+
+        // ---- the round's own rows
+        for (int tile = max(tile0, rq.ncache); P.kn && tile < tile1; ++tile) {
+            const int j0 = (tile - rq.ncache) * TILE;
+            __syncthreads();
+            for (int i = tid; i < MR; i += ANT) {
+                // bit j - j0: row t sees row j
+                const int t = (rt * MR + i) / P.G;
+                uint64_t bits = 0;
+                if (t < rq.rows) {
+                    if (!P.parents) {
+                        const int n = t + 1 - j0;
+                        bits = n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
+                    } else {
+                        int cur = t;
+                        for (;;) {
+                            if ((unsigned)(cur - j0) < 64u) bits |= 1ull << (cur - j0);
+                            if (cur == 0) break;
+                            const int p = __ldg(P.parents + (size_t)b * (P.T - 1) + cur - 1);
+                            if (p < -1 || p >= cur - 1) break;  // reported below; the walk always ends
+                            cur = p + 1;
+                        }
+                    }
+                }
+                smask[i] = bits;
+            }
+            if (P.parents)
+                for (int i = tid; i < rq.rows - 1; i += ANT) {
+                    const int p = __ldg(P.parents + (size_t)b * (P.T - 1) + i);
+                    if (p < -1 || p >= i) sstatus = ROW_BAD_PARENT;
+                }
+            __syncthreads();
+            const int jw = j0 + w * SLICE;
+            if (jw >= rq.rows) continue;
+            // 16 rows as halves, each scaled by a power of two as q is: keys [16][D], then values
+            __half* fk = reinterpret_cast<__half*>(my);
+            __half* fv = fk + SLICE * D;
+            unsigned bad = 0;  // rows of the slice whose values hold a NaN or an infinity
+            for (int i = 0; i < SLICE; ++i) {
+                const int j = jw + i;
+                const bool live = j < rq.rows;
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    const void* src = which ? P.vn : P.kn;
+                    const int64_t base = !live ? 0 : which ? b * P.vb + j * P.vt + h * P.vh : b * P.kb + j * P.kt + h * P.kh;
+                    float x[D / 32], amax = 0.0f;
+                    bool fin = true;
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        x[k] = live ? load_elem<DT>(src, base + lane + 32 * k) : 0.0f;
+                        if (fabsf(x[k]) < __int_as_float(0x7f800000)) amax = fmaxf(amax, fabsf(x[k]));
+                        else fin = false;
+                    }
+                    fin = __all_sync(0xffffffffu, fin);
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    const int e = min(max(exponent_of(amax), CACHE_E_MIN), 126) - 14;
+                    const float mul = exp2_int(-e);
+                    if (which && !fin) bad |= 1u << i;
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        // a value that only some rows see must not meet the others' zero weights as NaN
+                        const bool drop = which && !(fabsf(x[k]) < __int_as_float(0x7f800000));
+                        (which ? fv : fk)[i * D + lane + 32 * k] = __float2half_rn(drop ? 0.0f : x[k] * mul);
+                    }
+                    if (lane == 0) {
+                        if (which) fve[w][i] = (float)e;
+                        else fks[w][i] = exp2_int(e);
+                    }
+                }
+            }
+            __syncwarp();
+            auto ctok = [&](int nt, int j) { return nt * 8 + (j ? (2 * t4) ^ 5 : 2 * t4); };
+            auto kfrag = [&](int nt, int cc, uint32_t (&kb)[4][2]) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(&fk[ltok[nt] * D + 16 * (t4 + 4 * cc) + 4 * k]);
+                    kb[k][0] = v.x;
+                    kb[k][1] = v.y;
+                }
+            };
+            auto vfrag = [&](int q, uint32_t (&vb)[4][2]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const int ch = (D / 8) * g + 4 * q + i;
+                        vb[i][nt] = (uint32_t)__half_as_ushort(fv[ctok(nt, 0) * D + ch]) |
+                                    (uint32_t)__half_as_ushort(fv[ctok(nt, 1) * D + ch]) << 16;
+                    }
+            };
+            auto vis = [&](int mt, int hi, int nt, int j) {
+                return (smask[mt * 16 + 8 * hi + g] >> (w * SLICE + ctok(nt, j)) & 1ull) != 0;
+            };
+            slice_step<D, MT>(S, qf, F, kfrag, vfrag, [&](int nt, int j) { return fks[w][ctok(nt, j)]; },
+                              [&](int nt, int j) { return fve[w][ctok(nt, j)]; },
+                              [&](int nt, int j) { return exp2_int(-(int)fve[w][ctok(nt, j)]); }, vis);
+            // values that are not finite reach the rows that see them
+            for (unsigned left = bad; left; left &= left - 1) {
+                const int i = __ffs(left) - 1, j = jw + i;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int hi = 0; hi < 2; ++hi) {
+                        if (!(smask[mt * 16 + 8 * hi + g] >> (w * SLICE + i) & 1ull)) continue;
+#pragma unroll
+                        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int ch = (D / 8) * (2 * t4 + k) + n;
+                                const float x = load_elem<DT>(P.vn, b * P.vb + j * P.vt + h * P.vh + ch);
+                                if (!(fabsf(x) < __int_as_float(0x7f800000))) S.o[mt][n][2 * hi + k] += x;
+                            }
+                    }
+            }
+            __syncwarp();
+        }
+
+        // ---- join the warps: o to shared memory, m and l beside it
+        __syncwarp();
+        float* so = reinterpret_cast<float*>(my);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                float l = S.l[mt][hi];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                const int row = mt * 16 + 8 * hi + g;
+                if (t4 == 0) {
+                    wm[w][row] = S.m[mt][hi];
+                    wl[w][row] = l;
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int n = 0; n < D / 8; n += 4)
+                        *reinterpret_cast<float4*>(&so[row * D + (D / 8) * (2 * t4 + k) + n]) =
+                            make_float4(S.o[mt][n][2 * hi + k], S.o[mt][n + 1][2 * hi + k], S.o[mt][n + 2][2 * hi + k], S.o[mt][n + 3][2 * hi + k]);
+            }
+        __syncthreads();
+        const int status = sstatus;
+        float* part = P.parts + ((size_t)blockIdx.x * 2 + (first && first_cont ? 0 : 1)) * part_floats(D);
+        for (int i = tid; i < MR * (D / 4); i += ANT) {
+            const int row = i / (D / 4), d = i % (D / 4) * 4;
+            const int r = rt * MR + row;
+            if (r >= P.R) break;
+            float m = NEG_INF;
+#pragma unroll
+            for (int k = 0; k < AW; ++k) m = fmaxf(m, wm[k][row]);
+            float l = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < AW; ++k) {
+                // a warp that saw no token has m = -inf and sums of zero (or NaN, which stays)
+                const float f = wm[k][row] == NEG_INF ? 1.0f : ex2(wm[k][row] - m);
+                const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(ring + k * ASTAGES * STAGE) + row * D + d);
+                l = fmaf(wl[k][row], f, l);
+                o.x = fmaf(x.x, f, o.x);
+                o.y = fmaf(x.y, f, o.y);
+                o.z = fmaf(x.z, f, o.z);
+                o.w = fmaf(x.w, f, o.w);
+            }
+            if (whole) {
+                finish_row4<DT>(P, b, h, r, rq.rows, status, d, o, m, l);
+            } else {
+                *reinterpret_cast<float4*>(&part[row * D + d]) = o;
+                if (d == 0) {
+                    part[MR_MAX * D + row] = m;
+                    part[MR_MAX * D + MR_MAX + row] = l;
+                }
+            }
+        }
+        if (tid == 0) {
+            if (!whole) part[MR_MAX * D + 2 * MR_MAX] = __int_as_float(status);
+            else if (P.row_status && h == 0 && rt == 0) P.row_status[b] = status;
+        }
+        first = false;
+        u += tile1 - tile0;
+        while (u < u1 && u >= pre + (long long)rq.n * P.Hkv * P.RT) {
+            pre += (long long)rq.n * P.Hkv * P.RT;
+            rq = req_info(P, ++b);
+        }
+    }
+}
+
+// Joins the parts of the group that starts in streaming CTA blockIdx.x and ends in a later one.
+template <int DT, int D>
+__global__ void __launch_bounds__(256) attn_merge_kernel(AttnParams P, int MR)
+{
+    __shared__ Place place;
+    const int c = blockIdx.x, ctas = gridDim.x;
+    const Place at = find_place(P, c, ctas, &place);
+    const long long u0 = at.total * c / ctas, u1 = at.total * (c + 1) / ctas;
+    if (u0 >= u1) return;
+    // the group of the last unit
+    int b = at.b;
+    long long pre = at.pre;
+    ReqInfo rq = req_info(P, b);
+    while (u1 - 1 >= pre + (long long)rq.n * P.Hkv * P.RT) {
+        pre += (long long)rq.n * P.Hkv * P.RT;
+        rq = req_info(P, ++b);
+    }
+    const int grp = (int)((u1 - 1 - pre) / rq.n);
+    const long long gs = pre + (long long)grp * rq.n, ge = gs + rq.n;
+    if (gs < u0 || ge <= u1) return;
+    const int h = grp / P.RT, rt = grp % P.RT;
+    int last = c;  // the CTA that holds unit ge - 1
+    while (at.total * (last + 1) / ctas < ge) ++last;
+    const size_t pf = part_floats(D);
+    for (int i = threadIdx.x; i < MR * (D / 4); i += 256) {
+        const int row = i / (D / 4), d = i % (D / 4) * 4;
+        const int r = rt * MR + row;
+        if (r >= P.R) break;
+        float m = NEG_INF, l = 0.0f;
+        int status = ROW_OK;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k = c; k <= last; ++k) {
+            const float* part = P.parts + ((size_t)k * 2 + (k == c ? 1 : 0)) * pf;
+            if (at.total * k / ctas == at.total * (k + 1) / ctas) continue;
+            const float4 x = *reinterpret_cast<const float4*>(&part[row * D + d]);
+            const float mk = part[MR_MAX * D + row], lk = part[MR_MAX * D + MR_MAX + row];
+            status = max(status, __float_as_int(part[MR_MAX * D + 2 * MR_MAX]));
+            const float now = fmaxf(m, mk);
+            const float fa = m == NEG_INF ? 1.0f : ex2(m - now), fb = mk == NEG_INF ? 1.0f : ex2(mk - now);
+            l = l * fa + lk * fb;
+            o.x = o.x * fa + x.x * fb;
+            o.y = o.y * fa + x.y * fb;
+            o.z = o.z * fa + x.z * fb;
+            o.w = o.w * fa + x.w * fb;
+            m = now;
+        }
+        finish_row4<DT>(P, b, h, r, rq.rows, status, d, o, m, l);
+        if (i == 0 && P.row_status && h == 0 && rt == 0) P.row_status[b] = status;
+    }
+}
+
+template <int DT, int D, int MT>
+cudaError_t launch_rows(AttnParams& P, int sms, cudaStream_t st)
+{
+    constexpr int MR = MT * 16;
+    P.RT = (P.R + MR - 1) / MR;
+    const size_t smem = (size_t)AW * ASTAGES * 2 * SLICE * D;
+    static_assert((size_t)AW * ASTAGES * 2 * SLICE * D >= (size_t)AW * MR * D * 4, "the ring holds the warps' sums");
+    auto* k = attn_rows_kernel<DT, D, MT>;
+    static int per_sm = 0;
+    if (per_sm == 0) {
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        int n = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, ANT, smem);
+        if (e != cudaSuccess) return e;
+        per_sm = n < 1 ? 1 : n;
+    }
+    int ctas = per_sm * sms;
+    if (ctas > ATTN_MAX_CTAS) ctas = ATTN_MAX_CTAS;
+    k<<<ctas, ANT, smem, st>>>(P);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    attn_merge_kernel<DT, D><<<ctas, 256, 0, st>>>(P, MR);
+    return cudaGetLastError();
+}
+
+template <int DT, int D>
+cudaError_t launch_dim(AttnParams& P, int sms, cudaStream_t st)
+{
+    return P.R <= 16 ? launch_rows<DT, D, 1>(P, sms, st) : launch_rows<DT, D, 2>(P, sms, st);
+}
+
+}  // namespace
+
+size_t attn_workspace_bytes(int D) { return (size_t)2 * ATTN_MAX_CTAS * part_floats(D) * sizeof(float); }
+
+cudaError_t launch_attention(AttnParams& P, int dtype, int sms, cudaStream_t st)
+{
+    if (dtype == DT_BF16) return P.D == 128 ? launch_dim<DT_BF16, 128>(P, sms, st) : launch_dim<DT_BF16, 64>(P, sms, st);
+    return P.D == 128 ? launch_dim<DT_F16, 128>(P, sms, st) : launch_dim<DT_F16, 64>(P, sms, st);
+}
+
+}  // namespace sv

@@ -1,0 +1,332 @@
+// sv_cache.cu -- kv_cache_write and kv_cache_read: quantising key/value rows into the 8-bit paged cache
+// and reading them back.
+//
+// Write.  A block is one page of one key/value head, for the keys and for the values apart.  With A the
+// largest magnitude among the rows that the call puts into the block, the scale is the smallest 2^e with
+// A <= 448 * 2^e; a block that already holds tokens of the request (its length ends inside the page)
+// keeps the larger of that and its old scale, and its earlier codes move to the new one.  A block begun by the
+// call ignores whatever scale the page had.  One CTA per block: the rows are read once, into registers,
+// reduced to A, scaled (exactly) and rounded.  Bound by HBM for prompts, by the launch and a chain of four dependent
+// loads (length, page, rows, scale) for a round's few rows.
+//
+// Read.  One 16-byte vector of codes per thread and step, scaled and rounded once to the type asked for.
+#include <cuda_bf16.h>
+
+#include "sv_round.cuh"
+
+namespace sv {
+
+namespace {
+
+template <int DT>
+struct Elem;
+template <>
+struct Elem<DT_F32> {
+    static constexpr int VEC = 4;
+};
+template <>
+struct Elem<DT_BF16> {
+    static constexpr int VEC = 8;
+};
+template <>
+struct Elem<DT_F16> {
+    static constexpr int VEC = 8;
+};
+
+template <int DT>
+__device__ __forceinline__ void widen(const uint4& w, float (&x)[Elem<DT>::VEC])
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == DT_F32) {
+            x[i] = __uint_as_float(u[i]);
+        } else if constexpr (DT == DT_BF16) {
+            x[2 * i] = bf16lo(u[i]);
+            x[2 * i + 1] = bf16hi(u[i]);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+}
+
+// Source rows are read 16 bytes at a time where `ALIGNED`, else element by element.
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ uint4 load16(const void* base, int64_t elem)
+{
+    constexpr int ES = DT == DT_F32 ? 4 : 2;
+    const char* p = reinterpret_cast<const char*>(base) + elem * ES;
+    if constexpr (ALIGNED) {
+        return ld_stream_v4(p);
+    } else {
+        uint4 w;
+        uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (ES == 4) {
+                u[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+            } else {
+                const unsigned short* h = reinterpret_cast<const unsigned short*>(p) + 2 * i;
+                u[i] = (uint32_t)__ldg(h) | (uint32_t)__ldg(h + 1) << 16;
+            }
+        }
+        return w;
+    }
+}
+
+// Whether request b's rows can be written, looked at by every CTA of the request alike, so that either
+// all of them write or none.  Called by all threads.
+__device__ int write_status(const CacheWriteParams& P, int b, int len, int count)
+{
+    __shared__ int bad;
+    if (threadIdx.x == 0) bad = ROW_OK;
+    __syncthreads();
+    const long long room = (long long)P.table_width * P.page;
+    int mine = ROW_OK;
+    if (len < 0 || count > P.T || (long long)len + count > room ||
+        (P.out_nodes && count - 1 > P.nodes_width)) {
+        mine = ROW_BAD_LENGTH;
+    } else if (count > 0) {
+        const int p0 = len / P.page, p1 = (int)(((long long)len + count - 1) / P.page);
+        for (int j = p0 + threadIdx.x; j <= p1; j += blockDim.x)
+            if ((unsigned)__ldg(P.page_table + (size_t)b * P.table_width + j) >= (unsigned)P.pages) mine = ROW_BAD_PAGE;
+        if (P.out_nodes)
+            for (int i = threadIdx.x; i < count - 1; i += blockDim.x)
+                if ((unsigned)__ldg(P.out_nodes + (size_t)b * P.nodes_width + i) >= (unsigned)(P.T - 1)) mine = max(mine, (int)ROW_BAD_NODE);
+    }
+    if (mine != ROW_OK) atomicMax(&bad, mine);
+    __syncthreads();
+    return bad;
+}
+
+// NV: 16-byte source vectors per thread, at most (a page's worth over NT threads, rounded up to a power of two)
+template <int DT, int NV, bool ALIGNED>
+__global__ void __launch_bounds__(NT) cache_write_kernel(CacheWriteParams P)
+{
+    constexpr int VEC = Elem<DT>::VEC;
+    __shared__ float red[WARPS];
+    const int which = blockIdx.y & 1, h = blockIdx.y >> 1, b = blockIdx.z, t = threadIdx.x;
+    const int len = __ldg(P.lens + b);
+    const int count = P.accepted_len ? min(max(__ldg(P.accepted_len + b), -1), P.T) + 1 : P.T;
+    const int status = write_status(P, b, len, count);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) {
+        if (P.row_status) P.row_status[b] = status;
+        if (P.lens_out) P.lens_out[b] = status == ROW_OK ? len + count : len;
+    }
+    if (status != ROW_OK) return;
+    const int j = len / P.page + blockIdx.x;                       // page of the request
+    const int first = max((int)(len - (long long)j * P.page), 0);  // slots the request held before
+    const long long r0 = (long long)j * P.page + first - len;      // the first row that goes into this page
+    if (r0 >= count) return;
+    const int rows = (int)min((long long)count - r0, (long long)(P.page - first));
+    const int page = __ldg(P.page_table + (size_t)b * P.table_width + j);
+
+    const int vpr = P.D / VEC;  // vectors per row
+    uint4 x[NV];
+    float amax = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int i = t + k * NT;
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (i < rows * vpr) {
+            const int at = (int)r0 + i / vpr;
+            const int row = !P.out_nodes || at == 0 ? at : __ldg(P.out_nodes + (size_t)b * P.nodes_width + at - 1) + 1;
+            x[k] = load16<DT, ALIGNED>(P.src[which], b * P.sb[which] + row * P.st[which] + h * P.sh[which] + (i % vpr) * VEC);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        float f[VEC];
+        widen<DT>(x[k], f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float a = fabsf(f[e]);
+            // what the largest scale cannot hold (and an infinity) becomes NaN and sets no scale
+            if (a <= CACHE_MAX_CODE * 0x1p60f) amax = fmaxf(amax, a);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if ((t & 31) == 0) red[t >> 5] = amax;
+    float* sp = P.scale[which] + (size_t)page * P.Hkv + h;
+    const float old = first > 0 ? *sp : 0.0f;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) amax = fmaxf(amax, red[w]);
+    const int e = cache_scale_exp(amax);
+    float s = exp2_int(e);
+    float inv = exp2_int(-e);
+    uint8_t* dst = P.codes[which] + ((size_t)page * P.Hkv + h) * P.page * P.D;
+    if (old >= s) {
+        s = old;
+        inv = 1.0f / old;
+    } else if (first > 0) {
+        // the page's earlier codes move to the larger scale: exact but for subnormals
+        const float ratio = old * inv;
+        for (int i = t; i < first * P.D / 16; i += NT) {
+            uint4 w = reinterpret_cast<uint4*>(dst)[i];
+            uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t lo = e4m3x2_to_half2((uint16_t)u[k]), hi = e4m3x2_to_half2((uint16_t)(u[k] >> 16));
+                const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+                const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                u[k] = (uint32_t)e4m3x2_from(a.x * ratio, a.y * ratio) |
+                       (uint32_t)e4m3x2_from(c.x * ratio, c.y * ratio) << 16;
+            }
+            reinterpret_cast<uint4*>(dst)[i] = w;
+        }
+    }
+    if (t == 0) *sp = s;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int i = t + k * NT;
+        if (i < rows * vpr) {
+            float f[VEC];
+            widen<DT>(x[k], f);
+            uint16_t c[VEC / 2];
+#pragma unroll
+            for (int q = 0; q < VEC / 2; ++q) c[q] = e4m3x2_from(f[2 * q] * inv, f[2 * q + 1] * inv);
+            uint8_t* o = dst + (size_t)(first + i / vpr) * P.D + (i % vpr) * VEC;
+            if constexpr (VEC == 8)
+                *reinterpret_cast<uint2*>(o) = make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
+            else
+                *reinterpret_cast<uint32_t*>(o) = c[0] | (uint32_t)c[1] << 16;
+        }
+    }
+}
+
+template <int DT, bool ALIGNED>
+cudaError_t write_launch(const CacheWriteParams& P, cudaStream_t st)
+{
+    const int pages = (P.T + P.page - 2) / P.page + 1;  // pages that T rows can touch
+    const dim3 grid((unsigned)pages, (unsigned)(2 * P.Hkv), (unsigned)P.B);
+    const int vecs = (min(P.page, P.T) * P.D / Elem<DT>::VEC + NT - 1) / NT;
+    if (vecs <= 1) cache_write_kernel<DT, 1, ALIGNED><<<grid, NT, 0, st>>>(P);
+    else if (vecs <= 4) cache_write_kernel<DT, 4, ALIGNED><<<grid, NT, 0, st>>>(P);
+    else if (vecs <= 8) cache_write_kernel<DT, 8, ALIGNED><<<grid, NT, 0, st>>>(P);
+    else cache_write_kernel<DT, 16, ALIGNED><<<grid, NT, 0, st>>>(P);
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- read
+
+template <int DT>
+__device__ __forceinline__ void store_codes(void* out, int64_t elem, const uint4& w, float s)
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = e4m3x2_to_half2((uint16_t)u[i]), hi = e4m3x2_to_half2((uint16_t)(u[i] >> 16));
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+        const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+        x[4 * i] = a.x * s;
+        x[4 * i + 1] = a.y * s;
+        x[4 * i + 2] = c.x * s;
+        x[4 * i + 3] = c.y * s;
+    }
+    if constexpr (DT == DT_F32) {
+        float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + elem);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) __stcs(o + i, make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+    } else {
+        uint32_t r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (DT == DT_BF16)
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+            else
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+        }
+        uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(out) + elem);
+        __stcs(o, make_uint4(r[0], r[1], r[2], r[3]));
+        __stcs(o + 1, make_uint4(r[4], r[5], r[6], r[7]));
+    }
+}
+
+// Vector i of the output covers 16 channels of (b, token, head); consecutive threads take consecutive
+// vectors, so stores are contiguous and loads come in runs of a head's D bytes.
+template <int DT>
+__global__ void __launch_bounds__(NT) cache_read_kernel(CacheReadParams P)
+{
+    const int which = blockIdx.z, b = blockIdx.y;
+    const int vpt = P.Hkv * P.D / 16;
+    const long long n = (long long)P.max_len * vpt;
+    const int start = P.start ? __ldg(P.start + b) : 0;
+    const int len = __ldg(P.lens + b);
+    const long long room = (long long)P.table_width * P.page;
+    const bool bad_len = start < 0 || len < 0 || len > room;
+    const int32_t* table = P.page_table + (size_t)b * P.table_width;
+    if (blockIdx.x == 0 && which == 0 && P.row_status) {
+        int mine = bad_len ? ROW_BAD_LENGTH : ROW_OK;
+        if (!bad_len) {
+            const long long stop = min((long long)len, (long long)start + P.max_len);
+            for (long long j = start / P.page + (long long)threadIdx.x; j * P.page < stop; j += NT)
+                if ((unsigned)__ldg(table + j) >= (unsigned)P.pages) mine = ROW_BAD_PAGE;
+        }
+        mine = __syncthreads_or(mine == ROW_BAD_PAGE) ? ROW_BAD_PAGE : mine;
+        if (threadIdx.x == 0) P.row_status[b] = mine;
+    }
+    constexpr int U = 4;  // vectors in flight per thread
+    const long long stride = (long long)gridDim.x * NT;
+    for (long long i0 = (long long)blockIdx.x * NT + threadIdx.x; i0 < n; i0 += U * stride) {
+        uint4 w[U];
+        float s[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const long long i = i0 + k * stride;
+            w[k] = make_uint4(0, 0, 0, 0);
+            s[k] = bad_len ? __int_as_float(0x7fc00000) : 0.0f;
+            if (i < n && !bad_len) {
+                const long long tok = start + i / vpt;
+                if (tok < len) {
+                    const int hv = (int)(i % vpt), h = hv / (P.D / 16);
+                    const int page = __ldg(table + tok / P.page);
+                    if ((unsigned)page < (unsigned)P.pages) {
+                        const size_t blk = (size_t)page * P.Hkv + h;
+                        s[k] = __ldg(P.scale[which] + blk);
+                        w[k] = ld_stream_v4(P.codes[which] + (blk * P.page + tok % P.page) * P.D + (hv % (P.D / 16)) * 16);
+                    } else {
+                        s[k] = __int_as_float(0x7fc00000);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const long long i = i0 + k * stride;
+            if (i < n) store_codes<DT>(P.out[which], ((long long)b * n + i) * 16, w[k], s[k]);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const CacheWriteParams& P, int dtype, cudaStream_t st)
+{
+    const int vec = dtype == DT_F32 ? 4 : 8;
+    bool aligned = true;
+    for (int i = 0; i < 2; ++i)
+        aligned = aligned && reinterpret_cast<uintptr_t>(P.src[i]) % 16 == 0 && P.sb[i] % vec == 0 &&
+                  P.st[i] % vec == 0 && P.sh[i] % vec == 0;
+    if (dtype == DT_F32) return aligned ? write_launch<DT_F32, true>(P, st) : write_launch<DT_F32, false>(P, st);
+    if (dtype == DT_BF16) return aligned ? write_launch<DT_BF16, true>(P, st) : write_launch<DT_BF16, false>(P, st);
+    return aligned ? write_launch<DT_F16, true>(P, st) : write_launch<DT_F16, false>(P, st);
+}
+
+cudaError_t launch_cache_read(const CacheReadParams& P, int dtype, int sms, cudaStream_t st)
+{
+    const long long n = (long long)P.max_len * P.Hkv * P.D / 16;
+    const long long want = (n + 4 * NT - 1) / (4 * NT);
+    const long long most = max(1LL, 16LL * sms / P.B);  // about eight resident CTAs per SM, two tensors
+    const dim3 grid((unsigned)max(1LL, min(want, most)), (unsigned)P.B, 2);
+    if (dtype == DT_F32) cache_read_kernel<DT_F32><<<grid, NT, 0, st>>>(P);
+    else if (dtype == DT_BF16) cache_read_kernel<DT_BF16><<<grid, NT, 0, st>>>(P);
+    else cache_read_kernel<DT_F16><<<grid, NT, 0, st>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace sv
