@@ -412,11 +412,11 @@ spec_status spec_verify_noalloc(const void* target_logits, const void* draft_log
  *                           (with equal strides) but must not overlap it otherwise
  *   tokens  [B, N]          int32 drafted tokens, R <= N + 1, N <= 4096 (NULL when N == 0)
  *   parents [B, N]          int32 in [-1, i), as the tree calls take it; NULL: a chain
- *   history [B, H]          int32: tokens before the round (prompt, then output); entries outside [0, V) are
+ *   history [B, H]          int32, H <= 2^28: tokens before the round (prompt, then output); entries outside [0, V) are
  *                           ignored.  history_len [B] (NULL: H) of them count, the first prompt_len [B]
  *                           (NULL: 0) are the prompt
  *   repetition, presence, frequency [B]   fp32 (NULL: 1, 0, 0); repetition > 0
- *   bias_tokens, bias_values [B, nb]      int32, fp32; entries outside [0, V) are ignored; of entries that
+ *   bias_tokens, bias_values [B, nb]      int32, fp32, nb <= 16384; entries outside [0, V) are ignored; of entries that
  *                                         name one token the last holds
  *   allowed [B, R, ceil(V/32)]            uint32 bits as in spec_verify_masked, NULL: no mask
  *

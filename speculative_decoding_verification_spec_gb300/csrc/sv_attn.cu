@@ -35,8 +35,19 @@ constexpr int ASTAGES = 4;
 constexpr int MR_MAX = 32;      // rows of the largest row tile
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 
-// a part of a group in the workspace: o [MR_MAX][D], then m, l [MR_MAX], then the status
-__host__ __device__ constexpr size_t part_floats(int D) { return (size_t)MR_MAX * D + 2 * MR_MAX + 32; }
+// a part of a group of MR rows in the workspace: o [MR][D], then m, l [MR], then the status
+__host__ __device__ constexpr size_t part_floats(int MR, int D) { return (size_t)MR * D + 2 * MR + 32; }
+
+// parts of the group that starts in CTA c and ends at unit `end`: CTA k holds units [total k / ctas, total (k + 1) / ctas)
+__device__ __forceinline__ int parts_of(long long total, int c, int ctas, long long end)
+{
+    int last = c;
+    while (total * (last + 1) / ctas < end) ++last;
+    return last - c + 1;
+}
+
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t swz_off(int D, int row, int chunk)
 {
@@ -112,7 +123,7 @@ __device__ __forceinline__ ReqInfo req_info(const AttnParams& P, int b)
 // it, warp 0 works
 struct Place {
     long long total, pre;  // pre: units of the requests before b
-    int b;
+    int b, ctas;           // CTAs that work: no more than there are units, so none of them is empty
 };
 
 __device__ Place find_place(const AttnParams& P, int cta, int ctas, Place* sh)
@@ -127,7 +138,8 @@ __device__ Place find_place(const AttnParams& P, int cta, int ctas, Place* sh)
             for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
             total += v;
         }
-        const long long u0 = total * cta / ctas;
+        if (total < ctas) ctas = (int)total;
+        const long long u0 = cta < ctas ? total * cta / ctas : total;
         long long pre = 0;
         int found = P.B;
         for (int b0 = 0; b0 < P.B; b0 += 32) {
@@ -150,6 +162,7 @@ __device__ Place find_place(const AttnParams& P, int cta, int ctas, Place* sh)
             sh->total = total;
             sh->pre = pre;
             sh->b = found;
+            sh->ctas = ctas;
         }
     }
     __syncthreads();
@@ -303,9 +316,11 @@ __global__ void __launch_bounds__(ANT, MT == 1 ? 3 : 2) attn_rows_kernel(AttnPar
 
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const Place at = find_place(P, blockIdx.x, gridDim.x, &place);
-    long long u = at.total * blockIdx.x / gridDim.x;
-    const long long u1 = at.total * (blockIdx.x + 1) / gridDim.x;
-    if (u >= u1) return;
+    if (tid == 0) P.joins[blockIdx.x].parts = 0;
+    launch_dependents();
+    if ((int)blockIdx.x >= at.ctas) return;
+    long long u = at.total * blockIdx.x / at.ctas;
+    const long long u1 = at.total * (blockIdx.x + 1) / at.ctas;
     int b = at.b;
     long long pre = at.pre;
     ReqInfo rq = req_info(P, b);
@@ -609,7 +624,7 @@ __global__ void __launch_bounds__(ANT, MT == 1 ? 3 : 2) attn_rows_kernel(AttnPar
             }
         __syncthreads();
         const int status = sstatus;
-        float* part = P.parts + ((size_t)blockIdx.x * 2 + (first && first_cont ? 0 : 1)) * part_floats(D);
+        float* part = P.parts + ((size_t)blockIdx.x * 2 + (first && first_cont ? 0 : 1)) * part_floats(MR, D);
         for (int i = tid; i < MR * (D / 4); i += ANT) {
             const int row = i / (D / 4), d = i % (D / 4) * 4;
             const int r = rt * MR + row;
@@ -635,14 +650,19 @@ __global__ void __launch_bounds__(ANT, MT == 1 ? 3 : 2) attn_rows_kernel(AttnPar
             } else {
                 *reinterpret_cast<float4*>(&part[row * D + d]) = o;
                 if (d == 0) {
-                    part[MR_MAX * D + row] = m;
-                    part[MR_MAX * D + MR_MAX + row] = l;
+                    part[MR * D + row] = m;
+                    part[MR * D + MR + row] = l;
                 }
             }
         }
         if (tid == 0) {
-            if (!whole) part[MR_MAX * D + 2 * MR_MAX] = __int_as_float(status);
-            else if (P.row_status && h == 0 && rt == 0) P.row_status[b] = status;
+            if (whole) {
+                if (P.row_status && h == 0 && rt == 0) P.row_status[b] = status;
+            } else {
+                part[MR * D + 2 * MR] = __int_as_float(status);
+                // the group's first part: tell the joining kernel how far the group reaches
+                if (tile0 == 0) P.joins[blockIdx.x] = {parts_of(at.total, blockIdx.x, at.ctas, u + rq.n), b, h, rt, rq.rows};
+            }
         }
         first = false;
         u += tile1 - tile0;
@@ -653,55 +673,113 @@ __global__ void __launch_bounds__(ANT, MT == 1 ? 3 : 2) attn_rows_kernel(AttnPar
     }
 }
 
-// Joins the parts of the group that starts in streaming CTA blockIdx.x and ends in a later one.
+// Joins the parts of the group that starts in streaming CTA blockIdx.x and ends in a later one: part 0 is that
+// CTA's second slot, part k the first slot of CTA blockIdx.x + k.  Four warps share a row: each takes
+// every fourth part.
 template <int DT, int D>
 __global__ void __launch_bounds__(256) attn_merge_kernel(AttnParams P, int MR)
 {
-    __shared__ Place place;
-    const int c = blockIdx.x, ctas = gridDim.x;
-    const Place at = find_place(P, c, ctas, &place);
-    const long long u0 = at.total * c / ctas, u1 = at.total * (c + 1) / ctas;
-    if (u0 >= u1) return;
-    // the group of the last unit
-    int b = at.b;
-    long long pre = at.pre;
-    ReqInfo rq = req_info(P, b);
-    while (u1 - 1 >= pre + (long long)rq.n * P.Hkv * P.RT) {
-        pre += (long long)rq.n * P.Hkv * P.RT;
-        rq = req_info(P, ++b);
-    }
-    const int grp = (int)((u1 - 1 - pre) / rq.n);
-    const long long gs = pre + (long long)grp * rq.n, ge = gs + rq.n;
-    if (gs < u0 || ge <= u1) return;
-    const int h = grp / P.RT, rt = grp % P.RT;
-    int last = c;  // the CTA that holds unit ge - 1
-    while (at.total * (last + 1) / ctas < ge) ++last;
-    const size_t pf = part_floats(D);
-    for (int i = threadIdx.x; i < MR * (D / 4); i += 256) {
-        const int row = i / (D / 4), d = i % (D / 4) * 4;
-        const int r = rt * MR + row;
-        if (r >= P.R) break;
+    __shared__ float4 so[8][32];
+    __shared__ float sm[8], sl[8];
+    __shared__ int ss[8];
+    depend_wait();
+    const AttnJoin J = P.joins[blockIdx.x];
+    if (J.parts == 0) return;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, q = w & 3;
+    const size_t pf = part_floats(MR, D);
+    for (int row0 = blockIdx.y * 2; row0 < MR; row0 += gridDim.y * 2) {
+        const int row = row0 + (w >> 2), r = J.rt * MR + row;
+        const bool have = row < MR && r < P.R;
         float m = NEG_INF, l = 0.0f;
         int status = ROW_OK;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int k = c; k <= last; ++k) {
-            const float* part = P.parts + ((size_t)k * 2 + (k == c ? 1 : 0)) * pf;
-            if (at.total * k / ctas == at.total * (k + 1) / ctas) continue;
-            const float4 x = *reinterpret_cast<const float4*>(&part[row * D + d]);
-            const float mk = part[MR_MAX * D + row], lk = part[MR_MAX * D + MR_MAX + row];
-            status = max(status, __float_as_int(part[MR_MAX * D + 2 * MR_MAX]));
-            const float now = fmaxf(m, mk);
-            const float fa = m == NEG_INF ? 1.0f : ex2(m - now), fb = mk == NEG_INF ? 1.0f : ex2(mk - now);
-            l = l * fa + lk * fb;
-            o.x = o.x * fa + x.x * fb;
-            o.y = o.y * fa + x.y * fb;
-            o.z = o.z * fa + x.z * fb;
-            o.w = o.w * fa + x.w * fb;
-            m = now;
+        if (have) {
+            const auto part_of = [&](int k) { return P.parts + ((size_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * pf; };
+            // the largest reference of this warp's parts first, so that the sums need no rescaling
+            for (int k = q + 4 * lane; k < J.parts; k += 128) {
+                const float* part = part_of(k);
+                m = fmaxf(m, part[(size_t)MR * D + row]);
+                status = max(status, __float_as_int(part[(size_t)MR * D + 2 * MR]));
+            }
+#pragma unroll
+            for (int s = 16; s; s >>= 1) {
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+                status = max(status, __shfl_xor_sync(0xffffffffu, status, s));
+            }
+            constexpr int JU = 8;
+            for (int k0 = q; k0 < J.parts; k0 += 4 * JU) {
+                float4 x[JU];
+                float mk[JU], lk[JU];
+#pragma unroll
+                for (int j = 0; j < JU; ++j) {
+                    const int k = k0 + 4 * j;
+                    mk[j] = NEG_INF;
+                    lk[j] = 0.0f;
+                    x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (k < J.parts) {
+                        const float* part = part_of(k);
+                        mk[j] = part[(size_t)MR * D + row];
+                        lk[j] = part[(size_t)MR * D + MR + row];
+                        if (lane < D / 4) x[j] = *reinterpret_cast<const float4*>(&part[(size_t)row * D + lane * 4]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < JU; ++j) {
+                    const float f = mk[j] == NEG_INF ? 1.0f : ex2(mk[j] - m);  // without a token: zeros, or NaN, which stays
+                    l = fmaf(lk[j], f, l);
+                    o.x = fmaf(x[j].x, f, o.x);
+                    o.y = fmaf(x[j].y, f, o.y);
+                    o.z = fmaf(x[j].z, f, o.z);
+                    o.w = fmaf(x[j].w, f, o.w);
+                }
+            }
         }
-        finish_row4<DT>(P, b, h, r, rq.rows, status, d, o, m, l);
-        if (i == 0 && P.row_status && h == 0 && rt == 0) P.row_status[b] = status;
+        so[w][lane] = o;
+        if (lane == 0) {
+            sm[w] = m;
+            sl[w] = l;
+            ss[w] = status;
+        }
+        __syncthreads();
+        if (q == 0 && have) {
+            float M = NEG_INF, L = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                M = fmaxf(M, sm[w + k]);
+                status = max(status, ss[w + k]);
+            }
+            float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float f = sm[w + k] == NEG_INF ? 1.0f : ex2(sm[w + k] - M);
+                const float4 x = so[w + k][lane];
+                L = fmaf(sl[w + k], f, L);
+                O.x = fmaf(x.x, f, O.x);
+                O.y = fmaf(x.y, f, O.y);
+                O.z = fmaf(x.z, f, O.z);
+                O.w = fmaf(x.w, f, O.w);
+            }
+            if (lane < D / 4) finish_row4<DT>(P, J.b, J.h, r, J.rows, status, lane * 4, O, M, L);
+            if (row == 0 && lane == 0 && P.row_status && J.h == 0 && J.rt == 0) P.row_status[J.b] = status;
+        }
+        __syncthreads();
     }
+}
+
+// the joining kernel, launched so that its CTAs are in place when the streaming kernel ends
+template <int DT, int D>
+cudaError_t launch_merge(const AttnParams& P, int ctas, int MR, cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)min((MR + 1) / 2, 16));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_merge_kernel<DT, D>, P, MR);
 }
 
 template <int DT, int D, int MT>
@@ -726,8 +804,7 @@ cudaError_t launch_rows(AttnParams& P, int sms, cudaStream_t st)
     k<<<ctas, ANT, smem, st>>>(P);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    attn_merge_kernel<DT, D><<<ctas, 256, 0, st>>>(P, MR);
-    return cudaGetLastError();
+    return launch_merge<DT, D>(P, ctas, MR, st);
 }
 
 template <int DT, int D>
@@ -738,7 +815,10 @@ cudaError_t launch_dim(AttnParams& P, int sms, cudaStream_t st)
 
 }  // namespace
 
-size_t attn_workspace_bytes(int D) { return (size_t)2 * ATTN_MAX_CTAS * part_floats(D) * sizeof(float); }
+size_t attn_workspace_bytes(int D)
+{
+    return ATTN_MAX_CTAS * sizeof(AttnJoin) + (size_t)2 * ATTN_MAX_CTAS * part_floats(MR_MAX, D) * sizeof(float);
+}
 
 cudaError_t launch_attention(AttnParams& P, int dtype, int sms, cudaStream_t st)
 {

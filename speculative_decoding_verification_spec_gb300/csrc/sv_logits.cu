@@ -11,11 +11,12 @@
 // in fp32, rounded once to the logits' type.
 //
 // Bound by HBM: every logit is read and written once.  One CTA owns a run of `chunk` vocabulary entries of one
-// request for all its rows: it counts the history tokens that fall into its run in shared memory (a
-// 32-bit word per entry, so no count is kept from call to call), then streams the rows.  An entry's word and
-// bias serve every row.  A drafted token changes single entries of single rows: its entry's word
-// carries a flag, and the owning thread, alone, asks which of the run's drafted tokens lie on the row's
-// path; so rows need no barrier between them.
+// request for all its rows.  It counts the history tokens that fall into its run in shared memory (a 32-bit word per
+// entry, so nothing is kept from call to call) and lists the entries that anything touches.  Then it copies the rows in
+// 16-byte vectors, with the mask, and at last rewrites the touched entries, one thread per (entry, row): a
+// text's words crowd into few runs (frequent tokens have low numbers), and in the copy loop each of them would hold up
+// the 31 other lanes of its warp, row after row.  Rows need not start on a 16-byte boundary (an odd V): each row's
+// vectors start at its own first boundary, the few entries before it and after its last whole vector go one by one.
 #include "sv_round.cuh"
 
 namespace sv {
@@ -24,8 +25,12 @@ namespace {
 
 constexpr uint32_t LW_SEEN = 0x80000000u;   // the entry is in the prompt
 constexpr uint32_t LW_DRAFT = 0x40000000u;  // a drafted token names the entry
-constexpr uint32_t LW_COUNT = 0x3fffffffu;
-constexpr int LROWS = 4;                    // rows whose loads are in flight together
+constexpr uint32_t LW_BIAS = 0x20000000u;   // a bias names the entry
+constexpr uint32_t LW_COUNT = 0x1fffffffu;
+constexpr int LU = 8;                       // vectors in flight per thread
+constexpr int HU = 8;                       // history tokens in flight per thread
+constexpr int LMASK = 64;                   // drafted tokens of a run whose paths are kept as bit masks
+constexpr int LMASK_ROWS = 512;             // and the rows that this is done for
 
 // the node of row r - 1 (or its ancestors) is `node`: walks towards the frontier, whose parent is -1.
 // A parent outside [-1, i) ends the walk, so it always ends.
@@ -42,168 +47,355 @@ __device__ bool on_path(const LogitsParams& P, int b, int r, int node)
     return i == node;
 }
 
-template <int DT, int VEC>
-__device__ __forceinline__ void store_vec(char* row, long long v, const float (&x)[VEC])
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
-    if constexpr (DT == DT_BF16) {
-        auto pack = [](float lo, float hi) {
-            uint32_t r;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-            return r;
-        };
-        if constexpr (VEC == 8) {
-            uint4 w;
-            w.x = pack(x[0], x[1]);
-            w.y = pack(x[2], x[3]);
-            w.z = pack(x[4], x[5]);
-            w.w = pack(x[6], x[7]);
-            __stcs(reinterpret_cast<uint4*>(row) + v, w);
-        } else {
-            reinterpret_cast<unsigned short*>(row)[v] = (unsigned short)pack(x[0], 0.0f);
-        }
-    } else if constexpr (VEC == 4) {
-        __stcs(reinterpret_cast<float4*>(row) + v, make_float4(x[0], x[1], x[2], x[3]));
-    } else {
-        reinterpret_cast<float*>(row)[v] = x[0];
-    }
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
-template <int DT, int VEC>
-__device__ __forceinline__ void load_row_vec(const char* row, long long v, float (&x)[VEC])
+template <int DT>
+__device__ __forceinline__ float load_one(const char* row, int v)
 {
     // plain loads: `out` may be the logits themselves, so the read-only path is not used
-    if constexpr (DT == DT_BF16 && VEC == 8) {
-        const uint4 w = __ldcs(reinterpret_cast<const uint4*>(row) + v);
-        x[0] = bf16lo(w.x); x[1] = bf16hi(w.x); x[2] = bf16lo(w.y); x[3] = bf16hi(w.y);
-        x[4] = bf16lo(w.z); x[5] = bf16hi(w.z); x[6] = bf16lo(w.w); x[7] = bf16hi(w.w);
-    } else if constexpr (DT == DT_BF16) {
-        x[0] = __uint_as_float((uint32_t)reinterpret_cast<const unsigned short*>(row)[v] << 16);
-    } else if constexpr (VEC == 4) {
-        const float4 w = __ldcs(reinterpret_cast<const float4*>(row) + v);
-        x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
-    } else {
-        x[0] = reinterpret_cast<const float*>(row)[v];
-    }
+    if constexpr (DT == DT_BF16) return __uint_as_float((uint32_t)reinterpret_cast<const unsigned short*>(row)[v] << 16);
+    else return reinterpret_cast<const float*>(row)[v];
+}
+template <int DT>
+__device__ __forceinline__ void store_one(char* row, int v, float x)
+{
+    if constexpr (DT == DT_BF16) reinterpret_cast<unsigned short*>(row)[v] = (unsigned short)pack_bf16(x, 0.0f);
+    else reinterpret_cast<float*>(row)[v] = x;
 }
 
+// what a CTA knows of its request and run
+struct Run {
+    int b, v0, ndraft, nbias;
+    float rep, inv_rep, pres, freq;
+    const uint32_t* words;
+    const uint16_t* draft;
+    const uint16_t* bias;
+    const uint32_t* base;      // word of a drafted entry (its own holds the entry's number)
+    const uint64_t* same;      // which of the run's drafted tokens name that entry, or null
+    const uint64_t* row_path;  // which of them lie on each row's path
+};
+
+// the penalties of an entry that was generated c times; the division is a product with the reciprocal: one more
+// fp32 rounding
+__device__ __forceinline__ float penalised(const Run& q, float x, int c, bool seen)
+{
+    if (c > 0 || seen) x = x > 0.0f ? x * q.inv_rep : x * q.rep;
+    if (c > 0) x -= fmaf(q.freq, (float)c, q.pres);
+    return x;
+}
+
+// an entry that a drafted token or a bias names
+__device__ __noinline__ float touched_rare(const LogitsParams& P, const Run& q, int r, int v, float x, uint32_t w)
+{
+    int extra = 0;
+    float add = 0.0f;
+    if (w & LW_DRAFT) {
+        const int g = (int)(w & LW_COUNT);
+        w = q.base[g];
+        if (q.same) {
+            extra = __popcll(q.same[g] & q.row_path[r]);
+        } else {
+            for (int i = 0; i < q.ndraft; ++i) {
+                const int node = q.draft[i];
+                if (node < r && __ldg(P.tokens + (size_t)q.b * P.N + node) == v && on_path(P, q.b, r, node)) ++extra;
+            }
+        }
+    }
+    if (w & LW_BIAS) {
+        int last = -1;  // of entries that name one token the last holds
+        for (int i = 0; i < q.nbias; ++i) {
+            const int k = q.bias[i];
+            if (k > last && __ldg(P.bias_tokens + (size_t)q.b * P.nb + k) == v) last = k;
+        }
+        if (last >= 0) add = __ldg(P.bias_values + (size_t)q.b * P.nb + last);
+    }
+    return penalised(q, x, (int)(w & LW_COUNT) + extra, (w & LW_SEEN) != 0) + add;
+}
+
+// logit x of touched entry v in row r
+__device__ __forceinline__ float touched(const LogitsParams& P, const Run& q, int r, int v, float x)
+{
+    const uint32_t w = q.words[v - q.v0];
+    if (w & (LW_DRAFT | LW_BIAS)) return touched_rare(P, q, r, v, x, w);
+    return penalised(q, x, (int)(w & LW_COUNT), (w & LW_SEEN) != 0);
+}
+
+// The CTA that owns entry v of a row writes it: the one whose run holds the start of v's vector, or v itself where the
+// row has no whole vector around it (s entries before the first boundary, those from `tail` on).
+template <int VEC>
+__device__ __forceinline__ bool owns(int v, int s, int V, int v0, int n)
+{
+    const int tail = s + ((V - s) & ~(VEC - 1));
+    const int start = v < s || v >= tail ? v : s + ((v - s) & ~(VEC - 1));
+    return start >= v0 && start < v0 + n;
+}
+
+template <int DT, int VEC>
+__device__ __forceinline__ int lead_in(const char* row)  // entries before the row's first 16-byte boundary
+{
+    constexpr int ES = DT == DT_BF16 ? 2 : 4;
+    return VEC == 1 ? 0 : (int)((0u - (uint32_t)reinterpret_cast<uintptr_t>(row)) & 15u) / ES;
+}
+
+// VEC: elements of a 16-byte vector, or 1 where a row of the output is not aligned as its input is
 template <int DT, int VEC>
 __global__ void __launch_bounds__(NT) process_logits_kernel(LogitsParams P)
 {
+    constexpr size_t ES = DT == DT_BF16 ? 2 : 4;
     extern __shared__ uint32_t smem[];
-    uint32_t* words = smem;                                   // [chunk]
-    int32_t* bidx = reinterpret_cast<int32_t*>(smem) + P.chunk;  // [chunk], only with biases
-    __shared__ int ndraft, bad;
-    __shared__ uint16_t draft[LOGITS_MAX_NODES];              // nodes whose token falls into the run
+    // a vector that starts in the run may reach VEC - 1 entries past it: words and bits cover those too
+    const int room = P.chunk + 32;
+    uint32_t* words = smem;                                          // [room]
+    uint32_t* bits = smem + room;                                    // [room / 32] touched entries
+    uint32_t* base = bits + room / 32;                               // [N] words of the drafted entries
+    uint16_t* list = reinterpret_cast<uint16_t*>(base + P.N);        // [room] touched entries
+    uint16_t* draft = list + room;                                   // [N] nodes whose token is in the run
+    uint16_t* bias = draft + P.N;                                    // [nb]
+    __shared__ int ndraft, nentry, nbias, nlist, bad;
+    __shared__ uint64_t same[LMASK], row_path[LMASK_ROWS];
 
-    const int b = blockIdx.y;
-    const int v0 = blockIdx.x * P.chunk;
-    const int n = min(P.chunk, P.V - v0);
+    Run q;
+    const int b = q.b = blockIdx.y;
+    const int v0 = q.v0 = blockIdx.x * P.chunk;
+    const int n = min(P.chunk, P.V - v0);              // entries of the run
+    const int nw = min(n + VEC - 1, P.V - v0);         // and those that its last vectors may reach
     const int t = threadIdx.x;
-    for (int i = t; i < P.chunk; i += NT) words[i] = 0u;
-    if (P.nb)
-        for (int i = t; i < P.chunk; i += NT) bidx[i] = 0;
-    if (t == 0) ndraft = 0, bad = 0;
+    const char* in0 = reinterpret_cast<const char*>(P.logits) + (size_t)b * P.in_b * ES;
+    char* out0 = reinterpret_cast<char*>(P.out) + (size_t)b * P.out_b * ES;
+    const uint32_t* allowed0 = P.allowed ? P.allowed + (size_t)b * P.R * P.mwords : nullptr;
+    for (int i = t; i < room + room / 32; i += NT) smem[i] = 0u;
+    if (t == 0) ndraft = 0, nentry = 0, nbias = 0, nlist = 0, bad = 0;
+    if (t < LMASK) same[t] = 0;
     __syncthreads();
 
     if (P.history) {
         const int hl = min(max(P.history_len ? __ldg(P.history_len + b) : P.H, 0), P.H);
         const int pl = P.prompt_len ? __ldg(P.prompt_len + b) : 0;
         const int32_t* h = P.history + (size_t)b * P.H;
-        for (int i = t; i < hl; i += NT) {
-            const uint32_t k = (uint32_t)(__ldg(h + i) - v0);
-            if (k < (uint32_t)n) {
-                if (i < pl) atomicOr(&words[k], LW_SEEN);
-                else atomicAdd(&words[k], 1u);
+        for (int i0 = t; i0 < hl; i0 += NT * HU) {
+            uint32_t k[HU];
+#pragma unroll
+            for (int j = 0; j < HU; ++j) k[j] = i0 + j * NT < hl ? (uint32_t)(__ldg(h + i0 + j * NT) - v0) : 0xffffffffu;
+#pragma unroll
+            for (int j = 0; j < HU; ++j) {
+                if (k[j] < (uint32_t)nw) {
+                    if (i0 + j * NT < pl) atomicOr(&words[k[j]], LW_SEEN);
+                    else atomicAdd(&words[k[j]], 1u);
+                    atomicOr(&bits[k[j] >> 5], 1u << (k[j] & 31));
+                }
             }
         }
     }
+    for (int i = t; i < P.nb; i += NT) {
+        const uint32_t k = (uint32_t)(__ldg(P.bias_tokens + (size_t)b * P.nb + i) - v0);
+        if (k < (uint32_t)nw) {
+            atomicOr(&words[k], LW_BIAS);
+            atomicOr(&bits[k >> 5], 1u << (k & 31));
+            bias[atomicAdd(&nbias, 1)] = (uint16_t)i;
+        }
+    }
+    __syncthreads();
+    // A drafted entry's word moves to `base` and makes room for the entry's number: the one thread that finds the
+    // word unflagged does it.
     for (int i = t; i < P.N; i += NT) {
         const uint32_t k = (uint32_t)(__ldg(P.tokens + (size_t)b * P.N + i) - v0);
-        if (k < (uint32_t)n) {
-            atomicOr(&words[k], LW_DRAFT);
+        if (k < (uint32_t)nw) {
+            const uint32_t was = atomicOr(&words[k], LW_DRAFT);
             draft[atomicAdd(&ndraft, 1)] = (uint16_t)i;
+            if (!(was & LW_DRAFT)) {
+                const int g = atomicAdd(&nentry, 1);
+                base[g] = was;
+                words[k] = LW_DRAFT | (uint32_t)g;
+                atomicOr(&bits[k >> 5], 1u << (k & 31));
+            }
         }
         if (P.parents && blockIdx.x == 0) {
             const int p = __ldg(P.parents + (size_t)b * P.N + i);
             if (p < -1 || p >= i) bad = 1;
         }
     }
-    for (int i = t; i < P.nb; i += NT) {
-        const uint32_t k = (uint32_t)(__ldg(P.bias_tokens + (size_t)b * P.nb + i) - v0);
-        if (k < (uint32_t)n) atomicMax(&bidx[k], i + 1);  // of entries that name one token the last holds
-    }
     __syncthreads();
     if (P.row_status && blockIdx.x == 0 && t == 0) P.row_status[b] = bad ? ROW_BAD_PARENT : ROW_OK;
-
-    const float rep = P.repetition ? __ldg(P.repetition + b) : 1.0f;
-    const float pres = P.presence ? __ldg(P.presence + b) : 0.0f;
-    const float freq = P.frequency ? __ldg(P.frequency + b) : 0.0f;
-    constexpr size_t ES = DT == DT_BF16 ? 2 : 4;
-    const char* in = reinterpret_cast<const char*>(P.logits) + (size_t)b * P.in_b * ES;
-    char* out = reinterpret_cast<char*>(P.out) + (size_t)b * P.out_b * ES;
-    const uint32_t* allowed = P.allowed ? P.allowed + (size_t)b * P.R * P.mwords : nullptr;
-
-    for (int k = t; k < n / VEC; k += NT) {
-        const long long v = v0 / VEC + k;
-        uint32_t any = 0, w[VEC];
-        float bias[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            w[e] = words[k * VEC + e];
-            any |= w[e];
-            bias[e] = 0.0f;
+    const bool masks = ndraft <= LMASK && P.R <= LMASK_ROWS;
+    if (masks && ndraft > 0) {
+        if (t < ndraft) {
+            const int v = __ldg(P.tokens + (size_t)b * P.N + draft[t]);
+            atomicOr(reinterpret_cast<unsigned long long*>(&same[words[v - v0] & LW_COUNT]), 1ull << t);
         }
-        if (P.nb) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int i = bidx[k * VEC + e];
-                if (i) {
-                    bias[e] = __ldg(P.bias_values + (size_t)b * P.nb + i - 1);
-                    any |= 1u;
+        for (int r = t; r < P.R; r += NT) {
+            uint64_t m = 0;
+            for (int node = r - 1; node >= 0;) {
+                if (!P.parents) {
+                    for (int i = 0; i < ndraft; ++i) m |= (uint64_t)(draft[i] <= node) << i;
+                    break;
                 }
+                for (int i = 0; i < ndraft; ++i) m |= (uint64_t)(draft[i] == node) << i;
+                const int p = __ldg(P.parents + (size_t)b * P.N + node);
+                if (p >= node) break;  // out of range: the path ends here
+                node = p;
+            }
+            row_path[r] = m;
+        }
+    }
+    for (int i = t; i < room / 32; i += NT) {
+        uint32_t left = bits[i];
+        if (left) {
+            int at = atomicAdd(&nlist, __popc(left));
+            for (; left; left &= left - 1) list[at++] = (uint16_t)(i * 32 + __ffs(left) - 1);
+        }
+    }
+
+    // the copy, with the mask
+    if constexpr (VEC == 1) {
+        for (int r = 0; r < P.R; ++r) {
+            const uint32_t* allowed = allowed0 ? allowed0 + (size_t)r * P.mwords : nullptr;
+            for (int v = v0 + t; v < v0 + n; v += NT) {
+                float x = load_one<DT>(in0 + (size_t)r * P.in_r * ES, v);
+                if (allowed && !(__ldg(allowed + (v >> 5)) >> (v & 31) & 1u)) x = NEG_INF;
+                store_one<DT>(out0 + (size_t)r * P.out_r * ES, v, x);
             }
         }
-        for (int r0 = 0; r0 < P.R; r0 += LROWS) {
-            float x[LROWS][VEC];
-            uint32_t ok[LROWS];
+    } else {
+        // slots: the vectors of a row that a thread may own in this run, threads apart
+        const int slots = (n + VEC * NT - 1) / (VEC * NT);
+        const char* in = in0;
+        for (int r = 0, slot = 0; r < P.R;) {
+            uint4 w[LU];
+            uint32_t ok[LU];
+            char* to[LU];  // null: no vector
 #pragma unroll
-            for (int j = 0; j < LROWS; ++j) {
-                const int r = r0 + j;
+            for (int j = 0; j < LU; ++j) {
+                to[j] = nullptr;
                 ok[j] = 0xffffffffu;
                 if (r < P.R) {
-                    load_row_vec<DT, VEC>(in + (size_t)r * P.in_r * ES, v, x[j]);
-                    if (allowed) ok[j] = __ldg(allowed + (size_t)r * P.mwords + (v * VEC >> 5)) >> (v * VEC & 31);
+                    const int s = lead_in<DT, VEC>(in);
+                    const int first = s + ((v0 - s + VEC - 1) & ~(VEC - 1));  // the first vector that starts in the run
+                    const int v = first + (slot * NT + t) * VEC;
+                    if (v < v0 + n && v + VEC <= P.V) {
+                        to[j] = out0 + ((size_t)r * P.out_r + v) * ES;
+                        w[j] = __ldcs(reinterpret_cast<const uint4*>(in + (size_t)v * ES));
+                        if (allowed0) {
+                            const uint32_t* a = allowed0 + (size_t)r * P.mwords + (v >> 5);
+                            ok[j] = __ldg(a) >> (v & 31);
+                            if ((v & 31) + VEC > 32) ok[j] |= __ldg(a + 1) << (32 - (v & 31));
+                        }
+                    }
+                    if (++slot == slots) {
+                        slot = 0;
+                        ++r;
+                        in += (size_t)P.in_r * ES;
+                    }
                 }
             }
 #pragma unroll
-            for (int j = 0; j < LROWS; ++j) {
-                const int r = r0 + j;
-                if (r >= P.R) break;
-                if (any) {
+            for (int j = 0; j < LU; ++j) {
+                if (!to[j]) continue;
+                uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        int c = (int)(w[e] & LW_COUNT);
-                        if (w[e] & LW_DRAFT) {
-                            for (int i = 0; i < ndraft; ++i) {
-                                const int node = draft[i];
-                                if (node < r && __ldg(P.tokens + (size_t)b * P.N + node) == (int)(v * VEC) + e &&
-                                    on_path(P, b, r, node))
-                                    ++c;
-                            }
-                        }
-                        float y = x[j][e];
-                        if (c > 0 || (w[e] & LW_SEEN)) y = y > 0.0f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
-                        if (c > 0) y = __fsub_rn(y, __fadd_rn(__fmul_rn(freq, (float)c), pres));
-                        x[j][e] = __fadd_rn(y, bias[e]);
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (DT == DT_BF16) {
+                        if (!(ok[j] >> (2 * e) & 1u)) u[e] = (u[e] & 0xffff0000u) | 0xff80u;
+                        if (!(ok[j] >> (2 * e + 1) & 1u)) u[e] = (u[e] & 0xffffu) | 0xff800000u;
+                    } else {
+                        if (!(ok[j] >> e & 1u)) u[e] = 0xff800000u;
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (!(ok[j] >> e & 1u)) x[j][e] = NEG_INF;
-                store_vec<DT, VEC>(out + (size_t)r * P.out_r * ES, v, x[j]);
+                __stcs(reinterpret_cast<uint4*>(to[j]), make_uint4(u[0], u[1], u[2], u[3]));
+            }
+        }
+        // the entries before a row's first boundary and after its last whole vector: at most VEC - 1 each
+        for (int f = t; f < P.R * 2 * VEC; f += NT) {
+            const int r = f / (2 * VEC), e = f % (2 * VEC);
+            const char* row = in0 + (size_t)r * P.in_r * ES;
+            const int s = min(lead_in<DT, VEC>(row), P.V);
+            const int v = e < VEC ? e : s + ((P.V - s) & ~(VEC - 1)) + e - VEC;
+            if ((e < VEC ? v < s : v < P.V) && v >= v0 && v < v0 + n) {
+                float x = load_one<DT>(row, v);
+                if (allowed0 && !(__ldg(allowed0 + (size_t)r * P.mwords + (v >> 5)) >> (v & 31) & 1u)) x = NEG_INF;
+                store_one<DT>(out0 + (size_t)r * P.out_r * ES, v, x);
             }
         }
     }
+    __syncthreads();
+
+    // The touched entries.  In place they still hold their logits here: the copy wrote back what it read.
+    q.ndraft = ndraft;
+    q.nbias = nbias;
+    q.words = words;
+    q.draft = draft;
+    q.bias = bias;
+    q.base = base;
+    q.same = masks ? same : nullptr;
+    q.row_path = row_path;
+    q.rep = P.repetition ? __ldg(P.repetition + b) : 1.0f;
+    q.inv_rep = 1.0f / q.rep;
+    q.pres = P.presence ? __ldg(P.presence + b) : 0.0f;
+    q.freq = P.frequency ? __ldg(P.frequency + b) : 0.0f;
+    const int touched_n = nlist;
+    const long long items = (long long)P.R * touched_n;
+    constexpr int TU = 4;
+    for (long long i0 = t; i0 < items; i0 += TU * NT) {
+        float x[TU];
+        int row[TU], at[TU];
+#pragma unroll
+        for (int j = 0; j < TU; ++j) {
+            const long long i = i0 + j * NT;
+            at[j] = -1;
+            if (i < items) {
+                const int r = row[j] = items < (1LL << 31) ? (int)((uint32_t)i / (uint32_t)touched_n) : (int)(i / touched_n);
+                const int v = v0 + list[(int)(i - (long long)r * touched_n)];
+                const char* in = in0 + (size_t)r * P.in_r * ES;
+                if (owns<VEC>(v, min(lead_in<DT, VEC>(in), P.V), P.V, v0, n) &&
+                    !(allowed0 && !(__ldg(allowed0 + (size_t)r * P.mwords + (v >> 5)) >> (v & 31) & 1u))) {
+                    at[j] = v;
+                    x[j] = load_one<DT>(in, v);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < TU; ++j)
+            if (at[j] >= 0) store_one<DT>(out0 + (size_t)row[j] * P.out_r * ES, at[j], touched(P, q, row[j], at[j], x[j]));
+    }
+}
+
+template <auto K>
+cudaError_t launch_chunks(LogitsParams& P, int sms, cudaStream_t st)
+{
+    // The run length whose grid leaves the fewest SM slots idle in its last wave; of equal ones the longest, which
+    // reads the history least often.
+    const auto smem = [&](int chunk) {
+        return ((size_t)chunk + 32 + (chunk + 32) / 32 + P.N) * 4 + ((size_t)chunk + 32 + P.N + P.nb + 1) / 2 * 4;
+    };
+    static int per_sm = 0;  // CTAs that the registers allow
+    if (per_sm == 0) {
+        cudaFuncAttributes a;
+        const cudaError_t e = cudaFuncGetAttributes(&a, K);
+        if (e != cudaSuccess) return e;
+        per_sm = max(1, min(2048 / NT, 65536 / (((a.numRegs + 7) / 8 * 8) * NT)));
+    }
+    int best = 1024;
+    double most = 0.0;
+    for (int chunk = 8192; chunk >= 1024; chunk /= 2) {
+        const long long per = (P.V + chunk - 1) / chunk, ctas = per * P.B;
+        const long long slots = (long long)sms * min(per_sm, (int)(220000 / (smem(chunk) + 6144)));
+        if (slots < 1) continue;
+        const double full = (double)P.V * P.B / ((double)chunk * ((ctas + slots - 1) / slots * slots));
+        if (full > 1.02 * most) {
+            most = full;
+            best = chunk;
+        }
+    }
+    P.chunk = best;
+    const size_t bytes = smem(best);
+    const cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    K<<<dim3((unsigned)((P.V + best - 1) / best), (unsigned)P.B), NT, bytes, st>>>(P);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -211,23 +403,13 @@ __global__ void __launch_bounds__(NT) process_logits_kernel(LogitsParams P)
 cudaError_t launch_process_logits(LogitsParams& P, int dtype, int sms, cudaStream_t st)
 {
     const size_t es = dtype == DT_BF16 ? 2 : 4;
-    const int vmax = 16 / (int)es;
-    const bool vec = P.V % vmax == 0 && P.in_b % vmax == 0 && P.in_r % vmax == 0 && P.out_b % vmax == 0 &&
-                     P.out_r % vmax == 0 && reinterpret_cast<uintptr_t>(P.logits) % 16 == 0 &&
-                     reinterpret_cast<uintptr_t>(P.out) % 16 == 0;
-    // longer runs read the history less often; shorter ones give a small batch more CTAs
-    P.chunk = 4096;
-    while (P.chunk > 1024 && (long long)P.B * ((P.V + P.chunk - 1) / P.chunk) < 2LL * sms) P.chunk /= 2;
-    const dim3 grid((unsigned)((P.V + P.chunk - 1) / P.chunk), (unsigned)P.B);
-    const size_t smem = (size_t)P.chunk * 4 * (P.nb ? 2 : 1);
-    if (dtype == DT_BF16) {
-        if (vec) process_logits_kernel<DT_BF16, 8><<<grid, NT, smem, st>>>(P);
-        else process_logits_kernel<DT_BF16, 1><<<grid, NT, smem, st>>>(P);
-    } else {
-        if (vec) process_logits_kernel<DT_F32, 4><<<grid, NT, smem, st>>>(P);
-        else process_logits_kernel<DT_F32, 1><<<grid, NT, smem, st>>>(P);
-    }
-    return cudaGetLastError();
+    // vectors need every row of the output to lie on its 16-byte boundaries as its input does
+    const auto off = [&](int64_t a, int64_t b) { return (a - b) * (int64_t)es % 16 == 0; };
+    const bool vec = (reinterpret_cast<uintptr_t>(P.logits) - reinterpret_cast<uintptr_t>(P.out)) % 16 == 0 &&
+                     (P.B == 1 || off(P.in_b, P.out_b)) && (P.R == 1 || off(P.in_r, P.out_r));
+    if (dtype == DT_BF16)
+        return vec ? launch_chunks<process_logits_kernel<DT_BF16, 8>>(P, sms, st) : launch_chunks<process_logits_kernel<DT_BF16, 1>>(P, sms, st);
+    return vec ? launch_chunks<process_logits_kernel<DT_F32, 4>>(P, sms, st) : launch_chunks<process_logits_kernel<DT_F32, 1>>(P, sms, st);
 }
 
 }  // namespace sv

@@ -65,6 +65,7 @@ __device__ __forceinline__ uint16_t e4m3x2_from(float lo, float hi)
 // ---------------------------------------------------------------- logit processing
 
 constexpr int LOGITS_MAX_NODES = 4096;
+constexpr int LOGITS_MAX_BIASES = 16384;
 
 struct LogitsParams {
     const void* logits;
@@ -129,6 +130,12 @@ cudaError_t launch_cache_read(const CacheReadParams& P, int dtype, int sms, cuda
 constexpr int ATTN_MAX_ROWS = 256;   // rows of a round (T)
 constexpr int ATTN_MAX_CTAS = 1024;  // CTAs of one launch: the workspace holds two parts for each
 
+// a group of rows that starts in one streaming CTA and ends in a later one (parts == 0: none starts there)
+struct AttnJoin {
+    int parts, b, h, rt, rows;
+    int pad[3];
+};
+
 struct AttnParams {
     const void* q;                 // [B, T, Hq, D]
     int64_t qb, qt, qh;
@@ -146,7 +153,8 @@ struct AttnParams {
     void* out;                     // [B, T, Hq, D]
     float* lse;                    // [B, T, Hq] or null
     int32_t* row_status;
-    float* parts;                  // workspace: partial results
+    AttnJoin* joins;               // workspace: [CTAs]
+    float* parts;                  // workspace: partial results, two slots per CTA
     int B, T, Hq, Hkv, G, D, page, pages, table_width;
     int page_shift;
     int R;                         // T * G rows of a key/value head

@@ -53,7 +53,7 @@ spec_status process_logits(const void* logits, void* out, spec_dtype dtype, int 
 {
     if (B < 0 || R < 1 || V < 1 || N < 0 || H < 0 || nb < 0) return SPEC_ERR_INVALID_ARG;
     if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
-    if (B > 65535 || N > LOGITS_MAX_NODES || R > N + 1 || H > (1 << 29)) return SPEC_ERR_INVALID_ARG;
+    if (B > 65535 || N > LOGITS_MAX_NODES || R > N + 1 || H > (1 << 28) || nb > LOGITS_MAX_BIASES) return SPEC_ERR_INVALID_ARG;
     if (V > (1 << 30)) return SPEC_ERR_INVALID_ARG;
     if (B == 0) return SPEC_OK;
     const size_t es = dtype_size(dtype);
@@ -240,7 +240,8 @@ spec_status verify_attention(const void* q, const int64_t* q_strides, const void
     P.out = out;
     P.lse = lse;
     P.row_status = row_status;
-    P.parts = static_cast<float*>(workspace);
+    P.joins = static_cast<AttnJoin*>(workspace);
+    P.parts = reinterpret_cast<float*>(P.joins + ATTN_MAX_CTAS);
     P.B = B;
     P.T = T;
     P.Hq = Hq;
