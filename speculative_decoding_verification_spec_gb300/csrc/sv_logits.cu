@@ -17,6 +17,8 @@
 // text's words crowd into few runs (frequent tokens have low numbers), and in the copy loop each of them would hold up
 // the 31 other lanes of its warp, row after row.  Rows need not start on a 16-byte boundary (an odd V): each row's
 // vectors start at its own first boundary, the few entries before it and after its last whole vector go one by one.
+#include <type_traits>
+
 #include "sv_round.cuh"
 
 namespace sv {
@@ -27,7 +29,7 @@ constexpr uint32_t LW_SEEN = 0x80000000u;   // the entry is in the prompt
 constexpr uint32_t LW_DRAFT = 0x40000000u;  // a drafted token names the entry
 constexpr uint32_t LW_BIAS = 0x20000000u;   // a bias names the entry
 constexpr uint32_t LW_COUNT = 0x1fffffffu;
-constexpr int LU = 8;                       // vectors in flight per thread
+constexpr int LU = 4;                       // vectors in flight per thread
 constexpr int HU = 8;                       // history tokens in flight per thread
 constexpr int LMASK = 64;                   // drafted tokens of a run whose paths are kept as bit masks
 constexpr int LMASK_ROWS = 512;             // and the rows that this is done for
@@ -66,6 +68,35 @@ __device__ __forceinline__ void store_one(char* row, int v, float x)
 {
     if constexpr (DT == DT_BF16) reinterpret_cast<unsigned short*>(row)[v] = (unsigned short)pack_bf16(x, 0.0f);
     else reinterpret_cast<float*>(row)[v] = x;
+}
+
+// four mask bits as the top bits of four bytes, which a byte permutation can then spread
+__device__ __forceinline__ uint32_t spread4(uint32_t bits) { return (bits & 15u) * 0x10204080u & 0x80808080u; }
+
+// a vector with -inf where its entry's bit is not set
+template <int DT>
+__device__ __forceinline__ uint4 masked_vec(uint4 w, uint32_t ok)
+{
+    const auto pick = [](uint32_t x, uint32_t keep, uint32_t inf) { return (x & keep) | (inf & ~keep); };
+    const auto sign = [](uint32_t y, uint32_t sel) {
+        uint32_t r;
+        asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(y), "r"(sel));  // selector nibbles 8 + j: byte j's top bit, eight times
+        return r;
+    };
+    if constexpr (DT == DT_BF16) {
+        const uint32_t a = spread4(ok), b = spread4(ok >> 4);
+        w.x = pick(w.x, sign(a, 0x9988), 0xff80ff80u);
+        w.y = pick(w.y, sign(a, 0xbbaa), 0xff80ff80u);
+        w.z = pick(w.z, sign(b, 0x9988), 0xff80ff80u);
+        w.w = pick(w.w, sign(b, 0xbbaa), 0xff80ff80u);
+    } else {
+        const uint32_t a = spread4(ok);
+        w.x = pick(w.x, sign(a, 0x8888), 0xff800000u);
+        w.y = pick(w.y, sign(a, 0x9999), 0xff800000u);
+        w.z = pick(w.z, sign(a, 0xaaaa), 0xff800000u);
+        w.w = pick(w.w, sign(a, 0xbbbb), 0xff800000u);
+    }
+    return w;
 }
 
 // what a CTA knows of its request and run
@@ -143,8 +174,8 @@ __device__ __forceinline__ int lead_in(const char* row)  // entries before the r
 }
 
 // VEC: elements of a 16-byte vector, or 1 where a row of the output is not aligned as its input is
-template <int DT, int VEC>
-__global__ void __launch_bounds__(NT) process_logits_kernel(LogitsParams P)
+template <int DT, int VEC, bool MASK>
+__global__ void __launch_bounds__(NT, 5) process_logits_kernel(LogitsParams P)
 {
     constexpr size_t ES = DT == DT_BF16 ? 2 : 4;
     extern __shared__ uint32_t smem[];
@@ -167,7 +198,7 @@ __global__ void __launch_bounds__(NT) process_logits_kernel(LogitsParams P)
     const int t = threadIdx.x;
     const char* in0 = reinterpret_cast<const char*>(P.logits) + (size_t)b * P.in_b * ES;
     char* out0 = reinterpret_cast<char*>(P.out) + (size_t)b * P.out_b * ES;
-    const uint32_t* allowed0 = P.allowed ? P.allowed + (size_t)b * P.R * P.mwords : nullptr;
+    const uint32_t* allowed0 = MASK ? P.allowed + (size_t)b * P.R * P.mwords : nullptr;
     for (int i = t; i < room + room / 32; i += NT) smem[i] = 0u;
     if (t == 0) ndraft = 0, nentry = 0, nbias = 0, nlist = 0, bad = 0;
     if (t < LMASK) same[t] = 0;
@@ -253,10 +284,10 @@ __global__ void __launch_bounds__(NT) process_logits_kernel(LogitsParams P)
     // the copy, with the mask
     if constexpr (VEC == 1) {
         for (int r = 0; r < P.R; ++r) {
-            const uint32_t* allowed = allowed0 ? allowed0 + (size_t)r * P.mwords : nullptr;
+            const uint32_t* allowed = MASK ? allowed0 + (size_t)r * P.mwords : nullptr;
             for (int v = v0 + t; v < v0 + n; v += NT) {
                 float x = load_one<DT>(in0 + (size_t)r * P.in_r * ES, v);
-                if (allowed && !(__ldg(allowed + (v >> 5)) >> (v & 31) & 1u)) x = NEG_INF;
+                if (MASK && !(__ldg(allowed + (v >> 5)) >> (v & 31) & 1u)) x = NEG_INF;
                 store_one<DT>(out0 + (size_t)r * P.out_r * ES, v, x);
             }
         }
@@ -279,7 +310,7 @@ __global__ void __launch_bounds__(NT) process_logits_kernel(LogitsParams P)
                     if (v < v0 + n && v + VEC <= P.V) {
                         to[j] = out0 + ((size_t)r * P.out_r + v) * ES;
                         w[j] = __ldcs(reinterpret_cast<const uint4*>(in + (size_t)v * ES));
-                        if (allowed0) {
+                        if constexpr (MASK) {
                             const uint32_t* a = allowed0 + (size_t)r * P.mwords + (v >> 5);
                             ok[j] = __ldg(a) >> (v & 31);
                             if ((v & 31) + VEC > 32) ok[j] |= __ldg(a + 1) << (32 - (v & 31));
@@ -295,17 +326,8 @@ __global__ void __launch_bounds__(NT) process_logits_kernel(LogitsParams P)
 #pragma unroll
             for (int j = 0; j < LU; ++j) {
                 if (!to[j]) continue;
-                uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (DT == DT_BF16) {
-                        if (!(ok[j] >> (2 * e) & 1u)) u[e] = (u[e] & 0xffff0000u) | 0xff80u;
-                        if (!(ok[j] >> (2 * e + 1) & 1u)) u[e] = (u[e] & 0xffffu) | 0xff800000u;
-                    } else {
-                        if (!(ok[j] >> e & 1u)) u[e] = 0xff800000u;
-                    }
-                }
-                __stcs(reinterpret_cast<uint4*>(to[j]), make_uint4(u[0], u[1], u[2], u[3]));
+                if constexpr (MASK) w[j] = masked_vec<DT>(w[j], ok[j]);
+                __stcs(reinterpret_cast<uint4*>(to[j]), w[j]);
             }
         }
         // the entries before a row's first boundary and after its last whole vector: at most VEC - 1 each
@@ -316,7 +338,7 @@ __global__ void __launch_bounds__(NT) process_logits_kernel(LogitsParams P)
             const int v = e < VEC ? e : s + ((P.V - s) & ~(VEC - 1)) + e - VEC;
             if ((e < VEC ? v < s : v < P.V) && v >= v0 && v < v0 + n) {
                 float x = load_one<DT>(row, v);
-                if (allowed0 && !(__ldg(allowed0 + (size_t)r * P.mwords + (v >> 5)) >> (v & 31) & 1u)) x = NEG_INF;
+                if (MASK && !(__ldg(allowed0 + (size_t)r * P.mwords + (v >> 5)) >> (v & 31) & 1u)) x = NEG_INF;
                 store_one<DT>(out0 + (size_t)r * P.out_r * ES, v, x);
             }
         }
@@ -351,7 +373,7 @@ __global__ void __launch_bounds__(NT) process_logits_kernel(LogitsParams P)
                 const int v = v0 + list[(int)(i - (long long)r * touched_n)];
                 const char* in = in0 + (size_t)r * P.in_r * ES;
                 if (owns<VEC>(v, min(lead_in<DT, VEC>(in), P.V), P.V, v0, n) &&
-                    !(allowed0 && !(__ldg(allowed0 + (size_t)r * P.mwords + (v >> 5)) >> (v & 31) & 1u))) {
+                    !(MASK && !(__ldg(allowed0 + (size_t)r * P.mwords + (v >> 5)) >> (v & 31) & 1u))) {
                     at[j] = v;
                     x[j] = load_one<DT>(in, v);
                 }
@@ -363,11 +385,11 @@ __global__ void __launch_bounds__(NT) process_logits_kernel(LogitsParams P)
     }
 }
 
-template <auto K>
+template <auto K, int VEC>
 cudaError_t launch_chunks(LogitsParams& P, int sms, cudaStream_t st)
 {
     // The run length whose grid leaves the fewest SM slots idle in its last wave; of equal ones the longest, which
-    // reads the history least often.
+    // reads the history least often.  At least one vector per thread.
     const auto smem = [&](int chunk) {
         return ((size_t)chunk + 32 + (chunk + 32) / 32 + P.N) * 4 + ((size_t)chunk + 32 + P.N + P.nb + 1) / 2 * 4;
     };
@@ -378,9 +400,10 @@ cudaError_t launch_chunks(LogitsParams& P, int sms, cudaStream_t st)
         if (e != cudaSuccess) return e;
         per_sm = max(1, min(2048 / NT, 65536 / (((a.numRegs + 7) / 8 * 8) * NT)));
     }
-    int best = 1024;
+    int best = NT * (VEC == 1 ? 4 : VEC);
     double most = 0.0;
-    for (int chunk = 8192; chunk >= 1024; chunk /= 2) {
+    constexpr int LEAST = NT * (VEC == 1 ? 4 : VEC);
+    for (int chunk = 8192; chunk >= LEAST; chunk /= 2) {
         const long long per = (P.V + chunk - 1) / chunk, ctas = per * P.B;
         const long long slots = (long long)sms * min(per_sm, (int)(220000 / (smem(chunk) + 6144)));
         if (slots < 1) continue;
@@ -407,9 +430,16 @@ cudaError_t launch_process_logits(LogitsParams& P, int dtype, int sms, cudaStrea
     const auto off = [&](int64_t a, int64_t b) { return (a - b) * (int64_t)es % 16 == 0; };
     const bool vec = (reinterpret_cast<uintptr_t>(P.logits) - reinterpret_cast<uintptr_t>(P.out)) % 16 == 0 &&
                      (P.B == 1 || off(P.in_b, P.out_b)) && (P.R == 1 || off(P.in_r, P.out_r));
+    const auto go = [&](auto dt, auto v, auto mask) {
+        return launch_chunks<process_logits_kernel<dt.value, v.value, mask.value>, v.value>(P, sms, st);
+    };
+    const auto with = [&](auto dt, auto v) { return P.allowed ? go(dt, v, std::true_type{}) : go(dt, v, std::false_type{}); };
+    using std::integral_constant;
     if (dtype == DT_BF16)
-        return vec ? launch_chunks<process_logits_kernel<DT_BF16, 8>>(P, sms, st) : launch_chunks<process_logits_kernel<DT_BF16, 1>>(P, sms, st);
-    return vec ? launch_chunks<process_logits_kernel<DT_F32, 4>>(P, sms, st) : launch_chunks<process_logits_kernel<DT_F32, 1>>(P, sms, st);
+        return vec ? with(integral_constant<int, DT_BF16>{}, integral_constant<int, 8>{})
+                   : with(integral_constant<int, DT_BF16>{}, integral_constant<int, 1>{});
+    return vec ? with(integral_constant<int, DT_F32>{}, integral_constant<int, 4>{})
+               : with(integral_constant<int, DT_F32>{}, integral_constant<int, 1>{});
 }
 
 }  // namespace sv
