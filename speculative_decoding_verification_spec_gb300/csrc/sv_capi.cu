@@ -16,6 +16,7 @@ namespace sv {
 KernelEvents g_kernel_events;
 // polls of a ring or segment wait before it gives up (spec_set_wait_limit); read at every call
 static int g_wait_limit = MBAR_SPIN_LIMIT;
+int wait_limit_polls() { return g_wait_limit; }
 // tree_verify_sample's cluster size when forced (spec_set_tree_sample_cluster), else 0
 static int g_ts_cluster = 0;
 

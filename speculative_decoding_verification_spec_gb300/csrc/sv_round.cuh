@@ -128,7 +128,8 @@ cudaError_t launch_cache_read(const CacheReadParams& P, int dtype, int sms, cuda
 // ---------------------------------------------------------------- attention
 
 constexpr int ATTN_MAX_ROWS = 256;   // rows of a round (T)
-constexpr int ATTN_MAX_CTAS = 1024;  // CTAs of one launch: the workspace holds two parts for each
+constexpr int ATTN_MAX_CTAS = 1024;  // CTAs of one launch (few rows): the workspace holds two parts for each
+constexpr int ATTN_MAX_TC_CTAS = 256;  // and of the kernel for many rows
 
 // a group of rows that starts in one streaming CTA and ends in a later one (parts == 0: none starts there)
 struct AttnJoin {
@@ -160,7 +161,11 @@ struct AttnParams {
     int R;                         // T * G rows of a key/value head
     int RT;                        // row tiles
     float scale;
+    int wait_limit;                // polls of a wait before it gives up (ROW_TIMEOUT)
 };
+
+// polls of a bounded wait (spec_set_wait_limit)
+int wait_limit_polls();
 
 size_t attn_workspace_bytes(int D);
 cudaError_t launch_attention(AttnParams& P, int dtype, int sms, cudaStream_t st);

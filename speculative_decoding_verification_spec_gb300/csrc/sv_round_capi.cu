@@ -254,6 +254,7 @@ spec_status verify_attention(const void* q, const int64_t* q_strides, const void
     P.table_width = table_width;
     P.R = T * P.G;
     P.scale = scale;
+    P.wait_limit = wait_limit_polls();
     const cudaError_t e = launch_attention(P, (int)dtype, round_sm_count(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
