@@ -675,7 +675,7 @@ cudaError_t launch_attn_merge(const AttnParams& P, int dtype, int ctas, int MR, 
 
 size_t attn_workspace_bytes(int D)
 {
-    const size_t few = ATTN_MAX_CTAS * part_floats(16, D), many = ATTN_MAX_TC_CTAS * part_floats(160, D);
+    const size_t few = ATTN_MAX_CTAS * part_floats(16, D), many = ATTN_MAX_TC_CTAS * part_floats(128, D);
     return ATTN_MAX_CTAS * sizeof(AttnJoin) + 2 * (few > many ? few : many) * sizeof(float);
 }
 

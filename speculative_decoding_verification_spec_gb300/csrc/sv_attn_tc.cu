@@ -1,13 +1,13 @@
 // sv_attn_tc.cu -- verify_attention for many rows, on the tensor cores (tcgen05).
 //
 // The arithmetic is that of sv_attn.cu: u_j = log2(e) s_j + e_j, weights 2^(u_j - m) against a lazily moved reference m,
-// o = sum p' c / sum p' 2^(-e).  Tokens lie on the 128 lanes of an accumulator and the rows of q, up to 160 of one
+// o = sum p' c / sum p' 2^(-e).  Tokens lie on the 128 lanes of an accumulator and the rows of q, up to 128 of one
 // key/value head, are its columns, so a tile costs what its rows cost, without padding to 128:
 //   S^T [128 tokens, rows] = K [128, D] Q^T:   the codes of K go from memory to the product as they are (e4m3 x e4m3);
 //       a row of q, scaled by a power of two to a largest element in [128, 256), is split into e4m3 terms that sum to it,
 //       two for bf16 (4 bits each, the residual's sign the ninth: exact for elements above 2^-10 of the largest, off by at
 //       most 2^-17 of it below) and three for halfs, whose products accumulate.
-//   O^T [D, rows] += V^T [D, 128] P^T:   halfs; two warps widen the codes of V into shared memory, and the weights are
+//   O^T [D, rows] += V^T [D, 128] P^T:   halfs; six warps widen the codes of V into shared memory, and the weights are
 //       rounded to halfs (half a step, 2^-11, under the output's own rounding).
 // The round's own rows come last, as tiles of their own: keys and values as halfs scaled by a power of two per token, and a
 // copy of q as halfs.
@@ -15,10 +15,12 @@
 // One CTA per SM works through an equal run of all groups' tiles (as in sv_attn.cu), with a role per warp:
 //   0      copies: the pages' codes by TMA into a ring of stages, the pages' scales beside them
 //   1      products: one lane issues them; S is double-buffered, so S of the next tile runs under this tile's softmax
-//   2, 3   values to halfs
-//   4 - 11 softmax, two groups of four warps; a thread is a token, a group takes half of the columns.  The weights are taken
-//          against the reference as it stands; only when one passes 2^15 (the first tile of a group, and rarely after) does the
-//          group find the columns' maxima, move the reference, rescale its part of O^T and repeat the tile.
+//   2 - 7  values to halfs
+//   8 - 19 softmax, three groups of four warps; a thread is a token, a group takes a third of the columns.  The sums l stay in
+//          tensor memory beside S^T and O^T, one per token lane and column, so a thread holds 16 columns at a time.  The
+//          weights are taken against the reference as it stands; only when one passes 2^15 (the first tile of a group, and
+//          rarely after) does the group find the columns' maxima, move the reference, rescale its part of O^T and l and
+//          repeat the tile.
 // Every wait on an mbarrier is bounded; when one runs out the CTA's remaining groups report SPEC_ROW_TIMEOUT.  Between named
 // barriers the threads of a softmax group never part: what a wait returned is agreed on before anyone acts on it.
 #include <cuda.h>
@@ -33,22 +35,24 @@ namespace sv {
 namespace {
 
 constexpr int TT = 128;          // tokens of a tile
-constexpr int TNT = 384;         // threads
-constexpr int SMW0 = 4;          // first softmax warp
-constexpr int MAXR = 160;        // rows of a group, columns of S^T: S twice and O within 512 columns
-constexpr int HALFR = MAXR / 2;  // columns of a softmax group
+constexpr int VW0 = 2, VWN = 6;  // warps that widen the values
+constexpr int SMW0 = 8, NG = 3;  // first softmax warp (a multiple of 4), groups of four softmax warps
+constexpr int TNT = (SMW0 + 4 * NG) * 32;
+constexpr int MAXR = 128;        // rows of a group: S^T twice, O^T and the sums l take four times as many columns
+constexpr int MAXC = (MAXR / 16 + NG - 1) / NG * 16;  // columns of a softmax group
 constexpr int MAXSTAGES = 6;
 constexpr float WINDOW = 15.0f;  // a weight may reach 2^WINDOW (the largest half is near 2^16)
 constexpr float HEAD = 7.0f;     // a moved reference leaves the maximum at 2^HEAD
 constexpr float FAR = 40.0f;     // log2 of a weight that the first pass keeps out of l: with the 2^74 of a scale it could soon
                                  // leave fp32's range
-constexpr size_t TC_SMEM = 216 * 1024;  // dynamic shared memory; the static arrays take the rest of the SM's 227 KB
+constexpr size_t TC_SMEM = 214 * 1024;  // dynamic shared memory; the static arrays take the rest of the SM's 227 KB
 
 struct TcParams {
     AttnParams A;
     int MR, RN;          // rows of a row tile; padded to a multiple of 16
     int stages, np, nv;  // ring stages; buffers of P and of the widened values (1 or 2)
     uint32_t o_p, o_v, o_stage, v_buf, p_buf;  // offsets in dynamic shared memory, sizes
+    bool qvec, kvec, vvec;  // rows that allow loads of D / 32 elements at once
     int wait_limit;
 };
 
@@ -87,21 +91,21 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
 // 16 columns of this warp's 32 lanes
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16])
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t addr, uint32_t (&r)[16])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
                    "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                  : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16])
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st16_nowait(uint32_t addr, const uint32_t (&r)[16])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
                  :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
                     "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ unsigned long long f2_mul(unsigned long long a, unsigned long long b)
@@ -130,11 +134,12 @@ struct Shared {
     float2 scale[MAXSTAGES][8];   // of the stage's pages: keys, values
     int status[MAXSTAGES];
     float4 fr[2][MAXR / 2];       // per pair of columns: factors, references; two copies, one being rewritten
-    float wmax[2][4][HALFR];      // column maxima (and sums of l) of the softmax warps
-    float fac[2][HALFR];
+    float wred[NG][4][MAXC];      // column maxima and sums of the softmax warps
+    float4 col[NG][MAXC];         // a moved reference's factors; the outputs' columns
+    float unseen[NG][MAXC];       // 1: no token of the group so far was seen by the column
     uint32_t mask[MAXR][4];       // round's rows: which tokens of the tile a column sees
     float fks[2][TT], fve[2][TT]; // round's rows: scale of the keys and exponent of the values, per token
-    int vbad[4][2];               // round's rows: a tile's values hold a NaN or an infinity, per warp
+    int vbad[4][VWN];               // round's rows: a tile's values hold a NaN or an infinity, per warp
     int fail;
     uint32_t tmem;
     Place place;
@@ -352,10 +357,55 @@ __device__ void role_mma(const TcParams& T, Shared& sh, const Place& at, uint32_
     (void)mbar_wait(&sh.done, 0, MBAR_SPIN_LIMIT);
 }
 
+__device__ __forceinline__ float warp_max(float x)
+{
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// byte offset of channel d of a row of q in a term's tile (swizzled over 128 or 64 bytes, a row)
+template <int D>
+__device__ __forceinline__ uint32_t q_off(int col, int d)
+{
+    return D == 128 ? col * 128 + (((d >> 4) ^ (col & 7)) << 4) + (d & 15) : col * 64 + (((d >> 4) ^ ((col >> 1) & 3)) << 4) + (d & 15);
+}
+
 // byte offset of channels d .. (within 8) of a token in a [token][64 channels] block of halfs, 128-byte swizzle
 __device__ __forceinline__ uint32_t half_off(int token, int d)
 {
     return (uint32_t)(d >> 6) * 16384u + token * 128u + ((((d & 63) >> 3) ^ (token & 7)) << 4) + (d & 7) * 2;
+}
+
+// EPL consecutive elements, in one load where `vec` says that every row allows it
+template <int DT, int EPL>
+__device__ __forceinline__ void load_run(const void* p, int64_t i, bool vec, float (&x)[EPL])
+{
+    uint32_t u[EPL / 2];
+    if (vec) {
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + i;
+        if constexpr (EPL == 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(q));
+            u[0] = v.x;
+            u[1] = v.y;
+        } else {
+            u[0] = __ldg(reinterpret_cast<const uint32_t*>(q));
+        }
+#pragma unroll
+        for (int k = 0; k < EPL / 2; ++k) {
+            if constexpr (DT == DT_BF16) {
+                x[2 * k] = bf16lo(u[k]);
+                x[2 * k + 1] = bf16hi(u[k]);
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
+                x[2 * k] = f.x;
+                x[2 * k + 1] = f.y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < EPL; ++k) x[k] = load_elem<DT>(p, i + k);
+    }
 }
 
 template <int DT, int D>
@@ -363,7 +413,7 @@ __device__ void role_values(const TcParams& T, Shared& sh, const Place& at, uint
 {
     const AttnParams& P = T.A;
     constexpr int KB = TT * D, CH = D / 16, EPL = D / 32;
-    const int ct = threadIdx.x - 64, w2 = ct >> 5, lane = ct & 31;
+    const int ct = threadIdx.x - VW0 * 32, wv = ct >> 5, lane = ct & 31;
     int it = 0;
     bool ok = true;
     for (Walk w(P, at); ok && w.more(); w.next(P)) {
@@ -377,53 +427,66 @@ __device__ void role_values(const TcParams& T, Shared& sh, const Place& at, uint
             if (!ok) break;
             if (tile < w.rq.ncache) {
                 const int valid = w.rq.len - tile * TT;
-#pragma unroll 4
-                for (int i = ct; i < TT * CH; i += 64) {
-                    const int tok = i / CH, ch = i % CH;
-                    uint4 x = *reinterpret_cast<const uint4*>(kb + KB + i * 16);
-                    if (tok >= valid) x = make_uint4(0, 0, 0, 0);  // whatever the slot holds
-                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t y[8];
+                constexpr int U = 3;
+                for (int i0 = ct; i0 < TT * CH; i0 += U * VWN * 32) {
+                    uint4 x[U];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        y[2 * k] = e4m3x2_to_half2((uint16_t)u[k]);
-                        y[2 * k + 1] = e4m3x2_to_half2((uint16_t)(u[k] >> 16));
+                    for (int q = 0; q < U; ++q) {
+                        const int i = i0 + q * VWN * 32;
+                        x[q] = make_uint4(0, 0, 0, 0);  // tokens past the length, whatever their slots hold
+                        if (i < TT * CH && i / CH < valid) x[q] = *reinterpret_cast<const uint4*>(kb + KB + i * 16);
                     }
-                    const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-                    // the two blocks of 64 channels start with opposite halves, so a quarter-warp's stores meet no bank twice
-                    const int f = ch >> 2;
-                    *reinterpret_cast<uint4*>(vb + half_off(tok, ch * 16 + 8 * f)) = f ? hi : lo;
-                    *reinterpret_cast<uint4*>(vb + half_off(tok, ch * 16 + 8 * (f ^ 1))) = f ? lo : hi;
+#pragma unroll
+                    for (int q = 0; q < U; ++q) {
+                        const int i = i0 + q * VWN * 32, tok = i / CH, ch = i % CH;
+                        if (i >= TT * CH) break;
+                        const uint32_t u[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+                        uint32_t y[8];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            y[2 * k] = e4m3x2_to_half2((uint16_t)u[k]);
+                            y[2 * k + 1] = e4m3x2_to_half2((uint16_t)(u[k] >> 16));
+                        }
+                        const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+                        // the two blocks of 64 channels start with opposite halves, so a quarter-warp's stores meet no
+                        // bank twice
+                        const int f = ch >> 2;
+                        *reinterpret_cast<uint4*>(vb + half_off(tok, ch * 16 + 8 * f)) = f ? hi : lo;
+                        *reinterpret_cast<uint4*>(vb + half_off(tok, ch * 16 + 8 * (f ^ 1))) = f ? lo : hi;
+                    }
                 }
             } else {
                 // the round's rows: keys into the stage, values into the buffer, scaled by a power of two per token
-                const int j0 = (tile - w.rq.ncache) * TT;
+                const int j0 = (tile - w.rq.ncache) * TT, live = P.kn ? min(max(w.rq.rows - j0, 0), TT) : 0;
+                for (int i = ct; i < TT * (D / 8); i += VWN * 32)  // tokens that are none: zero values
+                    if (i / (D / 8) >= live) *reinterpret_cast<uint4*>(vb + half_off(i / (D / 8), i % (D / 8) * 8)) = make_uint4(0, 0, 0, 0);
+                for (int i = ct; i < TT; i += VWN * 32)
+                    if (i >= live) sh.fks[it & 1][i] = 1.0f, sh.fve[it & 1][i] = 0.0f;
                 bool vbad = false;
-                for (int i = w2; i < TT; i += 2) {
-                    const int j = j0 + i;
-                    const bool live = P.kn && j < w.rq.rows;
+                for (int i = wv; i < live; i += VWN) {
+                    const int64_t j = j0 + i;
+                    float x[2][EPL];
+                    load_run<DT, EPL>(P.kn, w.b * P.kb + j * P.kt + w.h * P.kh + lane * EPL, T.kvec, x[0]);
+                    load_run<DT, EPL>(P.vn, w.b * P.vb + j * P.vt + w.h * P.vh + lane * EPL, T.vvec, x[1]);
 #pragma unroll
                     for (int which = 0; which < 2; ++which) {
-                        const void* src = which ? P.vn : P.kn;
-                        const int64_t off = which ? w.b * P.vb + j * P.vt + w.h * P.vh : w.b * P.kb + j * P.kt + w.h * P.kh;
-                        float x[EPL], amax = 0.0f;
+                        float amax = 0.0f;
                         bool fin = true;
 #pragma unroll
                         for (int k = 0; k < EPL; ++k) {
-                            x[k] = live ? load_elem<DT>(src, off + lane * EPL + k) : 0.0f;
-                            if (fabsf(x[k]) < __int_as_float(0x7f800000)) amax = fmaxf(amax, fabsf(x[k]));
-                            else fin = false, x[k] = 0.0f;
+                            if (fabsf(x[which][k]) < __int_as_float(0x7f800000)) amax = fmaxf(amax, fabsf(x[which][k]));
+                            else fin = false, x[which][k] = 0.0f;
                         }
                         fin = __all_sync(0xffffffffu, fin);
-#pragma unroll
-                        for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                        amax = warp_max(amax);
                         const int e = min(max(exponent_of(amax), CACHE_E_MIN), 126) - 14;
                         const float mul = exp2_int(-e);
                         uint8_t* to = (which ? vb : kb) + half_off(i, lane * EPL);
                         if constexpr (EPL == 4)
-                            *reinterpret_cast<uint2*>(to) = make_uint2(pack_half2(x[0] * mul, x[1] * mul), pack_half2(x[2] * mul, x[3] * mul));
+                            *reinterpret_cast<uint2*>(to) = make_uint2(pack_half2(x[which][0] * mul, x[which][1] * mul),
+                                                                       pack_half2(x[which][2] * mul, x[which][3] * mul));
                         else
-                            *reinterpret_cast<uint32_t*>(to) = pack_half2(x[0] * mul, x[1] * mul);
+                            *reinterpret_cast<uint32_t*>(to) = pack_half2(x[which][0] * mul, x[which][1] * mul);
                         if (which) vbad = vbad || !fin;
                         if (lane == 0) {
                             if (which) sh.fve[it & 1][i] = (float)e;
@@ -431,7 +494,7 @@ __device__ void role_values(const TcParams& T, Shared& sh, const Place& at, uint
                         }
                     }
                 }
-                if (lane == 0) sh.vbad[it & 3][w2] = vbad;
+                if (lane == 0) sh.vbad[it & 3][wv] = vbad;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -443,19 +506,34 @@ __device__ void role_values(const TcParams& T, Shared& sh, const Place& at, uint
     }
 }
 
+// v[c] over the warp's lanes, for 16 columns at once: half of the columns travel at each step.  Column lane / 2's result in v[0].
+template <class Op>
+__device__ __forceinline__ float reduce16(float (&v)[16], int lane, Op op)
+{
+#pragma unroll
+    for (int n = 8, bit = 16; n; n >>= 1, bit >>= 1) {
+        const bool up = lane & bit;
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+            const float send = up ? v[k] : v[k + n], keep = up ? v[k + n] : v[k];
+            v[k] = op(keep, __shfl_xor_sync(0xffffffffu, send, bit));
+        }
+    }
+    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+}
+
 template <int DT, int D>
 __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uint8_t* smem, uint32_t tmem)
 {
     const AttnParams& P = T.A;
-    constexpr int TERMS = DT == DT_BF16 ? 2 : 3;
+    constexpr int TERMS = DT == DT_BF16 ? 2 : 3, EPL = D / 32;
     const int wid = (threadIdx.x >> 5) - SMW0, g = wid >> 2, quad = wid & 3, lane = threadIdx.x & 31;
     const int tok = quad * 32 + lane;       // this thread's token of a tile, and its channel of O^T
     const int bar_id = 1 + g;
-    const int ca = ((T.RN / 16 + 1) / 2) * 16;           // columns of group 0
-    const int col0 = g ? ca : 0, cw = g ? T.RN - ca : ca;
-    const int nch = cw / 16;
+    const int chunks = T.RN / 16, ch0 = g * chunks / NG, nch = (g + 1) * chunks / NG - ch0;
+    const int col0 = ch0 * 16, cw = nch * 16;  // this group's columns
     const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);  // this warp's lanes
-    const uint32_t t_o = tl + 2 * T.RN + col0;
+    const uint32_t t_o = tl + 2 * T.RN + col0, t_l = t_o + T.RN;
     float4* const fr0 = &sh.fr[0][col0 / 2];
     float4* const fr1 = &sh.fr[1][col0 / 2];
     int it = 0, rb = 0;
@@ -465,62 +543,58 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
         w.open();
         int status = w.rq.status;
         bool vbad = false;
-        unsigned long long l2[HALFR / 2];
-#pragma unroll
-        for (int i = 0; i < HALFR / 2; ++i) l2[i] = 0ull;
 
         if (!dead) {
-            // ---- the rows of q as e4m3 terms; a warp takes every fourth column of its group
-            for (int c = quad; c < cw; c += 4) {
-                const int col = col0 + c, r = w.rt * T.MR + col, t = r / P.G;
-                const bool live = col < T.MR && r < P.R && t < w.rq.rows;
-                constexpr int EPL = D / 32;
-                float x[EPL], amax = 0.0f;
-                bool fin = true;
-                const int64_t off = live ? (int64_t)w.b * P.qb + (int64_t)t * P.qt + (int64_t)(w.h * P.G + r % P.G) * P.qh : 0;
+            // ---- the rows of q as e4m3 terms; a warp takes every fourth column of its group, four of them at a time
+            for (int c0 = quad; c0 < cw; c0 += 16) {
+                float x[4][EPL];
 #pragma unroll
-                for (int k = 0; k < EPL; ++k) {
-                    x[k] = live ? load_elem<DT>(P.q, off + lane * EPL + k) : 0.0f;
-                    fin = fin && fabsf(x[k]) < __int_as_float(0x7f800000);
-                    amax = fmaxf(amax, fabsf(x[k]));
-                }
-                fin = __all_sync(0xffffffffu, fin);
+                for (int i = 0; i < 4; ++i) {
+                    const int col = col0 + c0 + 4 * i, r = w.rt * T.MR + col, t = r / P.G;
 #pragma unroll
-                for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                const int e = fin ? min(max(7 - exponent_of(amax), -120), 126) : 0;
-                const float mul = exp2_int(e);
-                if (!fin) {
-#pragma unroll
-                    for (int k = 0; k < EPL; ++k) x[k] = 0.0f;
+                    for (int k = 0; k < EPL; ++k) x[i][k] = 0.0f;
+                    if (c0 + 4 * i < cw && col < T.MR && r < P.R && t < w.rq.rows)
+                        load_run<DT, EPL>(P.q, (int64_t)w.b * P.qb + (int64_t)t * P.qt + (int64_t)(w.h * P.G + r % P.G) * P.qh + lane * EPL,
+                                          T.qvec, x[i]);
                 }
 #pragma unroll
-                for (int k = 0; k < EPL; ++k) x[k] *= mul;
-                const int d = lane * EPL;
-                const uint32_t at_q = D == 128 ? col * 128 + (((d >> 4) ^ (col & 7)) << 4) + (d & 15)
-                                               : col * 64 + (((d >> 4) ^ ((col >> 1) & 3)) << 4) + (d & 15);
+                for (int i = 0; i < 4; ++i) {
+                    const int c = c0 + 4 * i, col = col0 + c;
+                    if (c >= cw) break;
+                    float amax = 0.0f;
+                    bool fin = true;
 #pragma unroll
-                for (int q = 0; q < TERMS; ++q) {
-                    uint32_t code = 0;
-#pragma unroll
-                    for (int k = 0; k < EPL; k += 2) {
-                        const uint16_t c2 = e4m3x2_from(x[k], x[k + 1]);
-                        const uint32_t h2 = e4m3x2_to_half2(c2);
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                        x[k] -= f.x;
-                        x[k + 1] -= f.y;
-                        code |= (uint32_t)c2 << (8 * k);
+                    for (int k = 0; k < EPL; ++k) {
+                        fin = fin && fabsf(x[i][k]) < __int_as_float(0x7f800000);
+                        amax = fmaxf(amax, fabsf(x[i][k]));
                     }
-                    uint8_t* to = smem + (size_t)q * T.RN * D + at_q;
-                    if constexpr (EPL == 4) *reinterpret_cast<uint32_t*>(to) = code;
-                    else *reinterpret_cast<uint16_t*>(to) = (uint16_t)code;
-                }
-                if (lane == 0) {
-                    // a row of q with a NaN or an infinity has no scores
-                    const float F = fin ? P.scale * LOG2E * exp2_int(-e) : __int_as_float(0x7fc00000);
+                    fin = __all_sync(0xffffffffu, fin);
+                    amax = warp_max(amax);
+                    const int e = fin ? min(max(7 - exponent_of(amax), -120), 126) : 0;
+                    const float mul = exp2_int(e);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float* f = reinterpret_cast<float*>(k ? &fr1[c >> 1] : &fr0[c >> 1]);
-                        f[c & 1] = F;
+                    for (int k = 0; k < EPL; ++k) x[i][k] = fin ? x[i][k] * mul : 0.0f;
+                    const int d = lane * EPL;
+                    uint8_t* to = smem + q_off<D>(col, d);
+#pragma unroll
+                    for (int q = 0; q < TERMS; ++q) {
+                        uint32_t code = 0;
+#pragma unroll
+                        for (int k = 0; k < EPL; k += 2) {
+                            const uint16_t c2 = e4m3x2_from(x[i][k], x[i][k + 1]);
+                            const uint32_t h2 = e4m3x2_to_half2(c2);
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                            x[i][k] -= f.x;
+                            x[i][k + 1] -= f.y;
+                            code |= (uint32_t)c2 << (8 * k);
+                        }
+                        if constexpr (EPL == 4) *reinterpret_cast<uint32_t*>(to + (size_t)q * T.RN * D) = code;
+                        else *reinterpret_cast<uint16_t*>(to + (size_t)q * T.RN * D) = (uint16_t)code;
+                    }
+                    if (lane < 2) {
+                        // a row of q with a NaN or an infinity has no scores
+                        float* f = reinterpret_cast<float*>(lane ? &fr1[c >> 1] : &fr0[c >> 1]);
+                        f[c & 1] = fin ? P.scale * LOG2E * exp2_int(-e) : __int_as_float(0x7fc00000);
                         f[2 + (c & 1)] = 0.0f;
                     }
                 }
@@ -536,32 +610,27 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
             uint8_t* pb = smem + T.o_p + (it % T.np) * T.p_buf;
             bool fail = false;
             if (fresh) {
-                // a copy of q as halfs where P will be, and which rows each column sees
+                // q as halfs (the terms' sums) where P will be, and which rows each column sees
                 if (it >= 1) fail = !wait_warp(sh, &sh.pv[(it - 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit);
                 const int j0 = (tile - w.rq.ncache) * TT;
                 bool badp = false;
                 if (!fail) {
-                    for (int c = quad; c < cw; c += 4) {
-                        const int col = col0 + c, r = w.rt * T.MR + col, t = r / P.G;
-                        const bool live = col < T.MR && r < P.R && t < w.rq.rows;
-                        constexpr int EPL = D / 32;
-                        const int64_t off = live ? (int64_t)w.b * P.qb + (int64_t)t * P.qt + (int64_t)(w.h * P.G + r % P.G) * P.qh : 0;
-                        float x[EPL], amax = 0.0f;
+                    for (int i = tok; i < cw * (D / 8); i += 128) {
+                        const int col = col0 + i / (D / 8), d = i % (D / 8) * 8;
+                        alignas(16) __half2 x[4];
 #pragma unroll
-                        for (int k = 0; k < EPL; ++k) {
-                            x[k] = live ? load_elem<DT>(P.q, off + lane * EPL + k) : 0.0f;
-                            if (!(fabsf(x[k]) < __int_as_float(0x7f800000))) x[k] = 0.0f;  // its factor is NaN
-                            amax = fmaxf(amax, fabsf(x[k]));
+                        for (int q = 0; q < TERMS; ++q) {
+                            const uint2 code = *reinterpret_cast<const uint2*>(smem + (size_t)q * T.RN * D + q_off<D>(col, d));
+                            const uint32_t u[4] = {e4m3x2_to_half2((uint16_t)code.x), e4m3x2_to_half2((uint16_t)(code.x >> 16)),
+                                                   e4m3x2_to_half2((uint16_t)code.y), e4m3x2_to_half2((uint16_t)(code.y >> 16))};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const __half2 y = *reinterpret_cast<const __half2*>(&u[k]);
+                                x[k] = q ? __hadd2(x[k], y) : y;
+                            }
                         }
-#pragma unroll
-                        for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                        const float mul = exp2_int(min(max(7 - exponent_of(amax), -120), 126));
-                        const int d = lane * EPL;
-                        uint8_t* to = pb + (size_t)(d >> 6) * T.RN * 128 + col * 128 + ((((d & 63) >> 3) ^ (col & 7)) << 4) + (d & 7) * 2;
-                        if constexpr (EPL == 4)
-                            *reinterpret_cast<uint2*>(to) = make_uint2(pack_half2(x[0] * mul, x[1] * mul), pack_half2(x[2] * mul, x[3] * mul));
-                        else
-                            *reinterpret_cast<uint32_t*>(to) = pack_half2(x[0] * mul, x[1] * mul);
+                        *reinterpret_cast<uint4*>(pb + (size_t)(d >> 6) * T.RN * 128 + col * 128 + ((((d & 63) >> 3) ^ (col & 7)) << 4)) =
+                            *reinterpret_cast<const uint4*>(x);
                     }
                     if (tok < cw) {
                         const int r = w.rt * T.MR + col0 + tok, t = r / P.G;
@@ -602,47 +671,57 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
 
             fail = fail || !wait_warp(sh, &sh.sfull[it & 1], (it >> 1) & 1, T.wait_limit);
             if (!fresh && it >= T.np) fail = fail || !wait_warp(sh, &sh.pv[(it - T.np) & 1], ((it - T.np) >> 1) & 1, T.wait_limit);
-            float ks = 0.0f, ve = 0.0f;
-            bool okt = false, partial = false;
-            float vmax = NEG_INF;
+            float ks = 1.0f, ve = 0.0f;
+            bool okt = false, partial = true;
             const uint32_t ts = tl + (it & 1) * T.RN + col0;
             if (!fail) {
                 tc_fence_after();
                 if (!fresh) {
-                    const int s = it % T.stages;
-                    const float2 sc = sh.scale[s][tok >> P.page_shift];
-                    ks = sc.x;
-                    ve = (float)exponent_of(sc.y);
-                    const int left = w.rq.len - tile * TT;
+                    const int s = it % T.stages, left = w.rq.len - tile * TT;
                     partial = left < TT;
                     okt = tok < left;
-                    if (!okt) ks = 1.0f, ve = 0.0f;
+                    if (okt) {
+                        const float2 sc = sh.scale[s][tok >> P.page_shift];
+                        ks = sc.x;
+                        ve = (float)exponent_of(sc.y);
+                    }
                     status = max(status, sh.status[s]);
                 } else {
                     ks = sh.fks[it & 1][tok];
                     ve = sh.fve[it & 1][tok];
-                    partial = true;
-                    vbad = vbad || sh.vbad[it & 3][0] || sh.vbad[it & 3][1];
+#pragma unroll
+                    for (int k = 0; k < VWN; ++k) vbad = vbad || sh.vbad[it & 3][k];
                 }
             }
             const float inv = exp2_int(min(max(-(int)ve, -126), 127));
             const unsigned long long ks2 = f2_pack(ks, ks), ve2 = f2_pack(ve, ve), inv2 = f2_pack(inv, inv);
-            // which columns see this thread's token
-            const auto sees = [&](int c) {
-                return fresh ? (sh.mask[col0 + c][quad] >> lane & 1u) != 0 : okt;
+            // which of 16 columns see this thread's token
+            const auto seen16 = [&](int ch) -> uint32_t {
+                if (!fresh) return okt ? 0xffffu : 0u;
+                uint32_t m = 0;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) m |= (sh.mask[col0 + ch * 16 + j][quad] >> lane & 1u) << j;
+                return m;
             };
             // A pass over the tile: weights to shared memory, their sums to l.  The first pass goes by the reference as it
             // stands.  Where that turns out too low the sums are rescaled, this pass's share with them, and a second
             // one repeats the weights; it adds to l only what the first left out because it would have passed fp32's range.
+            float vmax = NEG_INF;
             const auto weights = [&](auto again) {
                 const float4* fr = rb ? fr1 : fr0;
                 const float4* old = rb ? fr0 : fr1;
+#pragma unroll 1
+                for (int ch = 0; ch < nch; ++ch) {
+                    uint32_t s[16], l[16], h[8];
+                    tmem_ld16_nowait(ts + ch * 16, s);
+                    if (again.value && first) {
 #pragma unroll
-                for (int ch = 0; ch < HALFR / 16; ++ch) {
-                    if (ch >= nch) break;
-                    uint32_t s[16], h[8];
-                    unsigned long long p2[8];
-                    tmem_ld16(ts + ch * 16, s);
+                        for (int j = 0; j < 16; ++j) l[j] = 0u;
+                    } else {
+                        tmem_ld16_nowait(t_l + ch * 16, l);
+                    }
+                    const uint32_t see = partial ? seen16(ch) : 0xffffu;
+                    tmem_wait_ld();
                     float top = NEG_INF;
                     unsigned far = 0;  // second pass: elements that the first left out
 #pragma unroll
@@ -657,45 +736,42 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
                             f2_unpack(f2_fma(x, ks2, f2_add(ve2, f2_pack(-o.z, -o.w))), c, d);
                             far |= (unsigned)(c > FAR) << (2 * j) | (unsigned)(d > FAR) << (2 * j + 1);
                         }
-                        if (partial) {
-                            a = sees(ch * 16 + 2 * j) ? a : NEG_INF;
-                            b = sees(ch * 16 + 2 * j + 1) ? b : NEG_INF;
-                        }
-                        top = fmaxf(top, fmaxf(a, b));
                         s[2 * j] = __float_as_uint(a);
                         s[2 * j + 1] = __float_as_uint(b);
-                        a = ex2(a);
-                        b = ex2(b);
-                        p2[j] = f2_pack(a, b);
-                        h[j] = pack_half2(a, b);
                     }
+                    if (partial) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) s[j] = see >> j & 1u ? s[j] : __float_as_uint(NEG_INF);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) top = fmaxf(top, __uint_as_float(s[j]));
                     vmax = fmaxf(vmax, top);
                     const bool all = again.value ? first : !__any_sync(0xffffffffu, top > FAR);
-                    if (all) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) l2[ch * 8 + j] = f2_fma(p2[j], inv2, l2[ch * 8 + j]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float a, b;
-                            f2_unpack(p2[j], a, b);
+                    for (int j = 0; j < 8; ++j) {
+                        float a = ex2(__uint_as_float(s[2 * j])), b = ex2(__uint_as_float(s[2 * j + 1]));
+                        h[j] = pack_half2(a, b);
+                        if (!all) {
                             if (again.value ? !(far >> (2 * j) & 1u) : __uint_as_float(s[2 * j]) > FAR) a = 0.0f;
                             if (again.value ? !(far >> (2 * j + 1) & 1u) : __uint_as_float(s[2 * j + 1]) > FAR) b = 0.0f;
-                            l2[ch * 8 + j] = f2_fma(f2_pack(a, b), inv2, l2[ch * 8 + j]);
                         }
+                        float c, d;
+                        f2_unpack(f2_fma(f2_pack(a, b), inv2, f2_pack(__uint_as_float(l[2 * j]), __uint_as_float(l[2 * j + 1]))), c, d);
+                        l[2 * j] = __float_as_uint(c);
+                        l[2 * j + 1] = __float_as_uint(d);
                     }
+                    tmem_st16_nowait(t_l + ch * 16, l);
                     const int col = col0 + ch * 16;
                     uint8_t* row = pb + (size_t)(col >> 6) * 16384 + tok * 128;
                     const int unit = (col & 63) >> 3;
                     *reinterpret_cast<uint4*>(row + ((unit ^ (tok & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                     *reinterpret_cast<uint4*>(row + (((unit + 1) ^ (tok & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
                 }
+                tmem_wait_st();
+                fence_proxy_async_smem();
             };
             // the first tile of a group has no reference yet
-            if (!fail && !first) {
-                weights(std::false_type{});
-                fence_proxy_async_smem();
-            }
+            if (!fail && !first) weights(std::false_type{});
             if (group_any(bar_id, fail || first || vmax > WINDOW)) {
                 if (group_any(bar_id, fail)) {
                     dead = true;
@@ -704,18 +780,20 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
                 // the columns' maxima over the tile
                 const float4* fr = rb ? fr1 : fr0;
                 float4* to = rb ? fr0 : fr1;
+#pragma unroll 1
                 for (int ch = 0; ch < nch; ++ch) {
                     uint32_t s[16];
-                    tmem_ld16(ts + ch * 16, s);
+                    float v[16];
+                    tmem_ld16_nowait(ts + ch * 16, s);
+                    const uint32_t see = seen16(ch);
+                    tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const float F = reinterpret_cast<const float*>(&fr[ch * 8 + (j >> 1)])[j & 1];
-                        float x = fmaf(__uint_as_float(s[j]) * F, ks, ve);
-                        x = sees(ch * 16 + j) ? x : NEG_INF;
-#pragma unroll
-                        for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                        if (lane == 0) sh.wmax[g][quad][ch * 16 + j] = x;
+                        v[j] = see >> j & 1u ? fmaf(__uint_as_float(s[j]) * F, ks, ve) : NEG_INF;
                     }
+                    const float m = reduce16(v, lane, [](float a, float b) { return fmaxf(a, b); });
+                    if (!(lane & 1)) sh.wred[g][quad][ch * 16 + (lane >> 1)] = m;
                 }
                 // O^T of the tile before has to be whole before it is rescaled
                 const bool okp = first || wait_warp(sh, &sh.pv[(it - 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit);
@@ -724,44 +802,37 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
                     break;
                 }
                 if (tok < cw) {
-                    float top = sh.wmax[g][0][tok];
-#pragma unroll
-                    for (int k = 1; k < 4; ++k) top = fmaxf(top, sh.wmax[g][k][tok]);
-                    // the reference of a column without a token yet is 0, which its zero sums do not feel
+                    const float top = fmaxf(fmaxf(sh.wred[g][0][tok], sh.wred[g][1][tok]), fmaxf(sh.wred[g][2][tok], sh.wred[g][3][tok]));
+                    // a column that has seen nothing yet keeps the reference 0, which its zero sums do not feel
                     const float* f = reinterpret_cast<const float*>(&fr[tok >> 1]);
                     float* n = reinterpret_cast<float*>(&to[tok >> 1]);
-                    const float was = f[2 + (tok & 1)];
-                    const bool none = first || sh.fac[g][tok] == -1.0f;
+                    const float was = first ? 0.0f : f[2 + (tok & 1)];
+                    const bool none = first || sh.unseen[g][tok] != 0.0f;
                     const bool move = none ? top > NEG_INF : top > was + WINDOW;
-                    const float now = move ? top - HEAD : (first ? 0.0f : was);
+                    const float now = move ? top - HEAD : was;
                     n[tok & 1] = f[tok & 1];
                     n[2 + (tok & 1)] = now;
-                    // factor of the sums so far; -1: still no token
-                    sh.wmax[g][0][tok] = none ? 0.0f : move ? ex2(was - now) : 1.0f;
-                    sh.fac[g][tok] = none && !move ? -1.0f : 0.0f;
+                    sh.col[g][tok].x = move && !none ? ex2(was - now) : 1.0f;  // of the sums so far
+                    sh.unseen[g][tok] = none && !move ? 1.0f : 0.0f;
                 }
                 group_sync(bar_id);
                 rb ^= 1;
                 if (!first) {
                     tc_fence_after();
-#pragma unroll
-                    for (int ch = 0; ch < HALFR / 16; ++ch) {
-                        if (ch >= nch) break;
+#pragma unroll 1
+                    for (int ch = 0; ch < 2 * nch; ++ch) {
+                        const uint32_t a = ch < nch ? t_o + ch * 16 : t_l + (ch - nch) * 16;
+                        const float4* f = &sh.col[g][(ch < nch ? ch : ch - nch) * 16];
                         uint32_t o[16];
-                        tmem_ld16(t_o + ch * 16, o);
+                        tmem_ld16_nowait(a, o);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sh.wmax[g][0][ch * 16 + j]);
-                        tmem_st16(t_o + ch * 16, o);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float2 f = *reinterpret_cast<const float2*>(&sh.wmax[g][0][ch * 16 + 2 * j]);
-                            l2[ch * 8 + j] = f2_mul(l2[ch * 8 + j], f2_pack(f.x, f.y));
-                        }
+                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[j].x);
+                        tmem_st16_nowait(a, o);
                     }
+                    tmem_wait_st();
                 }
                 weights(std::true_type{});
-                fence_proxy_async_smem();
-                tc_fence_before();
                 group_sync(bar_id);
             }
             tc_fence_before();
@@ -779,70 +850,98 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
         }
         if (dead) status = ROW_TIMEOUT;
         else tc_fence_after();
-        float4* const fr = rb ? fr1 : fr0;
-        const AttnParams& A = P;
-        float* part = A.parts + ((size_t)blockIdx.x * 2 + (w.first && w.tile0 != 0 ? 0 : 1)) * part_floats(T.MR, D);
+        float* part = P.parts + ((size_t)blockIdx.x * 2 + (w.first && w.tile0 != 0 ? 0 : 1)) * part_floats(T.MR, D);
+        if (!dead) {
+#pragma unroll 1
+            for (int ch = 0; ch < nch; ++ch) {
+                uint32_t l[16];
+                float v[16];
+                tmem_ld16_nowait(t_l + ch * 16, l);
+                tmem_wait_ld();
 #pragma unroll
-        for (int ch = 0; ch < HALFR / 16; ++ch) {
-            if (ch >= nch) break;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                float a, b;
-                f2_unpack(l2[ch * 8 + (j >> 1)], a, b);
-                float x = j & 1 ? b : a;
-#pragma unroll
-                for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                if (lane == 0) sh.wmax[g][quad][ch * 16 + j] = x;
+                for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(l[j]);
+                const float x = reduce16(v, lane, [](float a, float b) { return a + b; });
+                if (!(lane & 1)) sh.wred[g][quad][ch * 16 + (lane >> 1)] = x;
             }
         }
         group_sync(bar_id);
+        if (tok < cw) {
+            // a column's row of the output (-1: none), and the factor of its sums
+            const int col = col0 + tok, r = w.rt * T.MR + col, t = r / P.G;
+            const float l = dead ? 0.0f : (sh.wred[g][0][tok] + sh.wred[g][1][tok]) + (sh.wred[g][2][tok] + sh.wred[g][3][tok]);
+            const float m = dead || sh.unseen[g][tok] != 0.0f ? NEG_INF : reinterpret_cast<const float*>(&(rb ? fr1 : fr0)[tok >> 1])[2 + (tok & 1)];
+            float4 c = make_float4(0.0f, __int_as_float(-1), __int_as_float(t), 0.0f);
+            if (col < T.MR && r < P.R) {
+                const size_t row = ((size_t)w.b * P.T + t) * P.Hq + w.h * P.G + r % P.G;
+                c.y = __int_as_float(t * P.Hq + w.h * P.G + r % P.G);
+                const bool live = t < w.rq.rows && l != 0.0f;
+                if (w.whole) {
+                    float lse = live ? (m + log2f(l)) * LN2 : NEG_INF;
+                    c.x = live ? 1.0f / l : 0.0f;
+                    if (status != ROW_OK) lse = c.x = __int_as_float(0x7fc00000);
+                    if (P.lse) P.lse[row] = lse;
+                } else {
+                    part[(size_t)T.MR * D + col] = m;
+                    part[(size_t)T.MR * D + T.MR + col] = l;
+                }
+            }
+            sh.col[g][tok] = c;
+        }
+        group_sync(bar_id);
+        const size_t out0 = (size_t)w.b * P.T * P.Hq;
+#pragma unroll 1
         for (int ch = 0; ch < nch; ++ch) {
             uint32_t o[16];
-            if (!dead) tmem_ld16(t_o + ch * 16, o);
+            if (!dead) {
+                tmem_ld16_nowait(t_o + ch * 16, o);
+                tmem_wait_ld();
+            } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int c = ch * 16 + j, col = col0 + c, r = w.rt * T.MR + col;
-                if (col >= T.MR || r >= A.R) continue;
-                const float l = (sh.wmax[g][0][c] + sh.wmax[g][1][c]) + (sh.wmax[g][2][c] + sh.wmax[g][3][c]);
-                const float m = sh.fac[g][c] == -1.0f ? NEG_INF : reinterpret_cast<const float*>(&fr[c >> 1])[2 + (c & 1)];
-                const int t = r / A.G, hq = w.h * A.G + r % A.G;
-                float x = dead ? 0.0f : __uint_as_float(o[j]);
-                if (vbad && tok < D && t < w.rq.rows) {
-                    // values that are not finite reach the rows that see them
+                for (int j = 0; j < 16; ++j) o[j] = 0u;
+            }
+            if (tok >= D) continue;
+            if (vbad) {
+                // values that are not finite reach the rows that see them
+#pragma unroll 1
+                for (int j = 0; j < 16; ++j) {
+                    const float4 c = sh.col[g][ch * 16 + j];
+                    const int t = __float_as_int(c.z);
+                    if (__float_as_int(c.y) < 0 || t >= w.rq.rows) continue;
+                    float add = 0.0f;
                     for (int cur = t;;) {
-                        const float y = load_elem<DT>(A.vn, w.b * A.vb + cur * A.vt + w.h * A.vh + tok);
-                        if (!(fabsf(y) < __int_as_float(0x7f800000))) x += y;
+                        const float y = load_elem<DT>(P.vn, w.b * P.vb + cur * P.vt + w.h * P.vh + tok);
+                        if (!(fabsf(y) < __int_as_float(0x7f800000))) add += y;
                         if (cur == 0) break;
-                        const int p = A.parents ? __ldg(A.parents + (size_t)w.b * (A.T - 1) + cur - 1) : cur - 2;
+                        const int p = P.parents ? __ldg(P.parents + (size_t)w.b * (P.T - 1) + cur - 1) : cur - 2;
                         if (p < -1 || p >= cur - 1) break;
                         cur = p + 1;
                     }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        if (k == j) o[k] = __float_as_uint(__uint_as_float(o[k]) + add);
                 }
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float4 c = sh.col[g][ch * 16 + j];
+                const int row = __float_as_int(c.y);
+                if (row < 0) continue;
                 if (w.whole) {
-                    const bool live = t < w.rq.rows && l != 0.0f;
-                    float y = live ? x / l : 0.0f, lse = live ? (m + log2f(l)) * LN2 : NEG_INF;
-                    if (status != ROW_OK) y = lse = __int_as_float(0x7fc00000);
-                    const size_t row = ((size_t)w.b * A.T + t) * A.Hq + hq;
-                    if (tok < D) {
-                        const uint16_t v = DT == DT_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : __half_as_ushort(__float2half_rn(y));
-                        reinterpret_cast<uint16_t*>(A.out)[row * D + tok] = v;
-                    }
-                    if (tok == 0 && A.lse) A.lse[row] = lse;
+                    // a dead row's sums are zeros that no token touched, or NaN with the status
+                    const float y = c.x == 0.0f ? 0.0f : __uint_as_float(o[j]) * c.x;
+                    reinterpret_cast<uint16_t*>(P.out)[(out0 + row) * D + tok] =
+                        DT == DT_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : __half_as_ushort(__float2half_rn(y));
                 } else {
-                    if (tok < D) part[(size_t)col * D + tok] = x;
-                    if (tok == 0) {
-                        part[(size_t)T.MR * D + col] = m;
-                        part[(size_t)T.MR * D + T.MR + col] = l;
-                    }
+                    part[(size_t)(col0 + ch * 16 + j) * D + tok] = __uint_as_float(o[j]);
                 }
             }
         }
         if (threadIdx.x == SMW0 * 32) {
             if (w.whole) {
-                if (A.row_status && w.h == 0 && w.rt == 0) A.row_status[w.b] = status;
+                if (P.row_status && w.h == 0 && w.rt == 0) P.row_status[w.b] = status;
             } else {
                 part[(size_t)T.MR * D + 2 * T.MR] = __int_as_float(status);
-                if (w.tile0 == 0) A.joins[blockIdx.x] = {parts_of(at.total, blockIdx.x, at.ctas, w.u + w.rq.n), w.b, w.h, w.rt, w.rq.rows};
+                if (w.tile0 == 0) P.joins[blockIdx.x] = {parts_of(at.total, blockIdx.x, at.ctas, w.u + w.rq.n), w.b, w.h, w.rt, w.rq.rows};
             }
         }
         tc_fence_before();
@@ -863,17 +962,17 @@ attn_tc_kernel(const __grid_constant__ TcParams T, const __grid_constant__ CUten
         P.joins[blockIdx.x].parts = 0;
         for (int i = 0; i < T.stages; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], 3);  // the products' commit and the two warps that widen the values
+            mbar_init(&sh.empty[i], 1 + VWN);  // the products' commit and the warps that widen the values
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.sfull[i], 1);
-            mbar_init(&sh.sfree[i], 8);
-            mbar_init(&sh.pfull[i], 8);
-            mbar_init(&sh.vfull[i], 2);
+            mbar_init(&sh.sfree[i], 4 * NG);
+            mbar_init(&sh.pfull[i], 4 * NG);
+            mbar_init(&sh.vfull[i], VWN);
             mbar_init(&sh.pv[i], 1);
         }
-        mbar_init(&sh.qfull, 8);
-        mbar_init(&sh.q16, 8);
+        mbar_init(&sh.qfull, 4 * NG);
+        mbar_init(&sh.q16, 4 * NG);
         mbar_init(&sh.done, 1);
         sh.fail = 0;
         fence_mbar_init();
@@ -898,8 +997,8 @@ attn_tc_kernel(const __grid_constant__ TcParams T, const __grid_constant__ CUten
     else if (w == 1) {
         if ((tid & 31) == 0) role_mma<DT, D>(T, sh, at, smem_addr(smem), tmem);
         __syncwarp();
-    } else if (w < SMW0) role_values<DT, D>(T, sh, at, smem);
-    else role_softmax<DT, D>(T, sh, at, smem, tmem);
+    } else if (w < VW0 + VWN) role_values<DT, D>(T, sh, at, smem);
+    else if (w >= SMW0) role_softmax<DT, D>(T, sh, at, smem, tmem);
     tc_fence_before();
     __syncthreads();
     if (w == 1) {
@@ -948,14 +1047,26 @@ cudaError_t launch_tc(AttnParams& P, int sms, cudaStream_t st)
     T.wait_limit = P.wait_limit;
     const uint32_t terms = DT == DT_BF16 ? 2 : 3, blocks = (uint32_t)(T.RN + 63) / 64;
     T.p_buf = blocks * 16384;
-    T.np = T.nv = blocks == 1 ? 2 : 1;
     T.v_buf = D / 64 * 16384;
-    T.o_p = terms * T.RN * D;
-    T.o_v = T.o_p + T.np * T.p_buf;
-    T.o_stage = T.o_v + T.nv * T.v_buf + (D == 64 ? 16384 : 0);
     const uint32_t stage = 2 * TT * D;
-    T.stages = (int)((TC_SMEM - 1024 - T.o_stage) / stage);
+    // second buffers of the values and of P where three stages still fit beside them
+    for (int extra = 2;; --extra) {
+        T.nv = extra >= 1 ? 2 : 1;
+        T.np = extra >= 2 ? 2 : 1;
+        T.o_p = terms * T.RN * D;
+        T.o_v = T.o_p + T.np * T.p_buf;
+        T.o_stage = T.o_v + T.nv * T.v_buf + (D == 64 ? 16384 : 0);
+        T.stages = (int)(((int)TC_SMEM - 1024 - (int)T.o_stage) / (int)stage);
+        if (T.stages >= 3 || extra == 0) break;
+    }
     if (T.stages > MAXSTAGES) T.stages = MAXSTAGES;
+    const auto vec = [](const void* p, int64_t a, int64_t b, int64_t c) {
+        constexpr int64_t n = D / 32;
+        return reinterpret_cast<uintptr_t>(p) % (2 * n) == 0 && a % n == 0 && b % n == 0 && c % n == 0;
+    };
+    T.qvec = vec(P.q, P.qb, P.qt, P.qh);
+    T.kvec = vec(P.kn, P.kb, P.kt, P.kh);
+    T.vvec = vec(P.vn, P.vb, P.vt, P.vh);
     const size_t bytes = 1024 + T.o_stage + (size_t)T.stages * stage;
     auto* k = attn_tc_kernel<DT, D>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TC_SMEM);
