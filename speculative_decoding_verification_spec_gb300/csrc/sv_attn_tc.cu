@@ -58,13 +58,12 @@ struct TcParams {
 
 // ---------------------------------------------------------------- tcgen05
 
-__device__ __forceinline__ uint64_t desc_base(uint32_t layout, uint32_t lbo, uint32_t sbo)
-{
-    // strides in bytes; bit 46: the descriptor version of this architecture; bits 61-63: the swizzle
-    return (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 | (uint64_t)layout << 61;
-}
-__device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t addr) { return base | (uint64_t)((addr >> 4) & 0x3fffu); }
+// A shared-memory operand's descriptor in two words.  Low: the address and the stride between 64-channel blocks (operands
+// with M or N contiguous); high: the stride between groups of eight rows, the descriptor version of this architecture
+// (bit 46) and the swizzle (bits 61-63).
 constexpr uint32_t SW128 = 2, SW64 = 4;
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t swizzle, uint32_t sbo) { return sbo >> 4 | 1u << 14 | swizzle << 29; }
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4 & 0x3fffu) | lbo >> 4 << 16; }
 
 // instruction descriptor: fp32 accumulator, M = 128, N, both operands of format 0 (e4m3 / half); `mn`: both with their M / N
 // dimension contiguous
@@ -73,15 +72,23 @@ __device__ __forceinline__ uint32_t idesc(int N, bool mn)
     return 1u << 4 | (mn ? 1u << 15 | 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (128u >> 4) << 24;
 }
 
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc)
+__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t ah, uint32_t b, uint32_t bh, uint32_t id, bool acc)
 {
-    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }"
-                 :: "r"(d), "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc) : "memory");
+    asm volatile("{ .reg .pred p; .reg .b64 x, y; mov.b64 x, {%1, %2}; mov.b64 y, {%3, %4}; setp.ne.u32 p, %6, 0;"
+                 " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %5, p; }"
+                 :: "r"(d), "r"(a), "r"(ah), "r"(b), "r"(bh), "r"(id), "r"((uint32_t)acc) : "memory");
 }
-__device__ __forceinline__ void mma_h(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc)
+__device__ __forceinline__ void mma_h(uint32_t d, uint32_t a, uint32_t ah, uint32_t b, uint32_t bh, uint32_t id, bool acc)
 {
-    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
-                 :: "r"(d), "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc) : "memory");
+    asm volatile("{ .reg .pred p; .reg .b64 x, y; mov.b64 x, {%1, %2}; mov.b64 y, {%3, %4}; setp.ne.u32 p, %6, 0;"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p; }"
+                 :: "r"(d), "r"(a), "r"(ah), "r"(b), "r"(bh), "r"(id), "r"((uint32_t)acc) : "memory");
+}
+__device__ __forceinline__ bool elected()
+{
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar)
 {
@@ -130,10 +137,10 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes)
 
 struct Shared {
     uint64_t full[MAXSTAGES], empty[MAXSTAGES];
-    uint64_t sfull[2], sfree[2], pfull[2], vfull[2], pv[2], qfull, q16, done;
+    uint64_t sfull[2], ready[2], pv[2], own[2], qfull, done;
     float2 scale[MAXSTAGES][8];   // of the stage's pages: keys, values
     int status[MAXSTAGES];
-    float4 fr[2][MAXR / 2];       // per pair of columns: factors, references; two copies, one being rewritten
+    float4 fr[2][MAXR / 2];       // per pair of columns: factors, references negated; two copies, one being rewritten
     float wred[NG][4][MAXC];      // column maxima and sums of the softmax warps
     float4 col[NG][MAXC];         // a moved reference's factors; the outputs' columns
     float unseen[NG][MAXC];       // 1: no token of the group so far was seen by the column
@@ -145,12 +152,19 @@ struct Shared {
     Place place;
 };
 
-// Bounded wait; ends early once another role has given up.  The result is the warp's.
-__device__ __forceinline__ bool wait_on(Shared& sh, uint64_t* bar, uint32_t parity, int limit)
+// Bounded wait; ends early once another role has given up.  Out of line, as are a group's bookkeeping and the first pass over
+// a round's own rows: with everything inline the roles' loops together outgrow the instruction cache, and every step waits
+// for its code.
+__device__ __noinline__ bool wait_on(Shared& sh, uint64_t* bar, uint32_t parity, int limit)
 {
-    for (int n = 0; n < limit; n += 64) {
-        if (mbar_wait(bar, parity, min(64, limit - n))) return true;
-        if (*reinterpret_cast<volatile int*>(&sh.fail)) return false;
+    const uint32_t a = smem_addr(bar);
+#pragma unroll 1
+    for (int n = 0; n < limit; ++n) {
+        uint32_t done;
+        asm volatile("{ .reg .pred q; mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2; selp.u32 %0, 1, 0, q; }"
+                     : "=r"(done) : "r"(a), "r"(parity) : "memory");
+        if (done) return true;
+        if ((n & 63) == 63 && *reinterpret_cast<volatile int*>(&sh.fail)) return false;
     }
     *reinterpret_cast<volatile int*>(&sh.fail) = 1;
     return false;
@@ -180,7 +194,7 @@ struct Walk {
     int h, rt, tile0, tile1;
     bool whole, first;
 
-    __device__ Walk(const AttnParams& P, const Place& at)
+    __device__ __noinline__ Walk(const AttnParams& P, const Place& at)
     {
         u = at.total * blockIdx.x / at.ctas;
         u1 = at.total * (blockIdx.x + 1) / at.ctas;
@@ -191,7 +205,7 @@ struct Walk {
         first = true;
     }
     __device__ bool more() const { return u < u1; }
-    __device__ void open()
+    __device__ __noinline__ void open()
     {
         const long long rem = u - pre;
         const int grp = (int)(rem / rq.n);
@@ -201,7 +215,7 @@ struct Walk {
         tile1 = (int)min((long long)rq.n, tile0 + (u1 - u));
         whole = tile0 == 0 && tile1 == rq.n;
     }
-    __device__ void next(const AttnParams& P)
+    __device__ __noinline__ void next(const AttnParams& P)
     {
         first = false;
         u += tile1 - tile0;
@@ -279,8 +293,10 @@ __device__ void role_copy(const TcParams& T, Shared& sh, const Place& at, uint32
     __syncwarp();
 }
 
-// One lane.  Products of tile `it`: S^T as soon as its keys are there; O^T of the tile before after that, except
-// where the next S^T needs what the softmax does only after that O^T (a group's first tile, the round's rows).
+// Products of tile `it`: S^T as soon as its keys are there; O^T of the tile before after that, except where the next S^T
+// needs what the softmax does only after that O^T (a group's first tile, the round's rows).  S^T may be rewritten once the
+// weights of the tile before last are ready, which its O^T has waited for.  The whole warp walks through, so that the
+// operands are uniform registers; one elected lane issues.
 template <int DT, int D>
 __device__ void role_mma(const TcParams& T, Shared& sh, const Place& at, uint32_t base, uint32_t tmem)
 {
@@ -289,71 +305,82 @@ __device__ void role_mma(const TcParams& T, Shared& sh, const Place& at, uint32_
     constexpr uint32_t KB = TT * D;
     const uint32_t sp = base + T.o_p, sv_ = base + T.o_v, ring = base + T.o_stage;
     const uint32_t qterm = (uint32_t)T.RN * D;
-    const uint64_t dk = D == 128 ? desc_base(SW128, 16, 1024) : desc_base(SW64, 16, 512);
-    const uint64_t dkh = desc_base(SW128, 16, 1024);
-    const uint64_t dp = desc_base(SW128, 16384, 1024);
+    constexpr uint32_t H_K = D == 128 ? desc_hi(SW128, 1024) : desc_hi(SW64, 512), H_128 = desc_hi(SW128, 1024);
     const uint32_t id_s = idesc(T.RN, false), id_o = idesc(T.RN, true);
     const uint32_t t_o = tmem + 2 * T.RN;
-    int it = 0, seg = 0, own = 0;  // own: tiles of the rounds' rows so far
-    bool ok = true;
-    int pending = -1;
-    bool pending_first = false;
+    const auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    int it = 0, stage = 0, stage_par = 0, seg = 0;
+    uint32_t own = 0;                                        // phases of the two barriers of the rounds' rows
+    int pending = 0, pending_first = 0, ok = 1;              // pending: O^T of the tile before is still to be issued
 
-    const auto pv = [&]() {  // O^T of tile `pending`
-        const int i = pending;
-        pending = -1;
-        if (!wait_on(sh, &sh.pfull[i & 1], (i >> 1) & 1, T.wait_limit) || !wait_on(sh, &sh.vfull[i & 1], (i >> 1) & 1, T.wait_limit)) return false;
+    const auto pv = [&]() {  // O^T of the tile before
+        const int i = it - 1;
+        pending = 0;
+        if (!uni(wait_warp(sh, &sh.ready[i & 1], (i >> 1) & 1, T.wait_limit))) return 0;
         tc_fence_after();
-        const uint32_t vb = sv_ + (i % T.nv) * T.v_buf, pb = sp + (i % T.np) * T.p_buf;
+        const int vi = T.nv == 2 ? i & 1 : 0, pi = T.np == 2 ? i & 1 : 0;
         // the second block of 64 channels: the next 16 KB, or (D = 64) the block of zeros after the buffers
-        const uint64_t dv = desc_base(SW128, D == 128 ? 16384 : T.nv * T.v_buf - (i % T.nv) * T.v_buf, 1024);
+        const uint32_t lbo = D == 128 ? 16384 : (T.nv - vi) * T.v_buf;
+        const uint32_t a = desc_lo(sv_ + vi * T.v_buf, lbo), b = desc_lo(sp + pi * T.p_buf, 16384);
+        if (elected()) {
 #pragma unroll
-        for (int k = 0; k < TT / 16; ++k)
-            mma_h(t_o, desc_at(dv, vb + k * 2048), desc_at(dp, pb + k * 2048), id_o, !(pending_first && k == 0));
-        mma_commit(&sh.pv[i & 1]);
-        return true;
+            for (int k = 0; k < TT / 16; ++k)
+                mma_h(t_o, a + k * (2048 >> 4), H_128, b + k * (2048 >> 4), H_128, id_o, !pending_first || k > 0);
+            mma_commit(&sh.pv[i & 1]);
+        }
+        __syncwarp();
+        return 1;
     };
 
     for (Walk w(P, at); ok && w.more(); w.next(P), ++seg) {
         w.open();
-        for (int tile = w.tile0; ok && tile < w.tile1; ++tile, ++it) {
-            const int s = it % T.stages;
-            const bool fresh = tile >= w.rq.ncache;
-            const bool first = tile == w.tile0;
-            if (pending >= 0 && (first || fresh)) ok = pv();
-            ok = ok && wait_on(sh, &sh.full[s], (it / T.stages) & 1, T.wait_limit);
-            if (it >= 2) ok = ok && wait_on(sh, &sh.sfree[it & 1], ((it >> 1) & 1) ^ 1, T.wait_limit);
-            if (first) ok = ok && wait_on(sh, &sh.qfull, seg & 1, T.wait_limit);
+        const int tile0 = uni(w.tile0), tile1 = uni(w.tile1), ncache = uni(w.rq.ncache);
+        for (int tile = tile0; tile < tile1; ++tile) {
+            const bool fresh = tile >= ncache, first = tile == tile0;
+            if (pending && (first || fresh)) ok = pv();
+            ok = ok && uni(wait_warp(sh, &sh.full[stage], stage_par, T.wait_limit));
+            if (first) ok = ok && uni(wait_warp(sh, &sh.qfull, seg & 1, T.wait_limit));
             if (fresh) {
-                ok = ok && wait_on(sh, &sh.vfull[it & 1], (it >> 1) & 1, T.wait_limit) && wait_on(sh, &sh.q16, own & 1, T.wait_limit);
-                ++own;
+                ok = ok && uni(wait_warp(sh, &sh.own[it & 1], own >> (it & 1) & 1, T.wait_limit));
+                own ^= 1u << (it & 1);
             }
             if (!ok) break;
             tc_fence_after();
-            const uint32_t ts = tmem + (it & 1) * T.RN, kb = ring + s * 2 * KB;
+            const uint32_t ts = tmem + (it & 1) * T.RN, kb = ring + stage * 2 * KB;
             if (!fresh) {
+                const uint32_t a = desc_lo(kb, 16), b = desc_lo(base, 16);
+                if (elected()) {
 #pragma unroll
-                for (int q = 0; q < TERMS; ++q)
+                    for (int q = 0; q < TERMS; ++q)
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k)
-                        mma_f8(ts, desc_at(dk, kb + k * 32), desc_at(dk, base + q * qterm + k * 32), id_s, q + k > 0);
+                        for (int k = 0; k < D / 32; ++k)
+                            mma_f8(ts, a + k * 2, H_K, b + q * (qterm >> 4) + k * 2, H_K, id_s, q + k > 0);
+                    mma_commit(&sh.sfull[it & 1]);
+                    mma_commit(&sh.empty[stage]);
+                }
             } else {
-                const uint32_t qb = sp + (it % T.np) * T.p_buf;
+                const uint32_t a = desc_lo(kb, 16), b = desc_lo(sp + (T.np == 2 ? it & 1 : 0) * T.p_buf, 16);
+                if (elected()) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_h(ts, desc_at(dkh, kb + (k >> 2) * 16384 + (k & 3) * 32),
-                          desc_at(dkh, qb + (k >> 2) * T.RN * 128 + (k & 3) * 32), id_s, k > 0);
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_h(ts, a + (k >> 2) * (16384 >> 4) + (k & 3) * 2, H_128, b + (k >> 2) * (T.RN * 128 >> 4) + (k & 3) * 2, H_128,
+                              id_s, k > 0);
+                    mma_commit(&sh.sfull[it & 1]);
+                    mma_commit(&sh.empty[stage]);
+                }
             }
-            mma_commit(&sh.sfull[it & 1]);
-            mma_commit(&sh.empty[s]);
-            if (pending >= 0) ok = pv();
-            pending = it;
+            __syncwarp();
+            if (pending) ok = pv();
+            pending = 1;
             pending_first = first;
+            ++it;
+            if (++stage == T.stages) stage = 0, stage_par ^= 1;
         }
     }
-    if (ok && pending >= 0) (void)pv();
+    if (ok && pending) (void)pv();
     // everything issued has ended before the accumulators are given back
-    mma_commit(&sh.done);
+    if (elected()) mma_commit(&sh.done);
+    __syncwarp();
     (void)mbar_wait(&sh.done, 0, MBAR_SPIN_LIMIT);
 }
 
@@ -499,7 +526,8 @@ __device__ void role_values(const TcParams& T, Shared& sh, const Place& at, uint
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&sh.vfull[it & 1]);
+                if (tile >= w.rq.ncache) mbar_arrive(&sh.own[it & 1]);
+                mbar_arrive(&sh.ready[it & 1]);
                 mbar_arrive(&sh.empty[s]);
             }
         }
@@ -666,11 +694,12 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
                     fence_proxy_async_smem();
                 }
                 if (group_any(bar_id, badp)) status = ROW_BAD_PARENT;
-                if (!fail && lane == 0) mbar_arrive(&sh.q16);
+                if (!fail && lane == 0) mbar_arrive(&sh.own[it & 1]);
             }
 
             fail = fail || !wait_warp(sh, &sh.sfull[it & 1], (it >> 1) & 1, T.wait_limit);
-            if (!fresh && it >= T.np) fail = fail || !wait_warp(sh, &sh.pv[(it - T.np) & 1], ((it - T.np) >> 1) & 1, T.wait_limit);
+            // where P has one buffer, its last use; of two, S^T's commit stands for the use before last, which it followed
+            if (!fresh && T.np == 1 && it >= 1) fail = fail || !wait_warp(sh, &sh.pv[(it - 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit);
             float ks = 1.0f, ve = 0.0f;
             bool okt = false, partial = true;
             const uint32_t ts = tl + (it & 1) * T.RN + col0;
@@ -705,37 +734,25 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
             };
             // A pass over the tile: weights to shared memory, their sums to l.  The first pass goes by the reference as it
             // stands.  Where that turns out too low the sums are rescaled, this pass's share with them, and a second
-            // one repeats the weights; it adds to l only what the first left out because it would have passed fp32's range.
+            // one repeats the weights; it adds to l only what the first left out: 16 columns of a warp one of whose
+            // weights would have taken the sum out of fp32's range.
             float vmax = NEG_INF;
+            uint32_t left_out = first ? 0xffffffffu : 0u;
             const auto weights = [&](auto again) {
                 const float4* fr = rb ? fr1 : fr0;
-                const float4* old = rb ? fr0 : fr1;
 #pragma unroll 1
                 for (int ch = 0; ch < nch; ++ch) {
                     uint32_t s[16], l[16], h[8];
                     tmem_ld16_nowait(ts + ch * 16, s);
-                    if (again.value && first) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) l[j] = 0u;
-                    } else {
-                        tmem_ld16_nowait(t_l + ch * 16, l);
-                    }
+                    if (!(again.value && first)) tmem_ld16_nowait(t_l + ch * 16, l);
                     const uint32_t see = partial ? seen16(ch) : 0xffffu;
                     tmem_wait_ld();
-                    float top = NEG_INF;
-                    unsigned far = 0;  // second pass: elements that the first left out
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float4 f = fr[ch * 8 + j];
                         const unsigned long long x = f2_mul(f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), f2_pack(f.x, f.y));
                         float a, b;
-                        f2_unpack(f2_fma(x, ks2, f2_add(ve2, f2_pack(-f.z, -f.w))), a, b);
-                        if (again.value && !first) {
-                            const float4 o = old[ch * 8 + j];
-                            float c, d;
-                            f2_unpack(f2_fma(x, ks2, f2_add(ve2, f2_pack(-o.z, -o.w))), c, d);
-                            far |= (unsigned)(c > FAR) << (2 * j) | (unsigned)(d > FAR) << (2 * j + 1);
-                        }
+                        f2_unpack(f2_fma(x, ks2, f2_add(ve2, f2_pack(f.z, f.w))), a, b);
                         s[2 * j] = __float_as_uint(a);
                         s[2 * j + 1] = __float_as_uint(b);
                     }
@@ -743,32 +760,41 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
 #pragma unroll
                         for (int j = 0; j < 16; ++j) s[j] = see >> j & 1u ? s[j] : __float_as_uint(NEG_INF);
                     }
+                    bool sums;
+                    if constexpr (again.value) {
+                        sums = left_out >> ch & 1u;
+                    } else {
+                        float top = NEG_INF;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) top = fmaxf(top, __uint_as_float(s[j]));
-                    vmax = fmaxf(vmax, top);
-                    const bool all = again.value ? first : !__any_sync(0xffffffffu, top > FAR);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float a = ex2(__uint_as_float(s[2 * j])), b = ex2(__uint_as_float(s[2 * j + 1]));
-                        h[j] = pack_half2(a, b);
-                        if (!all) {
-                            if (again.value ? !(far >> (2 * j) & 1u) : __uint_as_float(s[2 * j]) > FAR) a = 0.0f;
-                            if (again.value ? !(far >> (2 * j + 1) & 1u) : __uint_as_float(s[2 * j + 1]) > FAR) b = 0.0f;
-                        }
-                        float c, d;
-                        f2_unpack(f2_fma(f2_pack(a, b), inv2, f2_pack(__uint_as_float(l[2 * j]), __uint_as_float(l[2 * j + 1]))), c, d);
-                        l[2 * j] = __float_as_uint(c);
-                        l[2 * j + 1] = __float_as_uint(d);
+                        for (int j = 0; j < 16; ++j) top = fmaxf(top, __uint_as_float(s[j]));
+                        vmax = fmaxf(vmax, top);
+                        sums = !__any_sync(0xffffffffu, top > FAR);
+                        if (!sums) left_out |= 1u << ch;
                     }
-                    tmem_st16_nowait(t_l + ch * 16, l);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) s[j] = __float_as_uint(ex2(__uint_as_float(s[j])));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) h[j] = pack_half2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
                     const int col = col0 + ch * 16;
                     uint8_t* row = pb + (size_t)(col >> 6) * 16384 + tok * 128;
                     const int unit = (col & 63) >> 3;
                     *reinterpret_cast<uint4*>(row + ((unit ^ (tok & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                     *reinterpret_cast<uint4*>(row + (((unit + 1) ^ (tok & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                    if (sums) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const unsigned long long p = f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+                            float c, d;
+                            if (again.value && first) f2_unpack(f2_mul(p, inv2), c, d);
+                            else f2_unpack(f2_fma(p, inv2, f2_pack(__uint_as_float(l[2 * j]), __uint_as_float(l[2 * j + 1]))), c, d);
+                            l[2 * j] = __float_as_uint(c);
+                            l[2 * j + 1] = __float_as_uint(d);
+                        }
+                        tmem_st16_nowait(t_l + ch * 16, l);
+                    }
                 }
-                tmem_wait_st();
                 fence_proxy_async_smem();
+                tmem_wait_st();
             };
             // the first tile of a group has no reference yet
             if (!fail && !first) weights(std::false_type{});
@@ -806,12 +832,12 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
                     // a column that has seen nothing yet keeps the reference 0, which its zero sums do not feel
                     const float* f = reinterpret_cast<const float*>(&fr[tok >> 1]);
                     float* n = reinterpret_cast<float*>(&to[tok >> 1]);
-                    const float was = first ? 0.0f : f[2 + (tok & 1)];
+                    const float was = first ? 0.0f : -f[2 + (tok & 1)];
                     const bool none = first || sh.unseen[g][tok] != 0.0f;
                     const bool move = none ? top > NEG_INF : top > was + WINDOW;
                     const float now = move ? top - HEAD : was;
                     n[tok & 1] = f[tok & 1];
-                    n[2 + (tok & 1)] = now;
+                    n[2 + (tok & 1)] = -now;
                     sh.col[g][tok].x = move && !none ? ex2(was - now) : 1.0f;  // of the sums so far
                     sh.unseen[g][tok] = none && !move ? 1.0f : 0.0f;
                 }
@@ -837,10 +863,7 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sh.sfree[it & 1]);
-                mbar_arrive(&sh.pfull[it & 1]);
-            }
+            if (lane == 0) mbar_arrive(&sh.ready[it & 1]);
         }
 
         // ---- outputs
@@ -869,7 +892,7 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
             // a column's row of the output (-1: none), and the factor of its sums
             const int col = col0 + tok, r = w.rt * T.MR + col, t = r / P.G;
             const float l = dead ? 0.0f : (sh.wred[g][0][tok] + sh.wred[g][1][tok]) + (sh.wred[g][2][tok] + sh.wred[g][3][tok]);
-            const float m = dead || sh.unseen[g][tok] != 0.0f ? NEG_INF : reinterpret_cast<const float*>(&(rb ? fr1 : fr0)[tok >> 1])[2 + (tok & 1)];
+            const float m = dead || sh.unseen[g][tok] != 0.0f ? NEG_INF : -reinterpret_cast<const float*>(&(rb ? fr1 : fr0)[tok >> 1])[2 + (tok & 1)];
             float4 c = make_float4(0.0f, __int_as_float(-1), __int_as_float(t), 0.0f);
             if (col < T.MR && r < P.R) {
                 const size_t row = ((size_t)w.b * P.T + t) * P.Hq + w.h * P.G + r % P.G;
@@ -966,13 +989,11 @@ attn_tc_kernel(const __grid_constant__ TcParams T, const __grid_constant__ CUten
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.sfull[i], 1);
-            mbar_init(&sh.sfree[i], 4 * NG);
-            mbar_init(&sh.pfull[i], 4 * NG);
-            mbar_init(&sh.vfull[i], VWN);
+            mbar_init(&sh.ready[i], 4 * NG + VWN);  // weights and values
+            mbar_init(&sh.own[i], 4 * NG + VWN);    // the round's rows: q, keys and values as halfs
             mbar_init(&sh.pv[i], 1);
         }
         mbar_init(&sh.qfull, 4 * NG);
-        mbar_init(&sh.q16, 4 * NG);
         mbar_init(&sh.done, 1);
         sh.fail = 0;
         fence_mbar_init();
@@ -995,8 +1016,7 @@ attn_tc_kernel(const __grid_constant__ TcParams T, const __grid_constant__ CUten
     const uint32_t tmem = sh.tmem;
     if (w == 0) role_copy<D>(T, sh, at, smem_addr(smem) + T.o_stage, &mk, &mv);
     else if (w == 1) {
-        if ((tid & 31) == 0) role_mma<DT, D>(T, sh, at, smem_addr(smem), tmem);
-        __syncwarp();
+        role_mma<DT, D>(T, sh, at, smem_addr(smem), tmem);
     } else if (w < VW0 + VWN) role_values<DT, D>(T, sh, at, smem);
     else if (w >= SMW0) role_softmax<DT, D>(T, sh, at, smem, tmem);
     tc_fence_before();
