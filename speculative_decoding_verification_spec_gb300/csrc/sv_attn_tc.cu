@@ -161,7 +161,8 @@ __device__ __noinline__ bool wait_on(Shared& sh, uint64_t* bar, uint32_t parity,
 #pragma unroll 1
     for (int n = 0; n < limit; ++n) {
         uint32_t done;
-        asm volatile("{ .reg .pred q; mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2; selp.u32 %0, 1, 0, q; }"
+        // suspended for up to 2 us a poll: a spinning warp would take its scheduler's slots from the working ones
+        asm volatile("{ .reg .pred q; mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2, 2000; selp.u32 %0, 1, 0, q; }"
                      : "=r"(done) : "r"(a), "r"(parity) : "memory");
         if (done) return true;
         if ((n & 63) == 63 && *reinterpret_cast<volatile int*>(&sh.fail)) return false;
@@ -323,7 +324,7 @@ __device__ void role_mma(const TcParams& T, Shared& sh, const Place& at, uint32_
         const uint32_t lbo = D == 128 ? 16384 : (T.nv - vi) * T.v_buf;
         const uint32_t a = desc_lo(sv_ + vi * T.v_buf, lbo), b = desc_lo(sp + pi * T.p_buf, 16384);
         if (elected()) {
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < TT / 16; ++k)
                 mma_h(t_o, a + k * (2048 >> 4), H_128, b + k * (2048 >> 4), H_128, id_o, !pending_first || k > 0);
             mma_commit(&sh.pv[i & 1]);
@@ -337,22 +338,28 @@ __device__ void role_mma(const TcParams& T, Shared& sh, const Place& at, uint32_
         const int tile0 = uni(w.tile0), tile1 = uni(w.tile1), ncache = uni(w.rq.ncache);
         for (int tile = tile0; tile < tile1; ++tile) {
             const bool fresh = tile >= ncache, first = tile == tile0;
-            if (pending && (first || fresh)) ok = pv();
+            // O^T of the tile before goes in front of S^T or after it: step 0 or 2, so that its code is here once
+#pragma unroll 1
+            for (int step = pending && (first || fresh) ? 0 : 1; ok && step < 3; ++step) {
+            if (step != 1) {
+                if (pending) ok = pv();
+                continue;
+            }
             ok = ok && uni(wait_warp(sh, &sh.full[stage], stage_par, T.wait_limit));
             if (first) ok = ok && uni(wait_warp(sh, &sh.qfull, seg & 1, T.wait_limit));
             if (fresh) {
                 ok = ok && uni(wait_warp(sh, &sh.own[it & 1], own >> (it & 1) & 1, T.wait_limit));
                 own ^= 1u << (it & 1);
             }
-            if (!ok) break;
+            if (!ok) continue;
             tc_fence_after();
             const uint32_t ts = tmem + (it & 1) * T.RN, kb = ring + stage * 2 * KB;
             if (!fresh) {
                 const uint32_t a = desc_lo(kb, 16), b = desc_lo(base, 16);
                 if (elected()) {
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < TERMS; ++q)
-#pragma unroll
+#pragma unroll 2
                         for (int k = 0; k < D / 32; ++k)
                             mma_f8(ts, a + k * 2, H_K, b + q * (qterm >> 4) + k * 2, H_K, id_s, q + k > 0);
                     mma_commit(&sh.sfull[it & 1]);
@@ -361,7 +368,7 @@ __device__ void role_mma(const TcParams& T, Shared& sh, const Place& at, uint32_
             } else {
                 const uint32_t a = desc_lo(kb, 16), b = desc_lo(sp + (T.np == 2 ? it & 1 : 0) * T.p_buf, 16);
                 if (elected()) {
-#pragma unroll
+#pragma unroll 2
                     for (int k = 0; k < D / 16; ++k)
                         mma_h(ts, a + (k >> 2) * (16384 >> 4) + (k & 3) * 2, H_128, b + (k >> 2) * (T.RN * 128 >> 4) + (k & 3) * 2, H_128,
                               id_s, k > 0);
@@ -370,7 +377,8 @@ __device__ void role_mma(const TcParams& T, Shared& sh, const Place& at, uint32_
                 }
             }
             __syncwarp();
-            if (pending) ok = pv();
+            }
+            if (!ok) break;
             pending = 1;
             pending_first = first;
             ++it;
@@ -435,11 +443,45 @@ __device__ __forceinline__ void load_run(const void* p, int64_t i, bool vec, flo
     }
 }
 
+// the values of one tile of the cache, codes to halfs; tokens from `valid` on become zeros, whatever their slots hold
+template <int D>
+__device__ __noinline__ void widen_tile(const uint8_t* codes, uint8_t* vb, int ct, int valid)
+{
+    constexpr int CH = D / 16, U = 3;
+#pragma unroll 1
+    for (int i0 = ct; i0 < TT * CH; i0 += U * VWN * 32) {
+        uint4 x[U];
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const int i = i0 + q * VWN * 32;
+            x[q] = make_uint4(0, 0, 0, 0);
+            if (i < TT * CH && i / CH < valid) x[q] = *reinterpret_cast<const uint4*>(codes + i * 16);
+        }
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const int i = i0 + q * VWN * 32, tok = i / CH, ch = i % CH;
+            if (i >= TT * CH) break;
+            const uint32_t u[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                y[2 * k] = e4m3x2_to_half2((uint16_t)u[k]);
+                y[2 * k + 1] = e4m3x2_to_half2((uint16_t)(u[k] >> 16));
+            }
+            const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+            // the two blocks of 64 channels start with opposite halves, so a quarter-warp's stores meet no bank twice
+            const int f = ch >> 2;
+            *reinterpret_cast<uint4*>(vb + half_off(tok, ch * 16 + 8 * f)) = f ? hi : lo;
+            *reinterpret_cast<uint4*>(vb + half_off(tok, ch * 16 + 8 * (f ^ 1))) = f ? lo : hi;
+        }
+    }
+}
+
 template <int DT, int D>
 __device__ void role_values(const TcParams& T, Shared& sh, const Place& at, uint8_t* smem)
 {
     const AttnParams& P = T.A;
-    constexpr int KB = TT * D, CH = D / 16, EPL = D / 32;
+    constexpr int KB = TT * D, EPL = D / 32;
     const int ct = threadIdx.x - VW0 * 32, wv = ct >> 5, lane = ct & 31;
     int it = 0;
     bool ok = true;
@@ -454,34 +496,7 @@ __device__ void role_values(const TcParams& T, Shared& sh, const Place& at, uint
             if (!ok) break;
             if (tile < w.rq.ncache) {
                 const int valid = w.rq.len - tile * TT;
-                constexpr int U = 3;
-                for (int i0 = ct; i0 < TT * CH; i0 += U * VWN * 32) {
-                    uint4 x[U];
-#pragma unroll
-                    for (int q = 0; q < U; ++q) {
-                        const int i = i0 + q * VWN * 32;
-                        x[q] = make_uint4(0, 0, 0, 0);  // tokens past the length, whatever their slots hold
-                        if (i < TT * CH && i / CH < valid) x[q] = *reinterpret_cast<const uint4*>(kb + KB + i * 16);
-                    }
-#pragma unroll
-                    for (int q = 0; q < U; ++q) {
-                        const int i = i0 + q * VWN * 32, tok = i / CH, ch = i % CH;
-                        if (i >= TT * CH) break;
-                        const uint32_t u[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
-                        uint32_t y[8];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            y[2 * k] = e4m3x2_to_half2((uint16_t)u[k]);
-                            y[2 * k + 1] = e4m3x2_to_half2((uint16_t)(u[k] >> 16));
-                        }
-                        const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-                        // the two blocks of 64 channels start with opposite halves, so a quarter-warp's stores meet no
-                        // bank twice
-                        const int f = ch >> 2;
-                        *reinterpret_cast<uint4*>(vb + half_off(tok, ch * 16 + 8 * f)) = f ? hi : lo;
-                        *reinterpret_cast<uint4*>(vb + half_off(tok, ch * 16 + 8 * (f ^ 1))) = f ? lo : hi;
-                    }
-                }
+                widen_tile<D>(kb + KB, vb, ct, valid);
             } else {
                 // the round's rows: keys into the stage, values into the buffer, scaled by a power of two per token
                 const int j0 = (tile - w.rq.ncache) * TT, live = P.kn ? min(max(w.rq.rows - j0, 0), TT) : 0;
@@ -548,6 +563,110 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane, Op op)
         }
     }
     return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+}
+
+// What softmax_run stopped at.
+struct RunEnd {
+    int n;              // tiles done
+    int status;
+    uint32_t left_out;  // of the tile it stopped at: the 16-column chunks whose sums this warp has not taken
+    bool stopped, fail;
+};
+
+// The softmax over a group's ordinary tiles: of the cache, with a reference.  One pass per tile; the run ends where a weight
+// passes the window (for any thread of the group) or a wait runs out.  A function of its own, so that the loop's code is one
+// piece.
+__device__ __noinline__ RunEnd softmax_run(const TcParams& T, Shared& sh, uint8_t* prow, const float4* fr, uint32_t tl, int col0, int nch,
+                                           int bar_id, int it, int tile, int end, int len)
+{
+    const int lane = threadIdx.x & 31, tok = ((threadIdx.x >> 5) & 3) * 32 + lane;
+    const int RN = T.RN, np = T.np, limit = T.wait_limit, stages = T.stages, page_shift = T.A.page_shift;
+    const uint32_t p_buf = T.p_buf, t_l = tl + 3 * RN + col0;
+    int s_at = it % stages;
+    RunEnd r = {0, ROW_OK, 0u, false, false};
+#pragma unroll 1
+    for (; tile < end; ++tile, ++it, ++r.n) {
+        bool fail = !wait_warp(sh, &sh.sfull[it & 1], (it >> 1) & 1, limit);
+        // where P has one buffer, its last use; of two, S^T's commit stands for the use before last, which it followed
+        if (np == 1) fail = fail || !wait_warp(sh, &sh.pv[(it - 1) & 1], ((it - 1) >> 1) & 1, limit);
+        float vmax = NEG_INF;
+        r.left_out = 0;
+        if (!fail) {
+            tc_fence_after();
+            const int left = len - tile * TT;
+            const bool okt = tok < left;
+            float ks = 1.0f, ve = 0.0f;
+            if (okt) {
+                const float2 sc = sh.scale[s_at][tok >> page_shift];
+                ks = sc.x;
+                ve = (float)exponent_of(sc.y);
+            }
+            r.status = max(r.status, sh.status[s_at]);
+            if (++s_at == stages) s_at = 0;
+            const float inv = exp2_int(min(max(-(int)ve, -126), 127));
+            const unsigned long long ks2 = f2_pack(ks, ks), ve2 = f2_pack(ve, ve), inv2 = f2_pack(inv, inv);
+            const uint32_t ts = tl + (it & 1) * RN + col0;
+            uint8_t* row = prow + (np == 2 ? it & 1 : 0) * p_buf;
+#pragma unroll 1
+            for (int ch = 0; ch < nch; ++ch) {
+                uint32_t s[16], l[16], h[8];
+                uint4 f[8];
+                tmem_ld16_nowait(ts + ch * 16, s);
+                // all eight in flight at once, beside the scores
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = lds128(reinterpret_cast<const uint4*>(&fr[ch * 8 + j]));
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const unsigned long long x = f2_mul(f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])),
+                                                        f2_pack(__uint_as_float(f[j].x), __uint_as_float(f[j].y)));
+                    float a, b;
+                    f2_unpack(f2_fma(x, ks2, f2_add(ve2, f2_pack(__uint_as_float(f[j].z), __uint_as_float(f[j].w)))), a, b);
+                    s[2 * j] = __float_as_uint(okt ? a : NEG_INF);
+                    s[2 * j + 1] = __float_as_uint(okt ? b : NEG_INF);
+                }
+                tmem_ld16_nowait(t_l + ch * 16, l);
+                float t8[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t8[j] = fmaxf(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+                const float top = fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])), fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
+                vmax = fmaxf(vmax, top);
+                const bool sums = !__any_sync(0xffffffffu, top > FAR);
+                if (!sums) r.left_out |= 1u << ch;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[j] = __float_as_uint(ex2(__uint_as_float(s[j])));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[j] = pack_half2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+                const int col = col0 + ch * 16, unit = (col & 63) >> 3;
+                uint8_t* to = row + (size_t)(col >> 6) * 16384;
+                *reinterpret_cast<uint4*>(to + ((unit ^ (tok & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(to + (((unit + 1) ^ (tok & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                tmem_wait_ld();
+                if (sums) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float c, d;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), inv2,
+                                         f2_pack(__uint_as_float(l[2 * j]), __uint_as_float(l[2 * j + 1]))), c, d);
+                        l[2 * j] = __float_as_uint(c);
+                        l[2 * j + 1] = __float_as_uint(d);
+                    }
+                    tmem_st16_nowait(t_l + ch * 16, l);
+                }
+            }
+            fence_proxy_async_smem();
+            tmem_wait_st();
+        }
+        if (group_any(bar_id, fail || vmax > WINDOW)) {
+            r.stopped = true;
+            r.fail = fail;
+            return r;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.ready[it & 1]);
+    }
+    return r;
 }
 
 template <int DT, int D>
@@ -635,8 +754,24 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
         for (int tile = w.tile0; tile < w.tile1; ++tile, ++it) {
             if (dead) break;
             const bool first = tile == w.tile0, fresh = tile >= w.rq.ncache;
+            bool fail = false, stopped = false;
+            uint32_t left_out = first ? 0xffffffffu : 0u;
+            if (!first && !fresh) {
+                const RunEnd r = softmax_run(T, sh, smem + T.o_p + tok * 128, rb ? fr1 : fr0, tl, col0, nch, bar_id, it, tile,
+                                             min(w.tile1, w.rq.ncache), w.rq.len);
+                status = max(status, r.status);
+                tile += r.n;
+                it += r.n;
+                if (!r.stopped) {
+                    --tile;
+                    --it;
+                    continue;
+                }
+                stopped = true;
+                fail = r.fail;
+                left_out = r.left_out;
+            }
             uint8_t* pb = smem + T.o_p + (it % T.np) * T.p_buf;
-            bool fail = false;
             if (fresh) {
                 // q as halfs (the terms' sums) where P will be, and which rows each column sees
                 if (it >= 1) fail = !wait_warp(sh, &sh.pv[(it - 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit);
@@ -697,9 +832,9 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
                 if (!fail && lane == 0) mbar_arrive(&sh.own[it & 1]);
             }
 
-            fail = fail || !wait_warp(sh, &sh.sfull[it & 1], (it >> 1) & 1, T.wait_limit);
-            // where P has one buffer, its last use; of two, S^T's commit stands for the use before last, which it followed
-            if (!fresh && T.np == 1 && it >= 1) fail = fail || !wait_warp(sh, &sh.pv[(it - 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit);
+            // (a tile that the run stopped at has waited; a group's first tile may overwrite P once the last group's outputs are
+            // out, which waited for its O^T)
+            fail = fail || (!stopped && !wait_warp(sh, &sh.sfull[it & 1], (it >> 1) & 1, T.wait_limit));
             float ks = 1.0f, ve = 0.0f;
             bool okt = false, partial = true;
             const uint32_t ts = tl + (it & 1) * T.RN + col0;
@@ -737,25 +872,28 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
             // one repeats the weights; it adds to l only what the first left out: 16 columns of a warp one of whose
             // weights would have taken the sum out of fp32's range.
             float vmax = NEG_INF;
-            uint32_t left_out = first ? 0xffffffffu : 0u;
             const auto weights = [&](auto again) {
                 const float4* fr = rb ? fr1 : fr0;
 #pragma unroll 1
                 for (int ch = 0; ch < nch; ++ch) {
                     uint32_t s[16], l[16], h[8];
+                    uint4 f[8];
                     tmem_ld16_nowait(ts + ch * 16, s);
-                    if (!(again.value && first)) tmem_ld16_nowait(t_l + ch * 16, l);
+                    // all eight in flight at once, beside the scores: one after another they would set the loop's pace
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] = lds128(reinterpret_cast<const uint4*>(&fr[ch * 8 + j]));
                     const uint32_t see = partial ? seen16(ch) : 0xffffu;
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float4 f = fr[ch * 8 + j];
-                        const unsigned long long x = f2_mul(f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), f2_pack(f.x, f.y));
+                        const unsigned long long x = f2_mul(f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])),
+                                                            f2_pack(__uint_as_float(f[j].x), __uint_as_float(f[j].y)));
                         float a, b;
-                        f2_unpack(f2_fma(x, ks2, f2_add(ve2, f2_pack(f.z, f.w))), a, b);
+                        f2_unpack(f2_fma(x, ks2, f2_add(ve2, f2_pack(__uint_as_float(f[j].z), __uint_as_float(f[j].w)))), a, b);
                         s[2 * j] = __float_as_uint(a);
                         s[2 * j + 1] = __float_as_uint(b);
                     }
+                    if (!(again.value && first)) tmem_ld16_nowait(t_l + ch * 16, l);
                     if (partial) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) s[j] = see >> j & 1u ? s[j] : __float_as_uint(NEG_INF);
@@ -764,9 +902,10 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
                     if constexpr (again.value) {
                         sums = left_out >> ch & 1u;
                     } else {
-                        float top = NEG_INF;
+                        float t8[8];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) top = fmaxf(top, __uint_as_float(s[j]));
+                        for (int j = 0; j < 8; ++j) t8[j] = fmaxf(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+                        const float top = fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])), fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
                         vmax = fmaxf(vmax, top);
                         sums = !__any_sync(0xffffffffu, top > FAR);
                         if (!sums) left_out |= 1u << ch;
@@ -780,6 +919,7 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
                     const int unit = (col & 63) >> 3;
                     *reinterpret_cast<uint4*>(row + ((unit ^ (tok & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                     *reinterpret_cast<uint4*>(row + (((unit + 1) ^ (tok & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                    tmem_wait_ld();
                     if (sums) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
@@ -797,8 +937,8 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
                 tmem_wait_st();
             };
             // the first tile of a group has no reference yet
-            if (!fail && !first) weights(std::false_type{});
-            if (group_any(bar_id, fail || first || vmax > WINDOW)) {
+            if (!fail && !first && !stopped) weights(std::false_type{});
+            if (stopped || group_any(bar_id, fail || first || vmax > WINDOW)) {
                 if (group_any(bar_id, fail)) {
                     dead = true;
                     break;
