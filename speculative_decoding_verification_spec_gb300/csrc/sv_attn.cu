@@ -622,7 +622,7 @@ template <int DT, int D>
 cudaError_t launch_merge(const AttnParams& P, int ctas, int MR, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)min((MR + 1) / 2, 16));
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)((MR + 1) / 2));
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr;

@@ -51,9 +51,10 @@ struct TcParams {
     AttnParams A;
     int MR, RN;          // rows of a row tile; padded to a multiple of 16
     int stages, np, nv;  // ring stages; buffers of P and of the widened values (1 or 2)
-    uint32_t o_p, o_v, o_stage, v_buf, p_buf;  // offsets in dynamic shared memory, sizes
-    bool qvec, kvec, vvec;  // rows that allow loads of D / 32 elements at once
+    uint32_t o_p, o_v, o_kh, o_stage, v_buf, p_buf;  // offsets in dynamic shared memory, sizes
+    bool qvec, kvec, vvec;  // rows that allow wide loads: 16 bytes of q, D / 32 elements of the others
     int wait_limit;
+    uint64_t inv_g;      // r / G = r * inv_g >> 32 for the rows of a head: a division costs a role hundreds of cycles
 };
 
 // ---------------------------------------------------------------- tcgen05
@@ -105,6 +106,16 @@ __device__ __forceinline__ void tmem_ld16_nowait(uint32_t addr, uint32_t (&r)[16
                    "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                  : "r"(addr));
 }
+// 4 columns
+__device__ __forceinline__ void tmem_ld4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4]; tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t addr, const uint32_t (&r)[4])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st16_nowait(uint32_t addr, const uint32_t (&r)[16])
@@ -137,9 +148,10 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes)
 
 struct Shared {
     uint64_t full[MAXSTAGES], empty[MAXSTAGES];
+    uint64_t info[MAXSTAGES];     // the stage's pages and scales are there
     uint64_t sfull[2], ready[2], pv[2], own[2], qfull, done;
     float2 scale[MAXSTAGES][8];   // of the stage's pages: keys, values
-    int status[MAXSTAGES];
+    int status[MAXSTAGES], page[MAXSTAGES][8];
     float4 fr[2][MAXR / 2];       // per pair of columns: factors, references negated; two copies, one being rewritten
     float wred[NG][4][MAXC];      // column maxima and sums of the softmax warps
     float4 col[NG][MAXC];         // a moved reference's factors; the outputs' columns
@@ -172,7 +184,7 @@ __device__ __noinline__ bool wait_on(Shared& sh, uint64_t* bar, uint32_t parity,
 }
 __device__ __forceinline__ bool wait_warp(Shared& sh, uint64_t* bar, uint32_t parity, int limit)
 {
-    return __all_sync(0xffffffffu, wait_on(sh, bar, parity, limit));
+    return __all_sync(0xffffffffu, (limit > 0 && mbar_wait(bar, parity, 1)) || wait_on(sh, bar, parity, limit));
 }
 
 __device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" :: "r"(id) : "memory"); }
@@ -195,7 +207,7 @@ struct Walk {
     int h, rt, tile0, tile1;
     bool whole, first;
 
-    __device__ __noinline__ Walk(const AttnParams& P, const Place& at)
+    __device__ __forceinline__ Walk(const AttnParams& P, const Place& at)
     {
         u = at.total * blockIdx.x / at.ctas;
         u1 = at.total * (blockIdx.x + 1) / at.ctas;
@@ -206,7 +218,7 @@ struct Walk {
         first = true;
     }
     __device__ bool more() const { return u < u1; }
-    __device__ __noinline__ void open()
+    __device__ __forceinline__ void open()
     {
         const long long rem = u - pre;
         const int grp = (int)(rem / rq.n);
@@ -216,7 +228,7 @@ struct Walk {
         tile1 = (int)min((long long)rq.n, tile0 + (u1 - u));
         whole = tile0 == 0 && tile1 == rq.n;
     }
-    __device__ __noinline__ void next(const AttnParams& P)
+    __device__ __forceinline__ void next(const AttnParams& P)
     {
         first = false;
         u += tile1 - tile0;
@@ -234,58 +246,67 @@ __device__ void role_copy(const TcParams& T, Shared& sh, const Place& at, uint32
 {
     const AttnParams& P = T.A;
     const int lane = threadIdx.x & 31;
-    const int ppt = TT / P.page;           // pages of a tile
-    const int per = 32 / ppt;              // tiles whose pages the warp's lanes hold at once
+    const int ppt = TT >> P.page_shift;    // pages of a tile
+    const int per = 32 >> (7 - P.page_shift);  // tiles whose pages the warp's lanes hold at once
+    const int my_tile = lane >> (7 - P.page_shift), my_page = lane & (ppt - 1);
     constexpr uint32_t KB = TT * D;
-    int it = 0;
+    int it = 0, s = 0, par = 1;  // tiles so far, the next stage and the parity of its last use's end
     bool ok = true;
     for (Walk w(P, at); ok && w.more(); w.next(P)) {
         w.open();
         const int32_t* table = P.page_table + (size_t)w.b * P.table_width;
-        const int c0 = min(w.tile0, w.rq.ncache), c1 = min(w.tile1, w.rq.ncache);
-        // lane k holds page k of a batch of `per` tiles: its number, and a batch ahead the next one's
-        const auto page_of = [&](int tile) {
-            const long long tok = (long long)tile * TT + (long long)lane * P.page;
-            return tile < c1 && tok < w.rq.len ? __ldg(table + (tok >> P.page_shift)) : 0;
-        };
-        int page = 0, ahead = c0 < c1 ? page_of(c0) : 0;
-        float ks = 1.0f, vs = 1.0f;
+        const int c0 = min(w.tile0, w.rq.ncache), c1 = min(w.tile1, w.rq.ncache), len = w.rq.len;
+        // Lane k holds page k of a batch of `per` tiles with its scales.  Two batches ahead the page numbers are loaded, one
+        // ahead the scales, so that neither is waited for in the loop.
+        const auto live_at = [&](int tile) { return tile + my_tile < c1 && (long long)tile * TT + (long long)lane * P.page < len; };
+        const auto page_of = [&](int tile) { return live_at(tile) ? __ldg(table + (((long long)tile * TT + (long long)lane * P.page) >> P.page_shift)) : -1; };
+        const auto block_of = [&](int page) { return (unsigned)page < (unsigned)P.pages ? (size_t)page * P.Hkv + w.h : 0; };
+        int page = -1, page1 = page_of(c0), page2 = page_of(c0 + per);
+        float ks = 1.0f, vs = 1.0f, ks1 = __ldg(P.ks + block_of(page1)), vs1 = __ldg(P.vs + block_of(page1));
         for (int tile = w.tile0; tile < w.tile1; ++tile, ++it) {
-            const int s = it % T.stages;
-            if (it >= T.stages && !wait_warp(sh, &sh.empty[s], ((it / T.stages) & 1) ^ 1, T.wait_limit)) {
+            // (a stage's first use asks for the phase before the first, which counts as over)
+            if (!wait_warp(sh, &sh.empty[s], par, T.wait_limit)) {
                 ok = false;
                 break;
             }
             if (tile < c1) {
-                const int at_lane = (tile - c0) % per * ppt;
-                if (at_lane == 0) {
-                    page = ahead;
-                    const bool good = (unsigned)page < (unsigned)P.pages;
-                    const size_t blk = good ? (size_t)page * P.Hkv + w.h : 0;
-                    const bool live = (long long)tile * TT + (long long)lane * P.page < w.rq.len && tile + lane / ppt < c1;
-                    ks = live ? __ldg(P.ks + blk) : 1.0f;
-                    vs = live ? __ldg(P.vs + blk) : 1.0f;
-                    ahead = page_of(tile + per);
+                const int k = (tile - c0) & (per - 1);
+                if (k == 0) {
+                    page = page1;
+                    ks = ks1;
+                    vs = vs1;
+                    page1 = page2;
+                    ks1 = __ldg(P.ks + block_of(page1));
+                    vs1 = __ldg(P.vs + block_of(page1));
+                    page2 = page_of(tile + 2 * per);
                 }
-                const int live_pages = min(ppt, (w.rq.len - tile * TT + P.page - 1) >> P.page_shift);
-                const bool mine = lane >= at_lane && lane < at_lane + live_pages;
-                const bool good = (unsigned)page < (unsigned)P.pages;
-                const unsigned use = __ballot_sync(0xffffffffu, mine && good);
-                if (lane == 0) mbar_expect(&sh.full[s], (uint32_t)__popc(use) * 2u * (uint32_t)(P.page * D));
+                const bool mine = my_tile == k && live_at(tile - k);
+                const bool good = mine && (unsigned)page < (unsigned)P.pages;
+                const unsigned use = __ballot_sync(0xffffffffu, good), want = __ballot_sync(0xffffffffu, mine);
+                if (lane == 0) {
+                    mbar_expect(&sh.full[s], (uint32_t)__popc(use) * (uint32_t)(P.page * D));
+                    sh.status[s] = use != want ? ROW_BAD_PAGE : ROW_OK;
+                }
                 __syncwarp();
-                if (mine && good) {
-                    const uint32_t dst = ring + s * 2 * KB + (lane - at_lane) * P.page * D;
-                    tma_page(dst, mk, page * P.Hkv + w.h, &sh.full[s]);
-                    tma_page(dst + KB, mv, page * P.Hkv + w.h, &sh.full[s]);
+                if (mine) {
+                    sh.scale[s][my_page] = make_float2(ks, vs);
+                    sh.page[s][my_page] = good ? page : -1;
                 }
-                if (mine) sh.scale[s][lane - at_lane] = make_float2(ks, vs);
-                const bool bad = __any_sync(0xffffffffu, mine && !good);
-                if (lane == 0) sh.status[s] = bad ? ROW_BAD_PAGE : ROW_OK;
+                if (good) {
+                    tma_page(ring + s * KB + my_page * P.page * D, mk, page * P.Hkv + w.h, &sh.full[s]);
+                    // the values go from L2 to the registers of the warps that widen them, some tiles later
+                    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
+                                 :: "l"(mv), "r"(0), "r"(0), "r"(page * P.Hkv + w.h) : "memory");
+                }
             } else if (lane == 0) {
                 sh.status[s] = ROW_OK;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.full[s]);
+            if (lane == 0) {
+                mbar_arrive(&sh.info[s]);
+                mbar_arrive(&sh.full[s]);
+            }
+            if (++s == T.stages) s = 0, par ^= 1;
         }
     }
     // no copy may be in flight when the CTA ends: the last fill of every stage
@@ -313,6 +334,7 @@ __device__ void role_mma(const TcParams& T, Shared& sh, const Place& at, uint32_
     int it = 0, stage = 0, stage_par = 0, seg = 0;
     uint32_t own = 0;                                        // phases of the two barriers of the rounds' rows
     int pending = 0, pending_first = 0, ok = 1;              // pending: O^T of the tile before is still to be issued
+    int have = 0;                                            // the next tile's codes have been waited for
 
     const auto pv = [&]() {  // O^T of the tile before
         const int i = it - 1;
@@ -345,7 +367,7 @@ __device__ void role_mma(const TcParams& T, Shared& sh, const Place& at, uint32_
                 if (pending) ok = pv();
                 continue;
             }
-            ok = ok && uni(wait_warp(sh, &sh.full[stage], stage_par, T.wait_limit));
+            if (!have) ok = ok && uni(wait_warp(sh, &sh.full[stage], stage_par, T.wait_limit));
             if (first) ok = ok && uni(wait_warp(sh, &sh.qfull, seg & 1, T.wait_limit));
             if (fresh) {
                 ok = ok && uni(wait_warp(sh, &sh.own[it & 1], own >> (it & 1) & 1, T.wait_limit));
@@ -353,7 +375,7 @@ __device__ void role_mma(const TcParams& T, Shared& sh, const Place& at, uint32_
             }
             if (!ok) continue;
             tc_fence_after();
-            const uint32_t ts = tmem + (it & 1) * T.RN, kb = ring + stage * 2 * KB;
+            const uint32_t ts = tmem + (it & 1) * T.RN, kb = ring + stage * KB;
             if (!fresh) {
                 const uint32_t a = desc_lo(kb, 16), b = desc_lo(base, 16);
                 if (elected()) {
@@ -366,7 +388,7 @@ __device__ void role_mma(const TcParams& T, Shared& sh, const Place& at, uint32_
                     mma_commit(&sh.empty[stage]);
                 }
             } else {
-                const uint32_t a = desc_lo(kb, 16), b = desc_lo(sp + (T.np == 2 ? it & 1 : 0) * T.p_buf, 16);
+                const uint32_t a = desc_lo(base + T.o_kh, 16), b = desc_lo(sp + (T.np == 2 ? it & 1 : 0) * T.p_buf, 16);
                 if (elected()) {
 #pragma unroll 2
                     for (int k = 0; k < D / 16; ++k)
@@ -377,12 +399,15 @@ __device__ void role_mma(const TcParams& T, Shared& sh, const Place& at, uint32_
                 }
             }
             __syncwarp();
+            // the next tile's codes, while the weights are still being computed
+            if (++stage == T.stages) stage = 0, stage_par ^= 1;
+            have = tile + 1 < tile1;
+            if (have) ok = uni(wait_warp(sh, &sh.full[stage], stage_par, T.wait_limit));
             }
             if (!ok) break;
             pending = 1;
             pending_first = first;
             ++it;
-            if (++stage == T.stages) stage = 0, stage_par ^= 1;
         }
     }
     if (ok && pending) (void)pv();
@@ -443,127 +468,175 @@ __device__ __forceinline__ void load_run(const void* p, int64_t i, bool vec, flo
     }
 }
 
-// the values of one tile of the cache, codes to halfs; tokens from `valid` on become zeros, whatever their slots hold
+// A thread's share of a tile's values: 16 codes each of up to VPT (token, channel) places.
+constexpr int VTHREADS = VWN * 32;
 template <int D>
-__device__ __noinline__ void widen_tile(const uint8_t* codes, uint8_t* vb, int ct, int valid)
+struct Codes {
+    static constexpr int CH = D / 16, N = (TT * CH + VTHREADS - 1) / VTHREADS;
+    uint4 x[N];
+};
+
+// Loads them; tokens from `valid` on, and those of a page that is none, are zeros.
+template <int D>
+__device__ __forceinline__ void load_codes(Codes<D>& c, const AttnParams& P, const int* pages, int h, int ct, int valid)
 {
-    constexpr int CH = D / 16, U = 3;
-#pragma unroll 1
-    for (int i0 = ct; i0 < TT * CH; i0 += U * VWN * 32) {
-        uint4 x[U];
+    constexpr int CH = D / 16;
 #pragma unroll
-        for (int q = 0; q < U; ++q) {
-            const int i = i0 + q * VWN * 32;
-            x[q] = make_uint4(0, 0, 0, 0);
-            if (i < TT * CH && i / CH < valid) x[q] = *reinterpret_cast<const uint4*>(codes + i * 16);
-        }
-#pragma unroll
-        for (int q = 0; q < U; ++q) {
-            const int i = i0 + q * VWN * 32, tok = i / CH, ch = i % CH;
-            if (i >= TT * CH) break;
-            const uint32_t u[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
-            uint32_t y[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                y[2 * k] = e4m3x2_to_half2((uint16_t)u[k]);
-                y[2 * k + 1] = e4m3x2_to_half2((uint16_t)(u[k] >> 16));
-            }
-            const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-            // the two blocks of 64 channels start with opposite halves, so a quarter-warp's stores meet no bank twice
-            const int f = ch >> 2;
-            *reinterpret_cast<uint4*>(vb + half_off(tok, ch * 16 + 8 * f)) = f ? hi : lo;
-            *reinterpret_cast<uint4*>(vb + half_off(tok, ch * 16 + 8 * (f ^ 1))) = f ? lo : hi;
+    for (int q = 0; q < Codes<D>::N; ++q) {
+        const int i = ct + q * VTHREADS, tok = i / CH;
+        c.x[q] = make_uint4(0, 0, 0, 0);
+        if (i < TT * CH && tok < valid) {
+            const int page = pages[tok >> P.page_shift];
+            if (page >= 0)
+                c.x[q] = ld_stream_v4(P.vc + ((((size_t)page * P.Hkv + h) << P.page_shift) + (tok & (P.page - 1))) * D + (i % CH) * 16);
         }
     }
 }
 
+template <int D>
+__device__ __forceinline__ void store_halfs(const Codes<D>& c, uint8_t* vb, int ct)
+{
+    constexpr int CH = D / 16;
+#pragma unroll
+    for (int q = 0; q < Codes<D>::N; ++q) {
+        const int i = ct + q * VTHREADS, tok = i / CH, ch = i % CH;
+        if (i >= TT * CH) break;
+        const uint32_t u[4] = {c.x[q].x, c.x[q].y, c.x[q].z, c.x[q].w};
+        uint32_t y[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            y[2 * k] = e4m3x2_to_half2((uint16_t)u[k]);
+            y[2 * k + 1] = e4m3x2_to_half2((uint16_t)(u[k] >> 16));
+        }
+        const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+        // the two blocks of 64 channels start with opposite halves, so a quarter-warp's stores meet no bank twice
+        const int f = ch >> 2;
+        *reinterpret_cast<uint4*>(vb + half_off(tok, ch * 16 + 8 * f)) = f ? hi : lo;
+        *reinterpret_cast<uint4*>(vb + half_off(tok, ch * 16 + 8 * (f ^ 1))) = f ? lo : hi;
+    }
+}
+
+// The round's rows of one tile: keys into the stage, values into the buffer, as halfs scaled by a power of two per token.  True
+// when a value is not finite.
+template <int DT, int D>
+__device__ __forceinline__ bool own_rows(const TcParams& T, Shared& sh, uint8_t* kb, uint8_t* vb, int it, int b, int h, int j0, int rows)
+{
+    const AttnParams& P = T.A;
+    constexpr int EPL = D / 32;
+    const int ct = threadIdx.x - VW0 * 32, wv = ct >> 5, lane = ct & 31;
+    const int live = P.kn ? min(max(rows - j0, 0), TT) : 0;
+#pragma unroll 1
+    for (int i = ct; i < TT * (D / 8); i += VWN * 32)  // tokens that are none: zero values
+        if (i / (D / 8) >= live) *reinterpret_cast<uint4*>(vb + half_off(i / (D / 8), i % (D / 8) * 8)) = make_uint4(0, 0, 0, 0);
+    if (ct < TT && ct >= live) sh.fks[it & 1][ct] = 1.0f, sh.fve[it & 1][ct] = 0.0f;
+    bool vbad = false;
+#pragma unroll 1
+    for (int i = wv; i < live; i += VWN) {
+        const int64_t j = j0 + i;
+        float x[2][EPL];
+        load_run<DT, EPL>(P.kn, b * P.kb + j * P.kt + h * P.kh + lane * EPL, T.kvec, x[0]);
+        load_run<DT, EPL>(P.vn, b * P.vb + j * P.vt + h * P.vh + lane * EPL, T.vvec, x[1]);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            float amax = 0.0f;
+            bool fin = true;
+#pragma unroll
+            for (int k = 0; k < EPL; ++k) {
+                if (fabsf(x[which][k]) < __int_as_float(0x7f800000)) amax = fmaxf(amax, fabsf(x[which][k]));
+                else fin = false, x[which][k] = 0.0f;
+            }
+            fin = __all_sync(0xffffffffu, fin);
+            amax = warp_max(amax);
+            const int e = min(max(exponent_of(amax), CACHE_E_MIN), 126) - 14;
+            const float mul = exp2_int(-e);
+            uint8_t* to = (which ? vb : kb) + half_off(i, lane * EPL);
+            if constexpr (EPL == 4)
+                *reinterpret_cast<uint2*>(to) = make_uint2(pack_half2(x[which][0] * mul, x[which][1] * mul),
+                                                           pack_half2(x[which][2] * mul, x[which][3] * mul));
+            else
+                *reinterpret_cast<uint32_t*>(to) = pack_half2(x[which][0] * mul, x[which][1] * mul);
+            if (which) vbad = vbad || !fin;
+            if (lane == 0) {
+                if (which) sh.fve[it & 1][i] = (float)e;
+                else sh.fks[it & 1][i] = fin ? exp2_int(e) : __int_as_float(0x7fc00000);  // a key that is not finite: NaN
+            }
+        }
+    }
+    return vbad;
+}
+
+// The next tile's codes are loaded into registers before this tile's are widened.
 template <int DT, int D>
 __device__ void role_values(const TcParams& T, Shared& sh, const Place& at, uint8_t* smem)
 {
     const AttnParams& P = T.A;
-    constexpr int KB = TT * D, EPL = D / 32;
     const int ct = threadIdx.x - VW0 * 32, wv = ct >> 5, lane = ct & 31;
-    int it = 0;
+    int it = 0, s = 0, par = 0;  // s, par: stage and phase of the tile after the loaded one
     bool ok = true;
     for (Walk w(P, at); ok && w.more(); w.next(P)) {
         w.open();
-        for (int tile = w.tile0; tile < w.tile1; ++tile, ++it) {
-            const int s = it % T.stages;
-            uint8_t* vb = smem + T.o_v + (it % T.nv) * T.v_buf;
-            uint8_t* kb = smem + T.o_stage + s * 2 * KB;
-            ok = wait_warp(sh, &sh.full[s], (it / T.stages) & 1, T.wait_limit);
-            if (it >= T.nv) ok = ok && wait_warp(sh, &sh.pv[(it - T.nv) & 1], ((it - T.nv) >> 1) & 1, T.wait_limit);
+        Codes<D> c;
+        const auto fetch = [&](int tile) {
+            ok = ok && wait_warp(sh, &sh.info[s], par, T.wait_limit);
+            if (ok && tile < w.rq.ncache) load_codes<D>(c, P, sh.page[s], w.h, ct, w.rq.len - tile * TT);
+        };
+        fetch(w.tile0);
+#pragma unroll 1
+        for (int tile = w.tile0; ok && tile < w.tile1; ++tile, ++it) {
+            uint8_t* vb = smem + T.o_v + (T.nv == 2 ? it & 1 : 0) * T.v_buf;
+            const bool own = tile >= w.rq.ncache;
+            Codes<D> now = c;
+            // the stage may be filled again once its pages are read: this is the codes' own end of it
+            __syncwarp();
+            if (lane == 0 && ok) mbar_arrive(&sh.empty[s]);
+            if (++s == T.stages) s = 0, par ^= 1;
+            if (tile + 1 < w.tile1) fetch(tile + 1);
+            // the buffer's last use (the first ones ask for a phase before the first, which counts as over)
+            ok = ok && wait_warp(sh, &sh.pv[(it + T.nv) & 1], ((it - T.nv) >> 1) & 1, T.wait_limit);
             if (!ok) break;
-            if (tile < w.rq.ncache) {
-                const int valid = w.rq.len - tile * TT;
-                widen_tile<D>(kb + KB, vb, ct, valid);
-            } else {
-                // the round's rows: keys into the stage, values into the buffer, scaled by a power of two per token
-                const int j0 = (tile - w.rq.ncache) * TT, live = P.kn ? min(max(w.rq.rows - j0, 0), TT) : 0;
-                for (int i = ct; i < TT * (D / 8); i += VWN * 32)  // tokens that are none: zero values
-                    if (i / (D / 8) >= live) *reinterpret_cast<uint4*>(vb + half_off(i / (D / 8), i % (D / 8) * 8)) = make_uint4(0, 0, 0, 0);
-                for (int i = ct; i < TT; i += VWN * 32)
-                    if (i >= live) sh.fks[it & 1][i] = 1.0f, sh.fve[it & 1][i] = 0.0f;
-                bool vbad = false;
-                for (int i = wv; i < live; i += VWN) {
-                    const int64_t j = j0 + i;
-                    float x[2][EPL];
-                    load_run<DT, EPL>(P.kn, w.b * P.kb + j * P.kt + w.h * P.kh + lane * EPL, T.kvec, x[0]);
-                    load_run<DT, EPL>(P.vn, w.b * P.vb + j * P.vt + w.h * P.vh + lane * EPL, T.vvec, x[1]);
-#pragma unroll
-                    for (int which = 0; which < 2; ++which) {
-                        float amax = 0.0f;
-                        bool fin = true;
-#pragma unroll
-                        for (int k = 0; k < EPL; ++k) {
-                            if (fabsf(x[which][k]) < __int_as_float(0x7f800000)) amax = fmaxf(amax, fabsf(x[which][k]));
-                            else fin = false, x[which][k] = 0.0f;
-                        }
-                        fin = __all_sync(0xffffffffu, fin);
-                        amax = warp_max(amax);
-                        const int e = min(max(exponent_of(amax), CACHE_E_MIN), 126) - 14;
-                        const float mul = exp2_int(-e);
-                        uint8_t* to = (which ? vb : kb) + half_off(i, lane * EPL);
-                        if constexpr (EPL == 4)
-                            *reinterpret_cast<uint2*>(to) = make_uint2(pack_half2(x[which][0] * mul, x[which][1] * mul),
-                                                                       pack_half2(x[which][2] * mul, x[which][3] * mul));
-                        else
-                            *reinterpret_cast<uint32_t*>(to) = pack_half2(x[which][0] * mul, x[which][1] * mul);
-                        if (which) vbad = vbad || !fin;
-                        if (lane == 0) {
-                            if (which) sh.fve[it & 1][i] = (float)e;
-                            else sh.fks[it & 1][i] = fin ? exp2_int(e) : __int_as_float(0x7fc00000);  // a key that is not finite: NaN
-                        }
-                    }
-                }
+            if (own) {
+                const bool vbad = own_rows<DT, D>(T, sh, smem + T.o_kh, vb, it, w.b, w.h, (tile - w.rq.ncache) * TT, w.rq.rows);
                 if (lane == 0) sh.vbad[it & 3][wv] = vbad;
+            } else {
+                store_halfs<D>(now, vb, ct);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                if (tile >= w.rq.ncache) mbar_arrive(&sh.own[it & 1]);
+                if (own) mbar_arrive(&sh.own[it & 1]);
                 mbar_arrive(&sh.ready[it & 1]);
-                mbar_arrive(&sh.empty[s]);
             }
         }
     }
 }
 
-// v[c] over the warp's lanes, for 16 columns at once: half of the columns travel at each step.  Column lane / 2's result in v[0].
-template <class Op>
-__device__ __forceinline__ float reduce16(float (&v)[16], int lane, Op op)
+// The sum of the values of channel d that are not finite over the rows that row t sees: products with a weight of zero would
+// carry them to every row, so they are kept out of the product and added to the rows that see them.
+template <int DT>
+__device__ __noinline__ float unfinite_values(const AttnParams& P, int b, int h, int t, int d)
 {
-#pragma unroll
-    for (int n = 8, bit = 16; n; n >>= 1, bit >>= 1) {
-        const bool up = lane & bit;
-#pragma unroll
-        for (int k = 0; k < n; ++k) {
-            const float send = up ? v[k] : v[k + n], keep = up ? v[k + n] : v[k];
-            v[k] = op(keep, __shfl_xor_sync(0xffffffffu, send, bit));
-        }
+    float add = 0.0f;
+#pragma unroll 1
+    for (int cur = t;;) {
+        const float y = load_elem<DT>(P.vn, b * P.vb + cur * P.vt + h * P.vh + d);
+        if (!(fabsf(y) < __int_as_float(0x7f800000))) add += y;
+        if (cur == 0) break;
+        const int p = P.parents ? __ldg(P.parents + (size_t)b * (P.T - 1) + cur - 1) : cur - 2;
+        if (p < -1 || p >= cur - 1) break;
+        cur = p + 1;
     }
-    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+    return add;
 }
+
+__device__ __forceinline__ int row_token(const TcParams& T, int r) { return (int)((uint64_t)(uint32_t)r * T.inv_g >> 32); }
+
+// What a thread of a softmax group keeps for the kernel's life.
+struct Lane {
+    uint8_t* smem;
+    uint32_t tl;            // this warp's lanes of tensor memory
+    int g, quad, lane, tok; // group, warp of the group, lane; this thread's token of a tile and channel of O^T
+    int bar_id, col0, nch;  // the group's barrier, first column and 16-column chunks
+};
 
 // What softmax_run stopped at.
 struct RunEnd {
@@ -573,42 +646,61 @@ struct RunEnd {
     bool stopped, fail;
 };
 
-// The softmax over a group's ordinary tiles: of the cache, with a reference.  One pass per tile; the run ends where a weight
-// passes the window (for any thread of the group) or a wait runs out.  A function of its own, so that the loop's code is one
-// piece.
-__device__ __noinline__ RunEnd softmax_run(const TcParams& T, Shared& sh, uint8_t* prow, const float4* fr, uint32_t tl, int col0, int nch,
-                                           int bar_id, int it, int tile, int end, int len)
+// Scale of the keys and scale exponent of the values of this thread's token, and the columns that see it (bit c: column c
+// of the group).
+__device__ __forceinline__ void token_terms(const Shared& sh, const Lane& L, int it, int s_at, int page_shift, int left, bool own, uint64_t see_own,
+                                            float& ks, float& ve, uint64_t& see)
 {
-    const int lane = threadIdx.x & 31, tok = ((threadIdx.x >> 5) & 3) * 32 + lane;
+    ks = 1.0f;
+    ve = 0.0f;
+    if (own) {
+        ks = sh.fks[it & 1][L.tok];
+        ve = sh.fve[it & 1][L.tok];
+        see = see_own;
+    } else {
+        see = 0;
+        if (L.tok < left) {
+            const float2 sc = sh.scale[s_at][L.tok >> page_shift];
+            ks = sc.x;
+            ve = (float)exponent_of(sc.y);
+            see = ~0ull;
+        }
+    }
+}
+
+// The softmax over tiles that have a reference: tiles of the cache in a row, or (own) one of the round's rows.  One pass per
+// tile; the run ends where a weight passes the window (for any thread of the group) or a wait runs out.  `take`: chunks whose
+// sums the first tile adds to l.  A function of its own, as compact as it can be: it is nearly all of the kernel's time, and
+// what does not fit the instruction cache waits for its code at every step.
+__device__ __forceinline__ RunEnd softmax_run(const TcParams& T, Shared& sh, const Lane L, const float4* fr, int it, int s_at, int tile, int end, int len,
+                                           bool own, uint64_t see_own, uint32_t take)
+{
     const int RN = T.RN, np = T.np, limit = T.wait_limit, stages = T.stages, page_shift = T.A.page_shift;
-    const uint32_t p_buf = T.p_buf, t_l = tl + 3 * RN + col0;
-    int s_at = it % stages;
+    const uint32_t p_buf = T.p_buf, t_l = L.tl + 3 * RN + L.col0;
+    uint8_t* const prow = L.smem + T.o_p + L.tok * 128;
     RunEnd r = {0, ROW_OK, 0u, false, false};
 #pragma unroll 1
     for (; tile < end; ++tile, ++it, ++r.n) {
         bool fail = !wait_warp(sh, &sh.sfull[it & 1], (it >> 1) & 1, limit);
-        // where P has one buffer, its last use; of two, S^T's commit stands for the use before last, which it followed
-        if (np == 1) fail = fail || !wait_warp(sh, &sh.pv[(it - 1) & 1], ((it - 1) >> 1) & 1, limit);
+        // Where P has one buffer, its last use; of two, S^T's commit stands for the use before last, which it followed.  (The
+        // kernel's first tile finds it free, and asks for a phase before the first, which counts as over.)
+        if (np == 1) fail = fail || !wait_warp(sh, &sh.pv[(it + 1) & 1], ((it - 1) >> 1) & 1, limit);
         float vmax = NEG_INF;
         r.left_out = 0;
         if (!fail) {
             tc_fence_after();
-            const int left = len - tile * TT;
-            const bool okt = tok < left;
-            float ks = 1.0f, ve = 0.0f;
-            if (okt) {
-                const float2 sc = sh.scale[s_at][tok >> page_shift];
-                ks = sc.x;
-                ve = (float)exponent_of(sc.y);
-            }
-            r.status = max(r.status, sh.status[s_at]);
+            float ks, ve;
+            uint64_t see;
+            token_terms(sh, L, it, s_at, page_shift, len - tile * TT, own, see_own, ks, ve, see);
+            r.status = max(r.status, own ? 0 : sh.status[s_at]);
             if (++s_at == stages) s_at = 0;
+            const bool some = __any_sync(0xffffffffu, see != ~0ull);
             const float inv = exp2_int(min(max(-(int)ve, -126), 127));
             const unsigned long long ks2 = f2_pack(ks, ks), ve2 = f2_pack(ve, ve), inv2 = f2_pack(inv, inv);
-            const uint32_t ts = tl + (it & 1) * RN + col0;
+            const uint32_t ts = L.tl + (it & 1) * RN + L.col0;
             uint8_t* row = prow + (np == 2 ? it & 1 : 0) * p_buf;
 #pragma unroll 1
-            for (int ch = 0; ch < nch; ++ch) {
+            for (int ch = 0; ch < L.nch; ++ch) {
                 uint32_t s[16], l[16], h[8];
                 uint4 f[8];
                 tmem_ld16_nowait(ts + ch * 16, s);
@@ -622,27 +714,32 @@ __device__ __noinline__ RunEnd softmax_run(const TcParams& T, Shared& sh, uint8_
                                                         f2_pack(__uint_as_float(f[j].x), __uint_as_float(f[j].y)));
                     float a, b;
                     f2_unpack(f2_fma(x, ks2, f2_add(ve2, f2_pack(__uint_as_float(f[j].z), __uint_as_float(f[j].w)))), a, b);
-                    s[2 * j] = __float_as_uint(okt ? a : NEG_INF);
-                    s[2 * j + 1] = __float_as_uint(okt ? b : NEG_INF);
+                    s[2 * j] = __float_as_uint(a);
+                    s[2 * j + 1] = __float_as_uint(b);
                 }
                 tmem_ld16_nowait(t_l + ch * 16, l);
+                if (some) {
+                    const uint32_t m = (uint32_t)(see >> (16 * ch));
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) s[j] = m >> j & 1u ? s[j] : __float_as_uint(NEG_INF);
+                }
                 float t8[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) t8[j] = fmaxf(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
                 const float top = fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])), fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
                 vmax = fmaxf(vmax, top);
-                const bool sums = !__any_sync(0xffffffffu, top > FAR);
-                if (!sums) r.left_out |= 1u << ch;
+                const bool far = __any_sync(0xffffffffu, top > FAR);
+                if (far) r.left_out |= 1u << ch;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) s[j] = __float_as_uint(ex2(__uint_as_float(s[j])));
 #pragma unroll
                 for (int j = 0; j < 8; ++j) h[j] = pack_half2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
-                const int col = col0 + ch * 16, unit = (col & 63) >> 3;
+                const int col = L.col0 + ch * 16, unit = (col & 63) >> 3;
                 uint8_t* to = row + (size_t)(col >> 6) * 16384;
-                *reinterpret_cast<uint4*>(to + ((unit ^ (tok & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(to + (((unit + 1) ^ (tok & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                *reinterpret_cast<uint4*>(to + ((unit ^ (L.tok & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(to + (((unit + 1) ^ (L.tok & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
                 tmem_wait_ld();
-                if (sums) {
+                if (!far && (take >> ch & 1u)) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         float c, d;
@@ -654,451 +751,372 @@ __device__ __noinline__ RunEnd softmax_run(const TcParams& T, Shared& sh, uint8_
                     tmem_st16_nowait(t_l + ch * 16, l);
                 }
             }
+            take = ~0u;
             fence_proxy_async_smem();
             tmem_wait_st();
         }
-        if (group_any(bar_id, fail || vmax > WINDOW)) {
+        if (group_any(L.bar_id, fail || vmax > WINDOW)) {
             r.stopped = true;
             r.fail = fail;
             return r;
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.ready[it & 1]);
+        if (L.lane == 0) {
+            mbar_arrive(&sh.ready[it & 1]);
+            mbar_arrive(&sh.empty[s_at == 0 ? stages - 1 : s_at - 1]);
+        }
     }
     return r;
+}
+
+// The reference of the columns that tile `it` takes past the window (or that have none): at 2^HEAD under the maximum; the sums so
+// far follow.  False when a wait ran out.  All of the group calls it.
+__device__ __forceinline__ bool move_reference(const TcParams& T, Shared& sh, const Lane L, int rb, int it, int s_at, int left, bool own, uint64_t see_own, bool first)
+{
+    const float4* fr = &sh.fr[rb][L.col0 / 2];
+    float4* to = &sh.fr[rb ^ 1][L.col0 / 2];
+    const uint32_t t_s = L.tl + (it & 1) * T.RN + L.col0, t_o = L.tl + 2 * T.RN + L.col0, t_l = t_o + T.RN;
+    const int cw = L.nch * 16;
+    const bool ok = wait_warp(sh, &sh.sfull[it & 1], (it >> 1) & 1, T.wait_limit) &&
+                    // O^T of the tile before has to be whole before it is rescaled
+                    (first || wait_warp(sh, &sh.pv[(it + 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit));
+    if (ok) {
+        tc_fence_after();
+        float ks, ve;
+        uint64_t see;
+        token_terms(sh, L, it, s_at, T.A.page_shift, left, own, see_own, ks, ve, see);
+#pragma unroll 1
+        for (int c = 0; c < cw; c += 4) {
+            uint32_t s[4];
+            tmem_ld4(t_s + c, s);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float F = reinterpret_cast<const float*>(&fr[(c + j) >> 1])[j & 1];
+                const float x = see >> (c + j) & 1ull ? fmaf(__uint_as_float(s[j]) * F, ks, ve) : NEG_INF;
+                const float m = warp_max(x);
+                if (L.lane == 0) sh.wred[L.g][L.quad][c + j] = m;
+            }
+        }
+    }
+    if (group_any(L.bar_id, !ok)) return false;
+    if (L.tok < cw) {
+        const float(*w)[MAXC] = sh.wred[L.g];
+        const float top = fmaxf(fmaxf(w[0][L.tok], w[1][L.tok]), fmaxf(w[2][L.tok], w[3][L.tok]));
+        // a column that has seen nothing yet keeps the reference 0, which its zero sums do not feel
+        const float* f = reinterpret_cast<const float*>(&fr[L.tok >> 1]);
+        float* n = reinterpret_cast<float*>(&to[L.tok >> 1]);
+        const float was = first ? 0.0f : -f[2 + (L.tok & 1)];
+        const bool none = first || sh.unseen[L.g][L.tok] != 0.0f;
+        const bool move = none ? top > NEG_INF : top > was + WINDOW;
+        const float now = move ? top - HEAD : was;
+        n[L.tok & 1] = f[L.tok & 1];
+        n[2 + (L.tok & 1)] = -now;
+        sh.col[L.g][L.tok].x = first ? 0.0f : move && !none ? ex2(was - now) : 1.0f;  // of the sums so far
+        sh.unseen[L.g][L.tok] = none && !move ? 1.0f : 0.0f;
+    }
+    group_sync(L.bar_id);
+    // a group's first tile: l starts from zero, and O^T's first product overwrites it
+#pragma unroll 1
+    for (int c = first ? cw : 0; c < 2 * cw; c += 4) {
+        const uint32_t a = c < cw ? t_o + c : t_l + c - cw;
+        const float4* f = &sh.col[L.g][c < cw ? c : c - cw];
+        uint32_t o[4] = {0u, 0u, 0u, 0u};
+        if (!first) {
+            tmem_ld4(a, o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[j].x);
+        }
+        tmem_st4(a, o);
+    }
+    tmem_wait_st();
+    return true;
+}
+
+// The rows of q as e4m3 terms, and the columns' factors.  A thread takes 16 channels, so a warp four rows (eight of 64 channels).
+template <int DT, int D>
+__device__ __forceinline__ void load_q(const TcParams& T, Shared& sh, const Lane L, int b, int h, int rt, int rows)
+{
+    const AttnParams& P = T.A;
+    constexpr int TERMS = DT == DT_BF16 ? 2 : 3, LPR = D / 16, RPW = 32 / LPR;  // lanes of a row, rows of a warp
+    const int cw = L.nch * 16, d = (L.lane % LPR) * 16;
+#pragma unroll 1
+    for (int c = L.quad * RPW + L.lane / LPR; c < cw; c += 4 * RPW) {
+        const int col = L.col0 + c, r = rt * T.MR + col, t = row_token(T, r);
+        uint32_t u[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        if (col < T.MR && r < P.R && t < rows) {
+            const uint16_t* q = reinterpret_cast<const uint16_t*>(P.q) + (int64_t)b * P.qb + (int64_t)t * P.qt + (int64_t)(h * P.G + r - t * P.G) * P.qh + d;
+            if (T.qvec) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(q)), z = __ldg(reinterpret_cast<const uint4*>(q) + 1);
+                u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
+                u[4] = z.x; u[5] = z.y; u[6] = z.z; u[7] = z.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) u[k] = (uint32_t)__ldg(q + 2 * k) | (uint32_t)__ldg(q + 2 * k + 1) << 16;
+            }
+        }
+        float x[16], amax = 0.0f;
+        bool fin = true;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if constexpr (DT == DT_BF16) {
+                x[2 * k] = bf16lo(u[k]);
+                x[2 * k + 1] = bf16hi(u[k]);
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
+                x[2 * k] = f.x;
+                x[2 * k + 1] = f.y;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            fin = fin && fabsf(x[k]) < __int_as_float(0x7f800000);
+            amax = fmaxf(amax, fabsf(x[k]));
+        }
+        // (cw is a multiple of 16 and the rows of a warp divide it, so all lanes of a row are here)
+        const unsigned row_lanes = (LPR == 8 ? 0xffu : 0xfu) << (L.lane / LPR * LPR);
+#pragma unroll
+        for (int o = LPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(row_lanes, amax, o));
+        fin = __all_sync(row_lanes, fin);
+        const int e = fin ? min(max(7 - exponent_of(amax), -120), 126) : 0;
+        const float mul = exp2_int(e);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = fin ? x[k] * mul : 0.0f;
+        uint8_t* to = L.smem + q_off<D>(col, d);
+#pragma unroll
+        for (int q = 0; q < TERMS; ++q, to += (size_t)T.RN * D) {
+            uint32_t code[4];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                uint16_t c2;  // magnitudes stay under 448
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c2) : "f"(x[2 * k + 1]), "f"(x[2 * k]));
+                const uint32_t h2 = e4m3x2_to_half2(c2);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                x[2 * k] -= f.x;
+                x[2 * k + 1] -= f.y;
+                code[k >> 1] = k & 1 ? code[k >> 1] | (uint32_t)c2 << 16 : c2;
+            }
+            *reinterpret_cast<uint4*>(to) = make_uint4(code[0], code[1], code[2], code[3]);
+        }
+        // a row of q with a NaN or an infinity has no scores
+        if (L.lane % LPR < 2)
+            reinterpret_cast<float*>(&sh.fr[L.lane % LPR][col >> 1])[c & 1] = fin ? P.scale * LOG2E * exp2_int(-e) : __int_as_float(0x7fc00000);
+    }
+    fence_proxy_async_smem();
+    group_sync(L.bar_id);
+    if (L.lane == 0) mbar_arrive(&sh.qfull);
+}
+
+// Before a tile of the round's rows: q as halfs (the terms' sums) where P will be, and which columns see this thread's token.
+// Returns whether a wait ran out; *bad: whether a parent is out of range.
+template <int DT, int D>
+__device__ __forceinline__ bool own_tile(const TcParams& T, Shared& sh, const Lane L, int it, int b, int rt, int rows, int j0, uint64_t* see, bool* bad)
+{
+    const AttnParams& P = T.A;
+    constexpr int TERMS = DT == DT_BF16 ? 2 : 3;
+    const int cw = L.nch * 16;
+    uint8_t* pb = L.smem + T.o_p + (T.np == 2 ? it & 1 : 0) * T.p_buf;
+    // (the kernel's first tile asks for a phase before the first, which counts as over)
+    const bool ok = wait_warp(sh, &sh.pv[(it + 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit);
+    bool badp = false;
+    if (ok) {
+#pragma unroll 1
+        for (int i = L.tok; i < cw * (D / 8); i += 128) {
+            const int col = L.col0 + i / (D / 8), d = i % (D / 8) * 8;
+            alignas(16) __half2 x[4];
+#pragma unroll
+            for (int q = 0; q < TERMS; ++q) {
+                const uint2 code = *reinterpret_cast<const uint2*>(L.smem + (size_t)q * T.RN * D + q_off<D>(col, d));
+                const uint32_t u[4] = {e4m3x2_to_half2((uint16_t)code.x), e4m3x2_to_half2((uint16_t)(code.x >> 16)),
+                                       e4m3x2_to_half2((uint16_t)code.y), e4m3x2_to_half2((uint16_t)(code.y >> 16))};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const __half2 y = *reinterpret_cast<const __half2*>(&u[k]);
+                    x[k] = q ? __hadd2(x[k], y) : y;
+                }
+            }
+            *reinterpret_cast<uint4*>(pb + (size_t)(d >> 6) * T.RN * 128 + col * 128 + ((((d & 63) >> 3) ^ (col & 7)) << 4)) =
+                *reinterpret_cast<const uint4*>(x);
+        }
+        if (L.tok < cw) {
+            // a thread per column: the rows on its row's path, as bits of the tile's 128 tokens
+            const int t = row_token(T, rt * T.MR + L.col0 + L.tok);
+            uint32_t* m = sh.mask[L.col0 + L.tok];
+            m[0] = m[1] = m[2] = m[3] = 0u;
+            if (P.kn && t < rows) {
+#pragma unroll 1
+                for (int cur = t;;) {
+                    if ((unsigned)(cur - j0) < (unsigned)TT) m[(cur - j0) >> 5] |= 1u << ((cur - j0) & 31);
+                    if (cur == 0) break;
+                    const int p = P.parents ? __ldg(P.parents + (size_t)b * (P.T - 1) + cur - 1) : cur - 2;
+                    if (p < -1 || p >= cur - 1) break;  // reported below; the walk always ends
+                    cur = p + 1;
+                }
+            }
+        }
+        if (P.parents)
+#pragma unroll 1
+            for (int i = L.tok; i < rows - 1; i += 128) {
+                const int p = __ldg(P.parents + (size_t)b * (P.T - 1) + i);
+                badp = badp || p < -1 || p >= i;
+            }
+        fence_proxy_async_smem();
+    }
+    *bad = group_any(L.bar_id, badp);
+    uint64_t v = 0;
+#pragma unroll 4
+    for (int c = 0; c < cw; ++c) v |= (uint64_t)(sh.mask[L.col0 + c][L.quad] >> L.lane & 1u) << c;
+    *see = v;
+    if (ok && L.lane == 0) mbar_arrive(&sh.own[it & 1]);
+    return !ok;
+}
+
+// A group's outputs: o = O^T / l and lse, or the part for attn_merge_kernel.
+template <int DT, int D>
+__device__ __forceinline__ void put_outputs(const TcParams& T, Shared& sh, const Lane L, int rb, int b, int h, int rt, int rows, bool whole, float* part,
+                                         int status, bool dead, bool vbad)
+{
+    const AttnParams& P = T.A;
+    const int cw = L.nch * 16;
+    const uint32_t t_o = L.tl + 2 * T.RN + L.col0, t_l = t_o + T.RN;
+    if (!dead) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < cw; c += 16) {
+            uint32_t l[16];
+            float v[16];
+            tmem_ld16_nowait(t_l + c, l);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(l[j]);
+            // the sums of 16 columns over the warp's lanes: half of the columns travel at each step
+#pragma unroll
+            for (int n = 8, bit = 16; n; n >>= 1, bit >>= 1) {
+                const bool up = L.lane & bit;
+#pragma unroll
+                for (int k = 0; k < n; ++k) {
+                    const float send = up ? v[k] : v[k + n], keep = up ? v[k + n] : v[k];
+                    v[k] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+                }
+            }
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+            if (!(L.lane & 1)) sh.wred[L.g][L.quad][c + (L.lane >> 1)] = v[0];
+        }
+    }
+    group_sync(L.bar_id);
+    if (L.tok < cw) {
+        // a column's row of the output (-1: none), and the factor of its sums
+        const int col = L.col0 + L.tok, r = rt * T.MR + col, t = row_token(T, r), row = t * P.Hq + h * P.G + r - t * P.G;
+        const float(*w)[MAXC] = sh.wred[L.g];
+        const float l = dead ? 0.0f : (w[0][L.tok] + w[1][L.tok]) + (w[2][L.tok] + w[3][L.tok]);
+        const float m = dead || sh.unseen[L.g][L.tok] != 0.0f ? NEG_INF : -reinterpret_cast<const float*>(&sh.fr[rb][col >> 1])[2 + (col & 1)];
+        float4 c = make_float4(1.0f, __int_as_float(-1), __int_as_float(t), 0.0f);
+        if (col < T.MR && r < P.R) {
+            c.y = __int_as_float(row);
+            const bool live = t < rows && l != 0.0f;
+            if (whole) {
+                float lse = live ? (m + log2f(l)) * LN2 : NEG_INF;
+                c.x = live ? 1.0f / l : 0.0f;
+                if (status != ROW_OK) lse = c.x = __int_as_float(0x7fc00000);
+                if (P.lse) P.lse[(size_t)b * P.T * P.Hq + row] = lse;
+            } else {
+                part[(size_t)T.MR * D + col] = m;
+                part[(size_t)T.MR * D + T.MR + col] = l;
+            }
+        }
+        sh.col[L.g][L.tok] = c;
+    }
+    group_sync(L.bar_id);
+    uint16_t* out = reinterpret_cast<uint16_t*>(P.out) + (size_t)b * P.T * P.Hq * D + L.tok;
+#pragma unroll 1
+    for (int c = 0; c < cw; c += 16) {
+        uint32_t o[16];
+        if (!dead) tmem_ld16_nowait(t_o + c, o);
+        tmem_wait_ld();
+        if (L.tok >= D) continue;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float4 q = sh.col[L.g][c + j];
+            const int row = __float_as_int(q.y);
+            if (row < 0) continue;
+            float x = dead ? 0.0f : __uint_as_float(o[j]);
+            if (vbad && __float_as_int(q.z) < rows) x += unfinite_values<DT>(P, b, h, __float_as_int(q.z), L.tok);
+            if (whole) {
+                // a dead row's sums are zeros that no token touched; with a status they become NaN
+                const float y = q.x == 0.0f ? 0.0f : x * q.x;
+                out[(size_t)row * D] = DT == DT_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : __half_as_ushort(__float2half_rn(y));
+            } else {
+                part[(size_t)(L.col0 + c + j) * D + L.tok] = x;
+            }
+        }
+    }
+    tc_fence_before();
+    group_sync(L.bar_id);
 }
 
 template <int DT, int D>
 __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uint8_t* smem, uint32_t tmem)
 {
     const AttnParams& P = T.A;
-    constexpr int TERMS = DT == DT_BF16 ? 2 : 3, EPL = D / 32;
-    const int wid = (threadIdx.x >> 5) - SMW0, g = wid >> 2, quad = wid & 3, lane = threadIdx.x & 31;
-    const int tok = quad * 32 + lane;       // this thread's token of a tile, and its channel of O^T
-    const int bar_id = 1 + g;
-    const int chunks = T.RN / 16, ch0 = g * chunks / NG, nch = (g + 1) * chunks / NG - ch0;
-    const int col0 = ch0 * 16, cw = nch * 16;  // this group's columns
-    const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);  // this warp's lanes
-    const uint32_t t_o = tl + 2 * T.RN + col0, t_l = t_o + T.RN;
-    float4* const fr0 = &sh.fr[0][col0 / 2];
-    float4* const fr1 = &sh.fr[1][col0 / 2];
-    int it = 0, rb = 0;
+    const int wid = (threadIdx.x >> 5) - SMW0, chunks = T.RN / 16;
+    Lane L;
+    L.smem = smem;
+    L.g = wid >> 2;
+    L.quad = wid & 3;
+    L.lane = threadIdx.x & 31;
+    L.tok = L.quad * 32 + L.lane;
+    L.tl = tmem + ((uint32_t)(L.quad * 32) << 16);
+    L.bar_id = 1 + L.g;
+    L.col0 = L.g * chunks / NG * 16;
+    L.nch = (L.g + 1) * chunks / NG - L.g * chunks / NG;
+    int it = 0, s_at = 0, rb = 0;
     bool dead = false;
-
     for (Walk w(P, at); w.more(); w.next(P)) {
         w.open();
         int status = w.rq.status;
         bool vbad = false;
-
-        if (!dead) {
-            // ---- the rows of q as e4m3 terms; a warp takes every fourth column of its group, four of them at a time
-            for (int c0 = quad; c0 < cw; c0 += 16) {
-                float x[4][EPL];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int col = col0 + c0 + 4 * i, r = w.rt * T.MR + col, t = r / P.G;
-#pragma unroll
-                    for (int k = 0; k < EPL; ++k) x[i][k] = 0.0f;
-                    if (c0 + 4 * i < cw && col < T.MR && r < P.R && t < w.rq.rows)
-                        load_run<DT, EPL>(P.q, (int64_t)w.b * P.qb + (int64_t)t * P.qt + (int64_t)(w.h * P.G + r % P.G) * P.qh + lane * EPL,
-                                          T.qvec, x[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = c0 + 4 * i, col = col0 + c;
-                    if (c >= cw) break;
-                    float amax = 0.0f;
-                    bool fin = true;
-#pragma unroll
-                    for (int k = 0; k < EPL; ++k) {
-                        fin = fin && fabsf(x[i][k]) < __int_as_float(0x7f800000);
-                        amax = fmaxf(amax, fabsf(x[i][k]));
-                    }
-                    fin = __all_sync(0xffffffffu, fin);
-                    amax = warp_max(amax);
-                    const int e = fin ? min(max(7 - exponent_of(amax), -120), 126) : 0;
-                    const float mul = exp2_int(e);
-#pragma unroll
-                    for (int k = 0; k < EPL; ++k) x[i][k] = fin ? x[i][k] * mul : 0.0f;
-                    const int d = lane * EPL;
-                    uint8_t* to = smem + q_off<D>(col, d);
-#pragma unroll
-                    for (int q = 0; q < TERMS; ++q) {
-                        uint32_t code = 0;
-#pragma unroll
-                        for (int k = 0; k < EPL; k += 2) {
-                            const uint16_t c2 = e4m3x2_from(x[i][k], x[i][k + 1]);
-                            const uint32_t h2 = e4m3x2_to_half2(c2);
-                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                            x[i][k] -= f.x;
-                            x[i][k + 1] -= f.y;
-                            code |= (uint32_t)c2 << (8 * k);
-                        }
-                        if constexpr (EPL == 4) *reinterpret_cast<uint32_t*>(to + (size_t)q * T.RN * D) = code;
-                        else *reinterpret_cast<uint16_t*>(to + (size_t)q * T.RN * D) = (uint16_t)code;
-                    }
-                    if (lane < 2) {
-                        // a row of q with a NaN or an infinity has no scores
-                        float* f = reinterpret_cast<float*>(lane ? &fr1[c >> 1] : &fr0[c >> 1]);
-                        f[c & 1] = fin ? P.scale * LOG2E * exp2_int(-e) : __int_as_float(0x7fc00000);
-                        f[2 + (c & 1)] = 0.0f;
-                    }
-                }
+        if (!dead) load_q<DT, D>(T, sh, L, w.b, w.h, w.rt, w.rq.rows);
+        for (int tile = w.tile0; tile < w.tile1 && !dead;) {
+            const bool own = tile >= w.rq.ncache;
+            uint64_t see = 0;
+            bool fail = false;
+            if (own) {
+                bool bad;
+                fail = own_tile<DT, D>(T, sh, L, it, w.b, w.rt, w.rq.rows, (tile - w.rq.ncache) * TT, &see, &bad);
+                if (bad) status = ROW_BAD_PARENT;
             }
-            fence_proxy_async_smem();
-        }
-        group_sync(bar_id);
-        if (!dead && lane == 0) mbar_arrive(&sh.qfull);
-
-        for (int tile = w.tile0; tile < w.tile1; ++tile, ++it) {
-            if (dead) break;
-            const bool first = tile == w.tile0, fresh = tile >= w.rq.ncache;
-            bool fail = false, stopped = false;
-            uint32_t left_out = first ? 0xffffffffu : 0u;
-            if (!first && !fresh) {
-                const RunEnd r = softmax_run(T, sh, smem + T.o_p + tok * 128, rb ? fr1 : fr0, tl, col0, nch, bar_id, it, tile,
-                                             min(w.tile1, w.rq.ncache), w.rq.len);
+            // a group's first tile has no reference yet; another's may turn out too low, and the tile is repeated
+            bool first = tile == w.tile0, again = first;
+            uint32_t take = ~0u;
+            const int end = own ? tile + 1 : min(w.tile1, w.rq.ncache);
+            while (tile < end) {
+                if (again) {
+                    if (!move_reference(T, sh, L, rb, it, s_at, w.rq.len - tile * TT, own, see, first)) {
+                        dead = true;
+                        break;
+                    }
+                    rb ^= 1;
+                }
+                const RunEnd r = softmax_run(T, sh, L, &sh.fr[rb][L.col0 / 2], it, s_at, tile, end, w.rq.len, own, see, take);
                 status = max(status, r.status);
                 tile += r.n;
                 it += r.n;
-                if (!r.stopped) {
-                    --tile;
-                    --it;
-                    continue;
-                }
-                stopped = true;
-                fail = r.fail;
-                left_out = r.left_out;
-            }
-            uint8_t* pb = smem + T.o_p + (it % T.np) * T.p_buf;
-            if (fresh) {
-                // q as halfs (the terms' sums) where P will be, and which rows each column sees
-                if (it >= 1) fail = !wait_warp(sh, &sh.pv[(it - 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit);
-                const int j0 = (tile - w.rq.ncache) * TT;
-                bool badp = false;
-                if (!fail) {
-                    for (int i = tok; i < cw * (D / 8); i += 128) {
-                        const int col = col0 + i / (D / 8), d = i % (D / 8) * 8;
-                        alignas(16) __half2 x[4];
-#pragma unroll
-                        for (int q = 0; q < TERMS; ++q) {
-                            const uint2 code = *reinterpret_cast<const uint2*>(smem + (size_t)q * T.RN * D + q_off<D>(col, d));
-                            const uint32_t u[4] = {e4m3x2_to_half2((uint16_t)code.x), e4m3x2_to_half2((uint16_t)(code.x >> 16)),
-                                                   e4m3x2_to_half2((uint16_t)code.y), e4m3x2_to_half2((uint16_t)(code.y >> 16))};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const __half2 y = *reinterpret_cast<const __half2*>(&u[k]);
-                                x[k] = q ? __hadd2(x[k], y) : y;
-                            }
-                        }
-                        *reinterpret_cast<uint4*>(pb + (size_t)(d >> 6) * T.RN * 128 + col * 128 + ((((d & 63) >> 3) ^ (col & 7)) << 4)) =
-                            *reinterpret_cast<const uint4*>(x);
-                    }
-                    if (tok < cw) {
-                        const int r = w.rt * T.MR + col0 + tok, t = r / P.G;
-                        uint32_t m[4] = {0, 0, 0, 0};
-                        if (P.kn && t < w.rq.rows) {
-                            if (!P.parents) {
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const int n = t + 1 - j0 - 32 * k;
-                                    m[k] = n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-                                }
-                            } else {
-                                for (int cur = t;;) {
-                                    const int o = cur - j0;
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        if ((o >> 5) == k && o >= 0) m[k] |= 1u << (o & 31);
-                                    if (cur == 0) break;
-                                    const int p = __ldg(P.parents + (size_t)w.b * (P.T - 1) + cur - 1);
-                                    if (p < -1 || p >= cur - 1) break;  // reported below; the walk always ends
-                                    cur = p + 1;
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) sh.mask[col0 + tok][k] = m[k];
-                    }
-                    if (P.parents)
-                        for (int i = tok; i < w.rq.rows - 1; i += 128) {
-                            const int p = __ldg(P.parents + (size_t)w.b * (P.T - 1) + i);
-                            badp = badp || p < -1 || p >= i;
-                        }
-                    fence_proxy_async_smem();
-                }
-                if (group_any(bar_id, badp)) status = ROW_BAD_PARENT;
-                if (!fail && lane == 0) mbar_arrive(&sh.own[it & 1]);
-            }
-
-            // (a tile that the run stopped at has waited; a group's first tile may overwrite P once the last group's outputs are
-            // out, which waited for its O^T)
-            fail = fail || (!stopped && !wait_warp(sh, &sh.sfull[it & 1], (it >> 1) & 1, T.wait_limit));
-            float ks = 1.0f, ve = 0.0f;
-            bool okt = false, partial = true;
-            const uint32_t ts = tl + (it & 1) * T.RN + col0;
-            if (!fail) {
-                tc_fence_after();
-                if (!fresh) {
-                    const int s = it % T.stages, left = w.rq.len - tile * TT;
-                    partial = left < TT;
-                    okt = tok < left;
-                    if (okt) {
-                        const float2 sc = sh.scale[s][tok >> P.page_shift];
-                        ks = sc.x;
-                        ve = (float)exponent_of(sc.y);
-                    }
-                    status = max(status, sh.status[s]);
-                } else {
-                    ks = sh.fks[it & 1][tok];
-                    ve = sh.fve[it & 1][tok];
-#pragma unroll
-                    for (int k = 0; k < VWN; ++k) vbad = vbad || sh.vbad[it & 3][k];
-                }
-            }
-            const float inv = exp2_int(min(max(-(int)ve, -126), 127));
-            const unsigned long long ks2 = f2_pack(ks, ks), ve2 = f2_pack(ve, ve), inv2 = f2_pack(inv, inv);
-            // which of 16 columns see this thread's token
-            const auto seen16 = [&](int ch) -> uint32_t {
-                if (!fresh) return okt ? 0xffffu : 0u;
-                uint32_t m = 0;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) m |= (sh.mask[col0 + ch * 16 + j][quad] >> lane & 1u) << j;
-                return m;
-            };
-            // A pass over the tile: weights to shared memory, their sums to l.  The first pass goes by the reference as it
-            // stands.  Where that turns out too low the sums are rescaled, this pass's share with them, and a second
-            // one repeats the weights; it adds to l only what the first left out: 16 columns of a warp one of whose
-            // weights would have taken the sum out of fp32's range.
-            float vmax = NEG_INF;
-            const auto weights = [&](auto again) {
-                const float4* fr = rb ? fr1 : fr0;
-#pragma unroll 1
-                for (int ch = 0; ch < nch; ++ch) {
-                    uint32_t s[16], l[16], h[8];
-                    uint4 f[8];
-                    tmem_ld16_nowait(ts + ch * 16, s);
-                    // all eight in flight at once, beside the scores: one after another they would set the loop's pace
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] = lds128(reinterpret_cast<const uint4*>(&fr[ch * 8 + j]));
-                    const uint32_t see = partial ? seen16(ch) : 0xffffu;
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const unsigned long long x = f2_mul(f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])),
-                                                            f2_pack(__uint_as_float(f[j].x), __uint_as_float(f[j].y)));
-                        float a, b;
-                        f2_unpack(f2_fma(x, ks2, f2_add(ve2, f2_pack(__uint_as_float(f[j].z), __uint_as_float(f[j].w)))), a, b);
-                        s[2 * j] = __float_as_uint(a);
-                        s[2 * j + 1] = __float_as_uint(b);
-                    }
-                    if (!(again.value && first)) tmem_ld16_nowait(t_l + ch * 16, l);
-                    if (partial) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) s[j] = see >> j & 1u ? s[j] : __float_as_uint(NEG_INF);
-                    }
-                    bool sums;
-                    if constexpr (again.value) {
-                        sums = left_out >> ch & 1u;
-                    } else {
-                        float t8[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) t8[j] = fmaxf(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
-                        const float top = fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])), fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
-                        vmax = fmaxf(vmax, top);
-                        sums = !__any_sync(0xffffffffu, top > FAR);
-                        if (!sums) left_out |= 1u << ch;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) s[j] = __float_as_uint(ex2(__uint_as_float(s[j])));
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) h[j] = pack_half2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
-                    const int col = col0 + ch * 16;
-                    uint8_t* row = pb + (size_t)(col >> 6) * 16384 + tok * 128;
-                    const int unit = (col & 63) >> 3;
-                    *reinterpret_cast<uint4*>(row + ((unit ^ (tok & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4*>(row + (((unit + 1) ^ (tok & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-                    tmem_wait_ld();
-                    if (sums) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const unsigned long long p = f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
-                            float c, d;
-                            if (again.value && first) f2_unpack(f2_mul(p, inv2), c, d);
-                            else f2_unpack(f2_fma(p, inv2, f2_pack(__uint_as_float(l[2 * j]), __uint_as_float(l[2 * j + 1]))), c, d);
-                            l[2 * j] = __float_as_uint(c);
-                            l[2 * j + 1] = __float_as_uint(d);
-                        }
-                        tmem_st16_nowait(t_l + ch * 16, l);
-                    }
-                }
-                fence_proxy_async_smem();
-                tmem_wait_st();
-            };
-            // the first tile of a group has no reference yet
-            if (!fail && !first && !stopped) weights(std::false_type{});
-            if (stopped || group_any(bar_id, fail || first || vmax > WINDOW)) {
-                if (group_any(bar_id, fail)) {
+                for (s_at += r.n; s_at >= T.stages;) s_at -= T.stages;
+                if (r.stopped && group_any(L.bar_id, fail || r.fail)) {
                     dead = true;
                     break;
                 }
-                // the columns' maxima over the tile
-                const float4* fr = rb ? fr1 : fr0;
-                float4* to = rb ? fr0 : fr1;
-#pragma unroll 1
-                for (int ch = 0; ch < nch; ++ch) {
-                    uint32_t s[16];
-                    float v[16];
-                    tmem_ld16_nowait(ts + ch * 16, s);
-                    const uint32_t see = seen16(ch);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float F = reinterpret_cast<const float*>(&fr[ch * 8 + (j >> 1)])[j & 1];
-                        v[j] = see >> j & 1u ? fmaf(__uint_as_float(s[j]) * F, ks, ve) : NEG_INF;
-                    }
-                    const float m = reduce16(v, lane, [](float a, float b) { return fmaxf(a, b); });
-                    if (!(lane & 1)) sh.wred[g][quad][ch * 16 + (lane >> 1)] = m;
-                }
-                // O^T of the tile before has to be whole before it is rescaled
-                const bool okp = first || wait_warp(sh, &sh.pv[(it - 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit);
-                if (group_any(bar_id, !okp)) {
-                    dead = true;
-                    break;
-                }
-                if (tok < cw) {
-                    const float top = fmaxf(fmaxf(sh.wred[g][0][tok], sh.wred[g][1][tok]), fmaxf(sh.wred[g][2][tok], sh.wred[g][3][tok]));
-                    // a column that has seen nothing yet keeps the reference 0, which its zero sums do not feel
-                    const float* f = reinterpret_cast<const float*>(&fr[tok >> 1]);
-                    float* n = reinterpret_cast<float*>(&to[tok >> 1]);
-                    const float was = first ? 0.0f : -f[2 + (tok & 1)];
-                    const bool none = first || sh.unseen[g][tok] != 0.0f;
-                    const bool move = none ? top > NEG_INF : top > was + WINDOW;
-                    const float now = move ? top - HEAD : was;
-                    n[tok & 1] = f[tok & 1];
-                    n[2 + (tok & 1)] = -now;
-                    sh.col[g][tok].x = move && !none ? ex2(was - now) : 1.0f;  // of the sums so far
-                    sh.unseen[g][tok] = none && !move ? 1.0f : 0.0f;
-                }
-                group_sync(bar_id);
-                rb ^= 1;
-                if (!first) {
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int ch = 0; ch < 2 * nch; ++ch) {
-                        const uint32_t a = ch < nch ? t_o + ch * 16 : t_l + (ch - nch) * 16;
-                        const float4* f = &sh.col[g][(ch < nch ? ch : ch - nch) * 16];
-                        uint32_t o[16];
-                        tmem_ld16_nowait(a, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[j].x);
-                        tmem_st16_nowait(a, o);
-                    }
-                    tmem_wait_st();
-                }
-                weights(std::true_type{});
-                group_sync(bar_id);
+                again = r.stopped;
+                first = false;
+                take = r.left_out;
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.ready[it & 1]);
+            if (own && !dead)
+                for (int k = 0; k < VWN; ++k) vbad = vbad || sh.vbad[(it - 1) & 3][k];
         }
-
-        // ---- outputs
-        if (!dead) {
-            const bool okp = wait_warp(sh, &sh.pv[(it - 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit);
-            dead = group_any(bar_id, !okp);
-        }
+        if (!dead) dead = group_any(L.bar_id, !wait_warp(sh, &sh.pv[(it - 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit));
         if (dead) status = ROW_TIMEOUT;
-        else tc_fence_after();
         float* part = P.parts + ((size_t)blockIdx.x * 2 + (w.first && w.tile0 != 0 ? 0 : 1)) * part_floats(T.MR, D);
-        if (!dead) {
-#pragma unroll 1
-            for (int ch = 0; ch < nch; ++ch) {
-                uint32_t l[16];
-                float v[16];
-                tmem_ld16_nowait(t_l + ch * 16, l);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(l[j]);
-                const float x = reduce16(v, lane, [](float a, float b) { return a + b; });
-                if (!(lane & 1)) sh.wred[g][quad][ch * 16 + (lane >> 1)] = x;
-            }
-        }
-        group_sync(bar_id);
-        if (tok < cw) {
-            // a column's row of the output (-1: none), and the factor of its sums
-            const int col = col0 + tok, r = w.rt * T.MR + col, t = r / P.G;
-            const float l = dead ? 0.0f : (sh.wred[g][0][tok] + sh.wred[g][1][tok]) + (sh.wred[g][2][tok] + sh.wred[g][3][tok]);
-            const float m = dead || sh.unseen[g][tok] != 0.0f ? NEG_INF : -reinterpret_cast<const float*>(&(rb ? fr1 : fr0)[tok >> 1])[2 + (tok & 1)];
-            float4 c = make_float4(0.0f, __int_as_float(-1), __int_as_float(t), 0.0f);
-            if (col < T.MR && r < P.R) {
-                const size_t row = ((size_t)w.b * P.T + t) * P.Hq + w.h * P.G + r % P.G;
-                c.y = __int_as_float(t * P.Hq + w.h * P.G + r % P.G);
-                const bool live = t < w.rq.rows && l != 0.0f;
-                if (w.whole) {
-                    float lse = live ? (m + log2f(l)) * LN2 : NEG_INF;
-                    c.x = live ? 1.0f / l : 0.0f;
-                    if (status != ROW_OK) lse = c.x = __int_as_float(0x7fc00000);
-                    if (P.lse) P.lse[row] = lse;
-                } else {
-                    part[(size_t)T.MR * D + col] = m;
-                    part[(size_t)T.MR * D + T.MR + col] = l;
-                }
-            }
-            sh.col[g][tok] = c;
-        }
-        group_sync(bar_id);
-        const size_t out0 = (size_t)w.b * P.T * P.Hq;
-#pragma unroll 1
-        for (int ch = 0; ch < nch; ++ch) {
-            uint32_t o[16];
-            if (!dead) {
-                tmem_ld16_nowait(t_o + ch * 16, o);
-                tmem_wait_ld();
-            } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = 0u;
-            }
-            if (tok >= D) continue;
-            if (vbad) {
-                // values that are not finite reach the rows that see them
-#pragma unroll 1
-                for (int j = 0; j < 16; ++j) {
-                    const float4 c = sh.col[g][ch * 16 + j];
-                    const int t = __float_as_int(c.z);
-                    if (__float_as_int(c.y) < 0 || t >= w.rq.rows) continue;
-                    float add = 0.0f;
-                    for (int cur = t;;) {
-                        const float y = load_elem<DT>(P.vn, w.b * P.vb + cur * P.vt + w.h * P.vh + tok);
-                        if (!(fabsf(y) < __int_as_float(0x7f800000))) add += y;
-                        if (cur == 0) break;
-                        const int p = P.parents ? __ldg(P.parents + (size_t)w.b * (P.T - 1) + cur - 1) : cur - 2;
-                        if (p < -1 || p >= cur - 1) break;
-                        cur = p + 1;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        if (k == j) o[k] = __float_as_uint(__uint_as_float(o[k]) + add);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float4 c = sh.col[g][ch * 16 + j];
-                const int row = __float_as_int(c.y);
-                if (row < 0) continue;
-                if (w.whole) {
-                    // a dead row's sums are zeros that no token touched, or NaN with the status
-                    const float y = c.x == 0.0f ? 0.0f : __uint_as_float(o[j]) * c.x;
-                    reinterpret_cast<uint16_t*>(P.out)[(out0 + row) * D + tok] =
-                        DT == DT_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : __half_as_ushort(__float2half_rn(y));
-                } else {
-                    part[(size_t)(col0 + ch * 16 + j) * D + tok] = __uint_as_float(o[j]);
-                }
-            }
-        }
+        put_outputs<DT, D>(T, sh, L, rb, w.b, w.h, w.rt, w.rq.rows, w.whole, part, status, dead, vbad);
         if (threadIdx.x == SMW0 * 32) {
             if (w.whole) {
                 if (P.row_status && w.h == 0 && w.rt == 0) P.row_status[w.b] = status;
@@ -1107,8 +1125,6 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
                 if (w.tile0 == 0) P.joins[blockIdx.x] = {parts_of(at.total, blockIdx.x, at.ctas, w.u + w.rq.n), w.b, w.h, w.rt, w.rq.rows};
             }
         }
-        tc_fence_before();
-        group_sync(bar_id);
     }
 }
 
@@ -1125,7 +1141,8 @@ attn_tc_kernel(const __grid_constant__ TcParams T, const __grid_constant__ CUten
         P.joins[blockIdx.x].parts = 0;
         for (int i = 0; i < T.stages; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], 1 + VWN);  // the products' commit and the warps that widen the values
+            mbar_init(&sh.info[i], 1);
+            mbar_init(&sh.empty[i], 1 + VWN + 4 * NG);  // the products' commit, and the warps that read the pages and the scales
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.sfull[i], 1);
@@ -1205,28 +1222,29 @@ cudaError_t launch_tc(AttnParams& P, int sms, cudaStream_t st)
     T.RN = (T.MR + 15) / 16 * 16;
     T.A = P;
     T.wait_limit = P.wait_limit;
+    T.inv_g = (1ull << 32) / (uint64_t)P.G + 1;
     const uint32_t terms = DT == DT_BF16 ? 2 : 3, blocks = (uint32_t)(T.RN + 63) / 64;
     T.p_buf = blocks * 16384;
     T.v_buf = D / 64 * 16384;
-    const uint32_t stage = 2 * TT * D;
-    // second buffers of the values and of P where three stages still fit beside them
+    const uint32_t stage = TT * D, keys = 2 * TT * D;
+    // second buffers of the values and of P where three stages of keys still fit beside them
     for (int extra = 2;; --extra) {
         T.nv = extra >= 1 ? 2 : 1;
         T.np = extra >= 2 ? 2 : 1;
         T.o_p = terms * T.RN * D;
         T.o_v = T.o_p + T.np * T.p_buf;
-        T.o_stage = T.o_v + T.nv * T.v_buf + (D == 64 ? 16384 : 0);
+        T.o_kh = T.o_v + T.nv * T.v_buf + (D == 64 ? 16384 : 0);
+        T.o_stage = T.o_kh + keys;
         T.stages = (int)(((int)TC_SMEM - 1024 - (int)T.o_stage) / (int)stage);
         if (T.stages >= 3 || extra == 0) break;
     }
     if (T.stages > MAXSTAGES) T.stages = MAXSTAGES;
-    const auto vec = [](const void* p, int64_t a, int64_t b, int64_t c) {
-        constexpr int64_t n = D / 32;
+    const auto vec = [](const void* p, int64_t a, int64_t b, int64_t c, int64_t n) {
         return reinterpret_cast<uintptr_t>(p) % (2 * n) == 0 && a % n == 0 && b % n == 0 && c % n == 0;
     };
-    T.qvec = vec(P.q, P.qb, P.qt, P.qh);
-    T.kvec = vec(P.kn, P.kb, P.kt, P.kh);
-    T.vvec = vec(P.vn, P.vb, P.vt, P.vh);
+    T.qvec = vec(P.q, P.qb, P.qt, P.qh, 8);
+    T.kvec = vec(P.kn, P.kb, P.kt, P.kh, D / 32);
+    T.vvec = vec(P.vn, P.vb, P.vt, P.vh, D / 32);
     const size_t bytes = 1024 + T.o_stage + (size_t)T.stages * stage;
     auto* k = attn_tc_kernel<DT, D>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TC_SMEM);
