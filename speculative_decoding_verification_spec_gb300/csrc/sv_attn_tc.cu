@@ -16,7 +16,7 @@
 //   0      copies: the pages' codes by TMA into a ring of stages, the pages' scales beside them
 //   1      products: one lane issues them; S is double-buffered, so S of the next tile runs under this tile's softmax
 //   2 - 7  values to halfs
-//   8 - 19 softmax, three groups of four warps; a thread is a token, a group takes a third of the columns.  The sums l stay in
+//   8 - 15 softmax, two groups of four warps; a thread is a token, a group takes half of the columns.  The sums l stay in
 //          tensor memory beside S^T and O^T, one per token lane and column, so a thread holds 16 columns at a time.  The
 //          weights are taken against the reference as it stands; only when one passes 2^15 (the first tile of a group, and
 //          rarely after) does the group find the columns' maxima, move the reference, rescale its part of O^T and l and
@@ -36,7 +36,7 @@ namespace {
 
 constexpr int TT = 128;          // tokens of a tile
 constexpr int VW0 = 2, VWN = 6;  // warps that widen the values
-constexpr int SMW0 = 8, NG = 3;  // first softmax warp (a multiple of 4), groups of four softmax warps
+constexpr int SMW0 = 8, NG = 2;  // first softmax warp (a multiple of 4), groups of four softmax warps
 constexpr int TNT = (SMW0 + 4 * NG) * 32;
 constexpr int MAXR = 128;        // rows of a group: S^T twice, O^T and the sums l take four times as many columns
 constexpr int MAXC = (MAXR / 16 + NG - 1) / NG * 16;  // columns of a softmax group
