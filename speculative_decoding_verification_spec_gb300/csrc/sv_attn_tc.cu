@@ -42,7 +42,8 @@ constexpr int MAXR = 128;        // rows of a group: S^T twice, O^T and the sums
 constexpr int MAXC = (MAXR / 16 + NG - 1) / NG * 16;  // columns of a softmax group
 constexpr int MAXSTAGES = 6;
 constexpr float WINDOW = 15.0f;  // a weight may reach 2^WINDOW (the largest half is near 2^16)
-constexpr float HEAD = 7.0f;     // a moved reference leaves the maximum at 2^HEAD
+constexpr float HEAD = 3.0f;     // a moved reference leaves the maximum at 2^HEAD: a move repeats a tile, so the room above
+                                 // is kept large; a weight 2^-28 of the largest is then the least that a half still holds
 constexpr float FAR = 40.0f;     // log2 of a weight that the first pass keeps out of l: with the 2^74 of a scale it could soon
                                  // leave fp32's range
 constexpr size_t TC_SMEM = 214 * 1024;  // dynamic shared memory; the static arrays take the rest of the SM's 227 KB
