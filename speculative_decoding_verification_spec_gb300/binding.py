@@ -461,79 +461,98 @@ def kv_cache(pages: int, heads: int, page_size: int, head_dim: int, device="cuda
                    *(torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2)))
 
 
+# A round's calls are short and many, so their marshalling avoids what costs microseconds: pointers go as plain ints,
+# dense tensors pass no strides, and the current stream's handle comes without a Stream object.
+
+_EMPTY = torch.empty
+
+
 def _new(shape, dtype, device, stream):
     """A new output, safe to be written on `stream` when that is not the current one."""
-    t = torch.empty(shape, dtype=dtype, device=device)
+    t = _EMPTY(shape, dtype=dtype, device=device)
     if stream is not None:
         t.record_stream(stream)
     return t
 
 
-def _round_workspace(ws, device, stream, nbytes):
+def _raw_stream(stream, device) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+_round_ws = {}
+
+
+def _round_workspace(ws, device, stream, raw, nbytes):
     """The call's workspace; by default one per device and stream, as calls on two streams may overlap."""
     if ws is not None:
         return ws.get(nbytes)
-    key = (str(device), (stream or torch.cuda.current_stream()).cuda_stream)
-    if key not in _default_ws:
-        _default_ws[key] = Workspace(device)
-    buf = _default_ws[key].get(nbytes)
-    if stream is not None:
-        buf.record_stream(stream)
+    key = (device, raw)
+    buf = _round_ws.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = _round_ws[key] = _new(nbytes, torch.uint8, device, stream)
     return buf
 
 
-def _round_dtype(t: torch.Tensor, what: str, allowed) -> int:
-    code = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}.get(t.dtype)
+_ROUND_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+
+
+def _round_dtype(dtype, what: str, allowed) -> int:
+    code = _ROUND_DTYPES.get(dtype)
     if code not in allowed:
-        raise TypeError(f"{what} has an unsupported dtype {t.dtype}")
+        raise TypeError(f"{what} has an unsupported dtype {dtype}")
     return code
 
 
 def _strides(t, n):
-    """The strides of the n leading dimensions for the C ABI; the last one must be contiguous.  A dimension of size 1
-    has no stride that matters, and torch may give it any."""
+    """The strides of the n leading dimensions for the C ABI (None: dense); the last one must be contiguous.  A dimension
+    of size 1 has no stride that matters, and torch may give it any."""
+    if t.is_contiguous():
+        return None
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError("the last dimension must be contiguous")
-    dense = [1] * (t.dim())
+    dense = [1] * t.dim()
     for i in range(t.dim() - 2, -1, -1):
         dense[i] = dense[i + 1] * t.shape[i + 1]
-    s = [t.stride(i) if t.shape[i] > 1 else dense[i] for i in range(n)]
-    return (ctypes.c_int64 * n)(*s)
+    return (ctypes.c_int64 * n)(*[t.stride(i) if t.shape[i] > 1 else dense[i] for i in range(n)])
 
 
-def _ints(t, shape, what, optional=False):
-    """A contiguous CUDA int32 tensor of this shape (its pointer)."""
-    if t is None and optional:
-        return None
-    if t is None or t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)}")
-    _need_cuda(t)
-    return _ptr(t)
+def _not_cuda():
+    raise SpecVerifyError("inputs must be CUDA tensors (there is no CPU path)")
 
 
-def _floats(t, shape, what):
+def _arg(t, dtype, shape, what):
+    """The pointer of an optional argument: a contiguous CUDA tensor of this dtype and shape."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous float32 tensor of shape {tuple(shape)}")
-    _need_cuda(t)
-    return _ptr(t)
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    if not t.is_cuda:
+        _not_cuda()
+    return t.data_ptr()
+
+
+_I32, _F32 = torch.int32, torch.float32
 
 
 def _cache_args(cache, page_table, lens, B):
     k, v, ks, vs = cache
-    if k.dim() != 4 or k.shape != v.shape or not (k.is_contiguous() and v.is_contiguous()):
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape or not (k.is_contiguous() and v.is_contiguous()):
         raise ValueError("the cache's codes must be contiguous [pages, heads, page_size, head_dim]")
     if k.element_size() != 1 or v.element_size() != 1:
         raise TypeError("the cache's codes must be e4m3 (one byte each)")
-    pages, heads, page, dim = k.shape
-    _need_cuda(k, v)
-    if page_table is None or page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError(f"page_table must be [{B}, width]")
+    if not (k.is_cuda and v.is_cuda):
+        _not_cuda()
+    pages, heads, page, dim = shape
+    if page_table is None or page_table.dim() != 2 or page_table.shape[0] != B or lens is None:
+        raise ValueError(f"page_table must be [{B}, width], with lens [{B}]")
     width = page_table.shape[1]
+    scales = (pages, heads)
     return (pages, heads, page, dim, width,
-            [_ptr(k), _ptr(v), _floats(ks, (pages, heads), "k_scale"), _floats(vs, (pages, heads), "v_scale")],
-            _ints(page_table, (B, width), "page_table"), _ints(lens, (B,), "lens"))
+            (k.data_ptr(), v.data_ptr(), _arg(ks, _F32, scales, "k_scale"), _arg(vs, _F32, scales, "v_scale")),
+            _arg(page_table, _I32, (B, width), "page_table"), _arg(lens, _I32, (B,), "lens"))
 
 
 def process_logits(logits, *, tokens=None, parents=None, history=None, prompt_len=None, history_len=None,
@@ -550,11 +569,13 @@ def process_logits(logits, *, tokens=None, parents=None, history=None, prompt_le
     Returns that dict.
     """
     lib = load()
-    _need_cuda(logits)
+    if not logits.is_cuda:
+        _not_cuda()
     if logits.dim() != 3:
         raise ValueError("logits must be [B, R, V]")
     B, R, V = logits.shape
-    dt = _round_dtype(logits, "logits", (SPEC_F32, SPEC_BF16))
+    dev = logits.device
+    dt = _round_dtype(logits.dtype, "logits", (SPEC_F32, SPEC_BF16))
     N = 0 if tokens is None else tokens.shape[-1]
     H = 0 if history is None else history.shape[-1]
     nb = 0 if bias_tokens is None else bias_tokens.shape[-1]
@@ -565,25 +586,31 @@ def process_logits(logits, *, tokens=None, parents=None, history=None, prompt_le
     if R > N + 1:
         raise ValueError(f"{R} rows need at least {R - 1} drafted tokens")
     if out is None:
-        out = dict(logits=_new((B, R, V), logits.dtype, logits.device, stream),
-                   row_status=_new(B, torch.int32, logits.device, stream))
-    y = out["logits"]
-    if y.shape != logits.shape or y.dtype != logits.dtype:
-        raise ValueError("out['logits'] must have the logits' shape and dtype")
-    W = (V + 31) // 32
+        y = _new((B, R, V), logits.dtype, dev, stream)
+        out = {"logits": y, "row_status": _new(B, _I32, dev, stream)}
+    else:
+        y = out["logits"]
+        if y.shape != logits.shape or y.dtype is not logits.dtype or not y.is_cuda:
+            raise ValueError("out['logits'] must have the logits' shape and dtype")
     if allowed is not None:
-        _need_cuda(allowed)
+        W = (V + 31) // 32
+        if not allowed.is_cuda:
+            _not_cuda()
         if tuple(allowed.shape) != (B, R, W) or allowed.element_size() != 4 or not allowed.is_contiguous():
             raise ValueError(f"allowed must be a contiguous 32-bit [B, R, {W}] tensor")
-    _check(lib.process_logits(
-        _ptr(logits), _ptr(y), dt, B, R, V, _strides(logits, 2), _strides(y, 2),
-        _ints(tokens, (B, N), "tokens", True) if N else None, _ints(parents, (B, N), "parents", True) if N else None, N,
-        _ints(history, (B, H), "history", True) if H else None, H, _ints(prompt_len, (B,), "prompt_len", True),
-        _ints(history_len, (B,), "history_len", True), _floats(repetition, (B,), "repetition"),
-        _floats(presence, (B,), "presence"), _floats(frequency, (B,), "frequency"),
-        _ints(bias_tokens, (B, nb), "bias_tokens", True) if nb else None,
-        _floats(bias_values, (B, nb), "bias_values") if nb else None, nb, _ptr(allowed),
-        _ptr(out.get("row_status")), _stream(stream)))
+    one = (B,)
+    rc = lib.process_logits(
+        logits.data_ptr(), y.data_ptr(), dt, B, R, V, _strides(logits, 2), _strides(y, 2),
+        _arg(tokens, _I32, (B, N), "tokens") if N else None, _arg(parents, _I32, (B, N), "parents") if N else None, N,
+        _arg(history, _I32, (B, H), "history") if H else None, H, _arg(prompt_len, _I32, one, "prompt_len"),
+        _arg(history_len, _I32, one, "history_len"), _arg(repetition, _F32, one, "repetition"),
+        _arg(presence, _F32, one, "presence"), _arg(frequency, _F32, one, "frequency"),
+        _arg(bias_tokens, _I32, (B, nb), "bias_tokens") if nb else None,
+        _arg(bias_values, _F32, (B, nb), "bias_values") if nb else None, nb,
+        None if allowed is None else allowed.data_ptr(), _arg(out.get("row_status"), _I32, one, "row_status"),
+        _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -596,25 +623,29 @@ def kv_cache_write(k, v, cache, page_table, lens, *, accepted_len=None, out_node
     all T rows are written.  Returns dict(lens, row_status): the lengths after the write.
     """
     lib = load()
-    _need_cuda(k, v)
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+    if not (k.is_cuda and v.is_cuda):
+        _not_cuda()
+    if k.dim() != 4 or k.shape != v.shape or k.dtype is not v.dtype:
         raise ValueError("k and v must be [B, T, heads, head_dim] of one dtype")
     B, T, heads, dim = k.shape
-    dt = _round_dtype(k, "k", (SPEC_F32, SPEC_BF16, SPEC_F16))
+    dev = k.device
+    dt = _round_dtype(k.dtype, "k", (SPEC_F32, SPEC_BF16, SPEC_F16))
     pages, h, page, d, width, ptrs, table, ln = _cache_args(cache, page_table, lens, B)
-    if (h, d) != (heads, dim):
+    if h != heads or d != dim:
         raise ValueError(f"the cache holds {h} heads of {d}, the rows {heads} of {dim}")
     if out_nodes is not None and accepted_len is None:
         raise ValueError("out_nodes need accepted_len")
     nw = 0 if out_nodes is None else out_nodes.shape[-1]
     if out is None:
-        out = dict(lens=_new(B, torch.int32, k.device, stream),
-                   row_status=_new(B, torch.int32, k.device, stream))
-    _check(lib.kv_cache_write(
-        _ptr(k), _strides(k, 3), _ptr(v), _strides(v, 3), dt, B, T, heads, dim, *ptrs, pages, page, table, width, ln,
-        _ints(accepted_len, (B,), "accepted_len", True),
-        _ints(out_nodes, (B, nw), "out_nodes", True) if nw else None, nw,
-        _ptr(out.get("lens")), _ptr(out.get("row_status")), _stream(stream)))
+        out = {"lens": _new(B, _I32, dev, stream), "row_status": _new(B, _I32, dev, stream)}
+    one = (B,)
+    rc = lib.kv_cache_write(
+        k.data_ptr(), _strides(k, 3), v.data_ptr(), _strides(v, 3), dt, B, T, heads, dim, *ptrs, pages, page, table, width,
+        ln, _arg(accepted_len, _I32, one, "accepted_len"),
+        _arg(out_nodes, _I32, (B, nw), "out_nodes") if nw else None, nw, _arg(out.get("lens"), _I32, one, "lens"),
+        _arg(out.get("row_status"), _I32, one, "row_status"), _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -625,16 +656,22 @@ def kv_cache_read(cache, page_table, lens, *, max_len: int, start=None, dtype=to
     B = lens.shape[0]
     pages, heads, page, dim, width, ptrs, table, ln = _cache_args(cache, page_table, lens, B)
     dev = cache[0].device
+    shape = (B, max_len, heads, dim)
     if out is None:
-        out = {n: _new((B, max_len, heads, dim), dtype, dev, stream) for n in ("k", "v")}
-        out["row_status"] = _new(B, torch.int32, dev, stream)
-    for n in ("k", "v"):
-        if tuple(out[n].shape) != (B, max_len, heads, dim) or not out[n].is_contiguous() or out[n].dtype != out["k"].dtype:
-            raise ValueError(f"out[{n!r}] must be contiguous [B, max_len, heads, head_dim]")
-    dt = _round_dtype(out["k"], "out", (SPEC_F32, SPEC_BF16, SPEC_F16))
-    _check(lib.kv_cache_read(*ptrs, pages, page, heads, dim, table, width, ln, _ints(start, (B,), "start", True), B,
-                             max_len, _ptr(out["k"]), _ptr(out["v"]), dt, _ptr(out.get("row_status")), _stream(stream)))
+        out = {"k": _new(shape, dtype, dev, stream), "v": _new(shape, dtype, dev, stream),
+               "row_status": _new(B, _I32, dev, stream)}
+    y, z = out["k"], out["v"]
+    dt = _round_dtype(y.dtype, "out", (SPEC_F32, SPEC_BF16, SPEC_F16))
+    one = (B,)
+    rc = lib.kv_cache_read(*ptrs, pages, page, heads, dim, table, width, ln, _arg(start, _I32, one, "start"), B, max_len,
+                           _arg(y, y.dtype, shape, "out['k']"), _arg(z, y.dtype, shape, "out['v']"), dt,
+                           _arg(out.get("row_status"), _I32, one, "row_status"), _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
     return out
+
+
+_attn_bytes = {}
 
 
 def verify_attention(q, cache, page_table, lens, *, k=None, v=None, parents=None, n_rows=None,
@@ -649,32 +686,44 @@ def verify_attention(q, cache, page_table, lens, *, k=None, v=None, parents=None
     with ``lse``, lse [B, T, Hq] in fp32).
     """
     lib = load()
-    _need_cuda(q, k, v)
+    if not q.is_cuda:
+        _not_cuda()
     if q.dim() != 4:
         raise ValueError("q must be [B, T, Hq, D]")
     B, T, hq, dim = q.shape
-    dt = _round_dtype(q, "q", (SPEC_BF16, SPEC_F16))
+    dev = q.device
+    dt = _round_dtype(q.dtype, "q", (SPEC_BF16, SPEC_F16))
     pages, hkv, page, d, width, ptrs, table, ln = _cache_args(cache, page_table, lens, B)
     if d != dim or hq % hkv:
         raise ValueError(f"q has {hq} heads of {dim}, the cache {hkv} of {d}")
-    if (k is None) != (v is None):
+    if k is None and v is None:
+        kp = vp = kst = vst = None
+    elif k is None or v is None:
         raise ValueError("k and v come together")
-    if k is not None and not (k.shape == v.shape == (B, T, hkv, dim) and k.dtype == v.dtype == q.dtype):
-        raise ValueError("k and v must be [B, T, Hkv, D] of q's dtype")
+    else:
+        if k.shape != (B, T, hkv, dim) or v.shape != k.shape or k.dtype is not q.dtype or v.dtype is not q.dtype:
+            raise ValueError("k and v must be [B, T, Hkv, D] of q's dtype")
+        if not (k.is_cuda and v.is_cuda):
+            _not_cuda()
+        kp, vp, kst, vst = k.data_ptr(), v.data_ptr(), _strides(k, 3), _strides(v, 3)
     if out is None:
-        out = dict(out=_new((B, T, hq, dim), q.dtype, q.device, stream),
-                   row_status=_new(B, torch.int32, q.device, stream))
+        out = {"out": _new(q.shape, q.dtype, dev, stream), "row_status": _new(B, _I32, dev, stream)}
         if lse:
-            out["lse"] = _new((B, T, hq), torch.float32, q.device, stream)
-    if out["out"].shape != q.shape or out["out"].dtype != q.dtype or not out["out"].is_contiguous():
+            out["lse"] = _new((B, T, hq), _F32, dev, stream)
+    y = out["out"]
+    if y.shape != q.shape or y.dtype is not q.dtype or not y.is_contiguous():
         raise ValueError("out['out'] must be contiguous, with q's shape and dtype")
-    nbytes = int(lib.verify_attention_workspace_bytes(B, T, hq, hkv, dim))
-    ws = _round_workspace(workspace, q.device, stream, nbytes)
-    s = float(dim) ** -0.5 if scale is None else float(scale)
-    _check(lib.verify_attention(
-        _ptr(q), _strides(q, 3), _ptr(k), None if k is None else _strides(k, 3), _ptr(v),
-        None if v is None else _strides(v, 3), dt, B, T, hq, hkv, dim, *ptrs, pages, page, table, width, ln,
-        _ints(parents, (B, T - 1), "parents", True) if T > 1 else None, _ints(n_rows, (B,), "n_rows", True), s,
-        _ptr(out["out"]), _floats(out.get("lse"), (B, T, hq), "lse"), _ptr(out.get("row_status")), _ptr(ws),
-        ws.numel(), _stream(stream)))
+    key = (T, hq, hkv, dim)
+    nbytes = _attn_bytes.get(key)
+    if nbytes is None:
+        nbytes = _attn_bytes[key] = int(lib.verify_attention_workspace_bytes(1, *key))
+    raw = _raw_stream(stream, dev)
+    ws = _round_workspace(workspace, dev, stream, raw, max(nbytes, 256))
+    rc = lib.verify_attention(
+        q.data_ptr(), _strides(q, 3), kp, kst, vp, vst, dt, B, T, hq, hkv, dim, *ptrs, pages, page, table, width, ln,
+        _arg(parents, _I32, (B, T - 1), "parents") if T > 1 else None, _arg(n_rows, _I32, (B,), "n_rows"),
+        dim ** -0.5 if scale is None else scale, y.data_ptr(), _arg(out.get("lse"), _F32, (B, T, hq), "lse"),
+        _arg(out.get("row_status"), _I32, (B,), "row_status"), ws.data_ptr(), ws.numel(), raw)
+    if rc:
+        _check(rc)
     return out

@@ -12,6 +12,8 @@
 // Read.  One 16-byte vector of codes per thread and step, scaled and rounded once to the type asked for.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "sv_round.cuh"
 
 namespace sv {
@@ -81,8 +83,6 @@ __device__ __forceinline__ uint4 load16(const void* base, int64_t elem)
 __device__ int write_status(const CacheWriteParams& P, int b, int len, int count)
 {
     __shared__ int bad;
-    if (threadIdx.x == 0) bad = ROW_OK;
-    __syncthreads();
     const long long room = (long long)P.table_width * P.page;
     int mine = ROW_OK;
     if (len < 0 || count > P.T || (long long)len + count > room ||
@@ -96,7 +96,10 @@ __device__ int write_status(const CacheWriteParams& P, int b, int len, int count
             for (int i = threadIdx.x; i < count - 1; i += blockDim.x)
                 if ((unsigned)__ldg(P.out_nodes + (size_t)b * P.nodes_width + i) >= (unsigned)(P.T - 1)) mine = max(mine, (int)ROW_BAD_NODE);
     }
-    if (mine != ROW_OK) atomicMax(&bad, mine);
+    if (!__syncthreads_or(mine != ROW_OK)) return ROW_OK;
+    if (threadIdx.x == 0) bad = ROW_OK;
+    __syncthreads();
+    atomicMax(&bad, mine);
     __syncthreads();
     return bad;
 }
@@ -110,19 +113,13 @@ __global__ void __launch_bounds__(NT) cache_write_kernel(CacheWriteParams P)
     const int which = blockIdx.y & 1, h = blockIdx.y >> 1, b = blockIdx.z, t = threadIdx.x;
     const int len = __ldg(P.lens + b);
     const int count = P.accepted_len ? min(max(__ldg(P.accepted_len + b), -1), P.T) + 1 : P.T;
-    const int status = write_status(P, b, len, count);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) {
-        if (P.row_status) P.row_status[b] = status;
-        if (P.lens_out) P.lens_out[b] = status == ROW_OK ? len + count : len;
-    }
-    if (status != ROW_OK) return;
     const int j = len / P.page + blockIdx.x;                       // page of the request
     const int first = max((int)(len - (long long)j * P.page), 0);  // slots the request held before
     const long long r0 = (long long)j * P.page + first - len;      // the first row that goes into this page
-    if (r0 >= count) return;
-    const int rows = (int)min((long long)count - r0, (long long)(P.page - first));
-    const int page = __ldg(P.page_table + (size_t)b * P.table_width + j);
+    const int rows = len < 0 ? 0 : (int)max(0LL, min(min((long long)count, (long long)P.T) - r0, (long long)(P.page - first)));
 
+    // The rows are on their way while the request is looked over: a prompt's CTAs spend their time in that chain of loads.
+    // (A node that is out of range is clamped here and refused below.)
     const int vpr = P.D / VEC;  // vectors per row
     uint4 x[NV];
     float amax = 0.0f;
@@ -132,10 +129,19 @@ __global__ void __launch_bounds__(NT) cache_write_kernel(CacheWriteParams P)
         x[k] = make_uint4(0, 0, 0, 0);
         if (i < rows * vpr) {
             const int at = (int)r0 + i / vpr;
-            const int row = !P.out_nodes || at == 0 ? at : __ldg(P.out_nodes + (size_t)b * P.nodes_width + at - 1) + 1;
+            int row = at;
+            if (P.out_nodes && at > 0)
+                row = at - 1 < P.nodes_width ? min(max(__ldg(P.out_nodes + (size_t)b * P.nodes_width + at - 1), -1), P.T - 2) + 1 : 0;
             x[k] = load16<DT, ALIGNED>(P.src[which], b * P.sb[which] + row * P.st[which] + h * P.sh[which] + (i % vpr) * VEC);
         }
     }
+    const int status = write_status(P, b, len, count);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) {
+        if (P.row_status) P.row_status[b] = status;
+        if (P.lens_out) P.lens_out[b] = status == ROW_OK ? len + count : len;
+    }
+    if (status != ROW_OK || rows <= 0) return;
+    const int page = __ldg(P.page_table + (size_t)b * P.table_width + j);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         float f[VEC];
@@ -247,14 +253,16 @@ __device__ __forceinline__ void store_codes(void* out, int64_t elem, const uint4
     }
 }
 
-// Vector i of the output covers 16 channels of (b, token, head); consecutive threads take consecutive
-// vectors, so stores are contiguous and loads come in runs of a head's D bytes.
+// A thread keeps one place (16 channels of a head) and steps through tokens, so consecutive threads store consecutive
+// vectors and load runs of a head's D bytes, and no index needs a division.
+constexpr int RU = 8;  // tokens in flight per thread
+
 template <int DT>
 __global__ void __launch_bounds__(NT) cache_read_kernel(CacheReadParams P)
 {
-    const int which = blockIdx.z, b = blockIdx.y;
-    const int vpt = P.Hkv * P.D / 16;
-    const long long n = (long long)P.max_len * vpt;
+    const int which = blockIdx.z, b = blockIdx.y, t = threadIdx.x;
+    const int vpt = P.Hkv * P.D / 16;                // places of a token
+    const int tpb = max(1, NT / vpt);                // tokens a CTA takes per step
     const int start = P.start ? __ldg(P.start + b) : 0;
     const int len = __ldg(P.lens + b);
     const long long room = (long long)P.table_width * P.page;
@@ -264,41 +272,43 @@ __global__ void __launch_bounds__(NT) cache_read_kernel(CacheReadParams P)
         int mine = bad_len ? ROW_BAD_LENGTH : ROW_OK;
         if (!bad_len) {
             const long long stop = min((long long)len, (long long)start + P.max_len);
-            for (long long j = start / P.page + (long long)threadIdx.x; j * P.page < stop; j += NT)
+            for (long long j = start / P.page + (long long)t; j * P.page < stop; j += NT)
                 if ((unsigned)__ldg(table + j) >= (unsigned)P.pages) mine = ROW_BAD_PAGE;
         }
         mine = __syncthreads_or(mine == ROW_BAD_PAGE) ? ROW_BAD_PAGE : mine;
-        if (threadIdx.x == 0) P.row_status[b] = mine;
+        if (t == 0) P.row_status[b] = mine;
     }
-    constexpr int U = 4;  // vectors in flight per thread
-    const long long stride = (long long)gridDim.x * NT;
-    for (long long i0 = (long long)blockIdx.x * NT + threadIdx.x; i0 < n; i0 += U * stride) {
-        uint4 w[U];
-        float s[U];
+    if (t >= tpb * vpt && vpt <= NT) return;
+    const float nan = __int_as_float(0x7fc00000);
+    const int shift = P.page_shift;
+    for (int place = vpt <= NT ? t % vpt : t; place < vpt; place += NT) {
+        const int h = place / (P.D / 16), ch = place % (P.D / 16) * 16;
+        const uint8_t* codes = P.codes[which] + ((size_t)h << shift) * P.D + ch;
+        const float* scale = P.scale[which] + h;
+        const long long block = (long long)P.Hkv * P.D << shift;  // codes of a page
+        for (long long i0 = (long long)blockIdx.x * tpb * RU + (vpt <= NT ? t / vpt : 0); i0 < P.max_len; i0 += (long long)gridDim.x * tpb * RU) {
+            uint4 w[RU];
+            float s[RU];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const long long i = i0 + k * stride;
-            w[k] = make_uint4(0, 0, 0, 0);
-            s[k] = bad_len ? __int_as_float(0x7fc00000) : 0.0f;
-            if (i < n && !bad_len) {
-                const long long tok = start + i / vpt;
-                if (tok < len) {
-                    const int hv = (int)(i % vpt), h = hv / (P.D / 16);
-                    const int page = __ldg(table + tok / P.page);
+            for (int k = 0; k < RU; ++k) {
+                const long long i = i0 + k * tpb, tok = start + i;
+                w[k] = make_uint4(0, 0, 0, 0);
+                s[k] = bad_len ? nan : 0.0f;
+                if (i < P.max_len && !bad_len && tok < len) {
+                    const int page = __ldg(table + (tok >> shift));
                     if ((unsigned)page < (unsigned)P.pages) {
-                        const size_t blk = (size_t)page * P.Hkv + h;
-                        s[k] = __ldg(P.scale[which] + blk);
-                        w[k] = ld_stream_v4(P.codes[which] + (blk * P.page + tok % P.page) * P.D + (hv % (P.D / 16)) * 16);
+                        s[k] = __ldg(scale + (size_t)page * P.Hkv);
+                        w[k] = ld_stream_v4(codes + page * block + (tok & (P.page - 1)) * P.D);
                     } else {
-                        s[k] = __int_as_float(0x7fc00000);
+                        s[k] = nan;
                     }
                 }
             }
-        }
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const long long i = i0 + k * stride;
-            if (i < n) store_codes<DT>(P.out[which], ((long long)b * n + i) * 16, w[k], s[k]);
+            for (int k = 0; k < RU; ++k) {
+                const long long i = i0 + k * tpb;
+                if (i < P.max_len) store_codes<DT>(P.out[which], (((long long)b * P.max_len + i) * vpt + place) * 16, w[k], s[k]);
+            }
         }
     }
 }
@@ -319,10 +329,10 @@ cudaError_t launch_cache_write(const CacheWriteParams& P, int dtype, cudaStream_
 
 cudaError_t launch_cache_read(const CacheReadParams& P, int dtype, int sms, cudaStream_t st)
 {
-    const long long n = (long long)P.max_len * P.Hkv * P.D / 16;
-    const long long want = (n + 4 * NT - 1) / (4 * NT);
-    const long long most = max(1LL, 16LL * sms / P.B);  // about eight resident CTAs per SM, two tensors
-    const dim3 grid((unsigned)max(1LL, min(want, most)), (unsigned)P.B, 2);
+    const int vpt = P.Hkv * P.D / 16, step = std::max(1, NT / vpt) * RU;
+    const long long want = (P.max_len + step - 1) / step;
+    const long long most = std::max(1LL, 32LL * sms / P.B);  // several waves, so that ragged requests even out
+    const dim3 grid((unsigned)std::max(1LL, std::min(want, most)), (unsigned)P.B, 2);
     if (dtype == DT_F32) cache_read_kernel<DT_F32><<<grid, NT, 0, st>>>(P);
     else if (dtype == DT_BF16) cache_read_kernel<DT_BF16><<<grid, NT, 0, st>>>(P);
     else cache_read_kernel<DT_F16><<<grid, NT, 0, st>>>(P);

@@ -31,6 +31,7 @@ constexpr uint32_t LW_BIAS = 0x20000000u;   // a bias names the entry
 constexpr uint32_t LW_COUNT = 0x1fffffffu;
 constexpr int LU = 4;                       // vectors in flight per thread
 constexpr int HU = 8;                       // history tokens in flight per thread
+constexpr int LOGITS_MAX_SMEM = 160 * 1024; // more than the longest run, draft and biases take
 constexpr int LMASK = 64;                   // drafted tokens of a run whose paths are kept as bit masks
 constexpr int LMASK_ROWS = 512;             // and the rows that this is done for
 
@@ -398,6 +399,8 @@ cudaError_t launch_chunks(LogitsParams& P, int sms, cudaStream_t st)
         cudaFuncAttributes a;
         const cudaError_t e = cudaFuncGetAttributes(&a, K);
         if (e != cudaSuccess) return e;
+        const cudaError_t f = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, LOGITS_MAX_SMEM);
+        if (f != cudaSuccess) return f;
         per_sm = max(1, min(2048 / NT, 65536 / (((a.numRegs + 7) / 8 * 8) * NT)));
     }
     int best = NT * (VEC == 1 ? 4 : VEC);
@@ -415,8 +418,6 @@ cudaError_t launch_chunks(LogitsParams& P, int sms, cudaStream_t st)
     }
     P.chunk = best;
     const size_t bytes = smem(best);
-    const cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return e;
     K<<<dim3((unsigned)((P.V + best - 1) / best), (unsigned)P.B), NT, bytes, st>>>(P);
     return cudaGetLastError();
 }

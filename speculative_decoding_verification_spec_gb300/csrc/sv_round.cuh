@@ -120,7 +120,7 @@ struct CacheReadParams {
     const int32_t* start;          // nullable: 0
     void* out[2];                  // [B, max_len, Hkv, D]
     int32_t* row_status;
-    int B, max_len, Hkv, D, page, pages, table_width;
+    int B, max_len, Hkv, D, page, page_shift, pages, table_width;
 };
 
 cudaError_t launch_cache_read(const CacheReadParams& P, int dtype, int sms, cudaStream_t st);

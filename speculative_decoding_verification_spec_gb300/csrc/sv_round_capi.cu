@@ -26,6 +26,8 @@ static bool on(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t
 static bool on_or_null(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 static size_t dtype_size(spec_dtype d) { return d == SPEC_F32 ? 4 : 2; }
 
+static int page_shift_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
 // what the three cache calls share
 static bool cache_ok(const void* kc, const void* vc, const float* ks, const float* vs, const int32_t* table,
                      const int32_t* lens, int pages, int table_width, int Hkv, int page, int D)
@@ -181,6 +183,7 @@ spec_status kv_cache_read(const void* k_cache, const void* v_cache, const float*
     P.Hkv = Hkv;
     P.D = D;
     P.page = page_size;
+    P.page_shift = page_shift_of(page_size);
     P.pages = pages;
     P.table_width = table_width;
     const cudaError_t e = launch_cache_read(P, (int)dtype, round_sm_count(), static_cast<cudaStream_t>(stream));
@@ -249,7 +252,7 @@ spec_status verify_attention(const void* q, const int64_t* q_strides, const void
     P.G = Hq / Hkv;
     P.D = D;
     P.page = page_size;
-    P.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+    P.page_shift = page_shift_of(page_size);
     P.pages = pages;
     P.table_width = table_width;
     P.R = T * P.G;
