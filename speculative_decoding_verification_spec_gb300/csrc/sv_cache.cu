@@ -78,6 +78,36 @@ __device__ __forceinline__ uint4 load16(const void* base, int64_t elem)
     }
 }
 
+// The magnitudes of a vector's elements folded into one word as bit patterns, whose order is the magnitudes' (an infinity and
+// NaN above all numbers): 16-bit types keep two maxima side by side.
+template <int DT>
+__device__ __forceinline__ uint32_t fold_magnitude(uint32_t m, const uint4& w)
+{
+    if constexpr (DT == DT_F32) {
+        constexpr uint32_t A = 0x7fffffffu;
+        return max(max(max(m, w.x & A), max(w.y & A, w.z & A)), w.w & A);
+    } else {
+        constexpr uint32_t A = 0x7fff7fffu;
+        return __vmaxu2(__vmaxu2(m, __vmaxu2(w.x & A, w.y & A)), __vmaxu2(w.z & A, w.w & A));
+    }
+}
+// the larger of the folded maxima as a float
+template <int DT>
+__device__ __forceinline__ float magnitude(uint32_t m)
+{
+    if constexpr (DT == DT_F32) return __uint_as_float(m);
+    const uint32_t h = max(m & 0xffffu, m >> 16);
+    return DT == DT_BF16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
+}
+
+// two scaled values as codes, `lo` in the low byte, where both are numbers of at most 448
+__device__ __forceinline__ uint16_t e4m3x2_plain(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Whether request b's rows can be written, looked at by every CTA of the request alike, so that either
 // all of them write or none.  Called by all threads.
 __device__ int write_status(const CacheWriteParams& P, int b, int len, int count)
@@ -106,10 +136,10 @@ __device__ int write_status(const CacheWriteParams& P, int b, int len, int count
 
 // NV: 16-byte source vectors per thread, at most (a page's worth over NT threads, rounded up to a power of two)
 template <int DT, int NV, bool ALIGNED>
-__global__ void __launch_bounds__(NT) cache_write_kernel(CacheWriteParams P)
+__global__ void __launch_bounds__(NT, NV <= 4 ? 6 : 1) cache_write_kernel(CacheWriteParams P)
 {
     constexpr int VEC = Elem<DT>::VEC;
-    __shared__ float red[WARPS];
+    __shared__ uint32_t red[WARPS];
     const int which = blockIdx.y & 1, h = blockIdx.y >> 1, b = blockIdx.z, t = threadIdx.x;
     const int len = __ldg(P.lens + b);
     const int count = P.accepted_len ? min(max(__ldg(P.accepted_len + b), -1), P.T) + 1 : P.T;
@@ -120,47 +150,57 @@ __global__ void __launch_bounds__(NT) cache_write_kernel(CacheWriteParams P)
 
     // The rows are on their way while the request is looked over: a prompt's CTAs spend their time in that chain of loads.
     // (A node that is out of range is clamped here and refused below.)
-    const int vpr = P.D / VEC;  // vectors per row
+    const int vshift = 31 - __clz(P.D / VEC), vpr = 1 << vshift;  // vectors per row
     uint4 x[NV];
-    float amax = 0.0f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int i = t + k * NT;
         x[k] = make_uint4(0, 0, 0, 0);
         if (i < rows * vpr) {
-            const int at = (int)r0 + i / vpr;
+            const int at = (int)r0 + (i >> vshift);
             int row = at;
             if (P.out_nodes && at > 0)
                 row = at - 1 < P.nodes_width ? min(max(__ldg(P.out_nodes + (size_t)b * P.nodes_width + at - 1), -1), P.T - 2) + 1 : 0;
-            x[k] = load16<DT, ALIGNED>(P.src[which], b * P.sb[which] + row * P.st[which] + h * P.sh[which] + (i % vpr) * VEC);
+            x[k] = load16<DT, ALIGNED>(P.src[which], b * P.sb[which] + row * P.st[which] + h * P.sh[which] + (i & (vpr - 1)) * VEC);
         }
     }
+    const int page = rows > 0 && j < P.table_width ? __ldg(P.page_table + (size_t)b * P.table_width + j) : 0;
     const int status = write_status(P, b, len, count);
     if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) {
         if (P.row_status) P.row_status[b] = status;
         if (P.lens_out) P.lens_out[b] = status == ROW_OK ? len + count : len;
     }
     if (status != ROW_OK || rows <= 0) return;
-    const int page = __ldg(P.page_table + (size_t)b * P.table_width + j);
+    uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        float f[VEC];
-        widen<DT>(x[k], f);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float a = fabsf(f[e]);
-            // what the largest scale cannot hold (and an infinity) becomes NaN and sets no scale
-            if (a <= CACHE_MAX_CODE * 0x1p60f) amax = fmaxf(amax, a);
-        }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if ((t & 31) == 0) red[t >> 5] = amax;
+    for (int k = 0; k < NV; ++k) top = fold_magnitude<DT>(top, x[k]);
+    top = __reduce_max_sync(0xffffffffu, __float_as_uint(magnitude<DT>(top)));
+    if ((t & 31) == 0) red[t >> 5] = top;
     float* sp = P.scale[which] + (size_t)page * P.Hkv + h;
     const float old = first > 0 ? *sp : 0.0f;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) amax = fmaxf(amax, red[w]);
+    for (int w = 0; w < WARPS; ++w) top = max(top, red[w]);
+    float amax = __uint_as_float(top);
+    const bool plain = amax <= CACHE_MAX_CODE * 0x1p60f;
+    if (!plain) {
+        // something that no scale holds (or an infinity, or NaN): it becomes NaN and sets no scale
+        amax = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float f[VEC];
+            widen<DT>(x[k], f);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (fabsf(f[e]) <= CACHE_MAX_CODE * 0x1p60f) amax = fmaxf(amax, fabsf(f[e]));
+        }
+        amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+        __syncthreads();
+        if ((t & 31) == 0) red[t >> 5] = __float_as_uint(amax);
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) amax = fmaxf(amax, __uint_as_float(red[w]));
+    }
     const int e = cache_scale_exp(amax);
     float s = exp2_int(e);
     float inv = exp2_int(-e);
@@ -194,8 +234,9 @@ __global__ void __launch_bounds__(NT) cache_write_kernel(CacheWriteParams P)
             widen<DT>(x[k], f);
             uint16_t c[VEC / 2];
 #pragma unroll
-            for (int q = 0; q < VEC / 2; ++q) c[q] = e4m3x2_from(f[2 * q] * inv, f[2 * q + 1] * inv);
-            uint8_t* o = dst + (size_t)(first + i / vpr) * P.D + (i % vpr) * VEC;
+            for (int q = 0; q < VEC / 2; ++q)
+                c[q] = plain ? e4m3x2_plain(f[2 * q] * inv, f[2 * q + 1] * inv) : e4m3x2_from(f[2 * q] * inv, f[2 * q + 1] * inv);
+            uint8_t* o = dst + first * P.D + i * VEC;
             if constexpr (VEC == 8)
                 *reinterpret_cast<uint2*>(o) = make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
             else
