@@ -526,3 +526,73 @@ def test_logits_bad_parent():
     c["parents"][2, 0] = -2
     out = check_logits(c)
     assert out["row_status"].tolist() == [0, B_.ROW_BAD_PARENT, B_.ROW_BAD_PARENT]
+
+
+# ------------------------------------------------------------------ waits and the whole round
+
+def test_attention_wait_limit_reports_a_timeout():
+    """With no polls allowed every wait of the many-rows kernel runs out at once: status and NaN, no hang; afterwards the
+    same call gives what it gave before."""
+    g = torch.Generator().manual_seed(31)
+    p = Pool(g, [700, 3, 0], 2, 64, 128)
+    q, kn, vn = round_inputs(g, 3, 6, 8, 2, 128, "bf16")
+    clean = run_attention(p, q, kn, vn)
+    old = sv.set_wait_limit(0)
+    try:
+        r = run_attention(p, q, kn, vn)
+    finally:
+        sv.set_wait_limit(old)
+    assert r["row_status"].tolist() == [B_.ROW_TIMEOUT] * 3
+    assert bool(r["out"].isnan().all()) and bool(r["lse"].isnan().all())
+    again = run_attention(p, q, kn, vn)
+    assert torch.equal(again["out"], clean["out"]) and torch.equal(again["lse"], clean["lse"])
+
+
+@pytest.mark.parametrize("T,hq,hkv,dtype", [(24, 16, 1, "bf16"), (40, 16, 1, "f16"), (65, 16, 1, "bf16"), (17, 1, 1, "f16"), (128, 2, 1, "bf16")])
+def test_attention_many_rows_of_a_head(T, hq, hkv, dtype):
+    """Rows that fill several row tiles, with an odd rest."""
+    g = torch.Generator().manual_seed(T * hq)
+    p = Pool(g, [129, 1000], hkv, 128, 128)
+    q, kn, vn = round_inputs(g, 2, T, hq, hkv, 128, dtype)
+    check_attention(p, q, kn, vn)
+
+
+@pytest.mark.parametrize("hq,T", [(1, 1), (8, 5)])
+def test_attention_reference_moves_late(hq, T):
+    """Scores that climb along the context, so that the running maximum leaves its window again and again."""
+    g = torch.Generator().manual_seed(33)
+    p = Pool(g, [2000], 1, 16, 64)
+    q, kn, vn = round_inputs(g, 1, T, hq, 1, 64, "bf16")
+    q[:] = q.abs() + 0.5
+    for j in range(125):
+        page = int(p.table[0, j])
+        p.codes[0][page] = torch.full((1, 16, 64), 1.0 + 0.0625 * (j % 8)).to(R.FP8)
+        p.scales[0][page] = 2.0 ** (-6 + j // 16)
+    p.cache.k.view(torch.uint8).copy_(p.codes[0].view(torch.uint8).cuda())
+    p.cache.k_scale.copy_(p.scales[0])
+    check_attention(p, q, kn, vn)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_example_runs_a_whole_round(tree):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "verification_round.py")
+    spec = importlib.util.spec_from_file_location("verification_round", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    r = ex.run(rounds=3, tree=tree)
+    acc = r["accepted"]
+    assert bool((acc >= 0).all())
+    if tree:
+        assert int(acc.sum()) > 0
+    assert r["lens"].tolist() == (149 + (acc + 1).sum(0)).tolist()
+    assert r["hist_len"].tolist() == (r["lens"] + 1).tolist()
+    # what the cache holds are the keys of the committed tokens, to a code's precision
+    toy = r["toy"]
+    for b in range(acc.shape[1]):
+        n = int(r["lens"][b])
+        _, _, k, _ = toy.qkv(r["history"][b, :n])
+        got, want = r["cache_k"][b, :n], k.float()
+        lim = 2.0 ** -4 * want.abs() + 2.0 ** -10 * (2 * want.abs().max() / 448 * 2)
+        assert bool(((got - want).abs() <= lim).all())
