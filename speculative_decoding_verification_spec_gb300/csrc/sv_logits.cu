@@ -200,31 +200,39 @@ __global__ void __launch_bounds__(NT, 5) process_logits_kernel(LogitsParams P)
     const char* in0 = reinterpret_cast<const char*>(P.logits) + (size_t)b * P.in_b * ES;
     char* out0 = reinterpret_cast<char*>(P.out) + (size_t)b * P.out_b * ES;
     const uint32_t* allowed0 = MASK ? P.allowed + (size_t)b * P.R * P.mwords : nullptr;
-    for (int i = t; i < room + room / 32; i += NT) smem[i] = 0u;
+    // Everything of the first round of loads is asked for at once: one after another, with barriers between, the lengths, the
+    // history, the biases and the draft would take as long as the copy.
+    const int32_t* h = P.history + (size_t)b * P.H;
+    const int32_t hl_ = P.history_len ? __ldg(P.history_len + b) : P.H, pl = P.prompt_len ? __ldg(P.prompt_len + b) : 0;
+    int32_t said[HU];
+#pragma unroll
+    for (int j = 0; j < HU; ++j) said[j] = t + j * NT < P.H ? __ldg(h + t + j * NT) : -1;
+    const int32_t bias_t = t < P.nb ? __ldg(P.bias_tokens + (size_t)b * P.nb + t) : -1;
+    const int32_t draft_t = t < P.N ? __ldg(P.tokens + (size_t)b * P.N + t) : -1;
+    for (int i = t; i < (room + room / 32) / 4; i += NT) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = (room + room / 32) / 4 * 4 + t; i < room + room / 32; i += NT) smem[i] = 0u;
     if (t == 0) ndraft = 0, nentry = 0, nbias = 0, nlist = 0, bad = 0;
     if (t < LMASK) same[t] = 0;
     __syncthreads();
 
-    if (P.history) {
-        const int hl = min(max(P.history_len ? __ldg(P.history_len + b) : P.H, 0), P.H);
-        const int pl = P.prompt_len ? __ldg(P.prompt_len + b) : 0;
-        const int32_t* h = P.history + (size_t)b * P.H;
-        for (int i0 = t; i0 < hl; i0 += NT * HU) {
-            uint32_t k[HU];
+    const int hl = min(max((int)hl_, 0), P.H);
+    for (int i0 = t; i0 < hl; i0 += NT * HU) {
+        if (i0 != t) {
 #pragma unroll
-            for (int j = 0; j < HU; ++j) k[j] = i0 + j * NT < hl ? (uint32_t)(__ldg(h + i0 + j * NT) - v0) : 0xffffffffu;
+            for (int j = 0; j < HU; ++j) said[j] = i0 + j * NT < hl ? __ldg(h + i0 + j * NT) : -1;
+        }
 #pragma unroll
-            for (int j = 0; j < HU; ++j) {
-                if (k[j] < (uint32_t)nw) {
-                    if (i0 + j * NT < pl) atomicOr(&words[k[j]], LW_SEEN);
-                    else atomicAdd(&words[k[j]], 1u);
-                    atomicOr(&bits[k[j] >> 5], 1u << (k[j] & 31));
-                }
+        for (int j = 0; j < HU; ++j) {
+            const uint32_t k = (uint32_t)(said[j] - v0);
+            if (k < (uint32_t)nw && i0 + j * NT < hl) {
+                if (i0 + j * NT < pl) atomicOr(&words[k], LW_SEEN);
+                else atomicAdd(&words[k], 1u);
+                atomicOr(&bits[k >> 5], 1u << (k & 31));
             }
         }
     }
     for (int i = t; i < P.nb; i += NT) {
-        const uint32_t k = (uint32_t)(__ldg(P.bias_tokens + (size_t)b * P.nb + i) - v0);
+        const uint32_t k = (uint32_t)((i == t ? bias_t : __ldg(P.bias_tokens + (size_t)b * P.nb + i)) - v0);
         if (k < (uint32_t)nw) {
             atomicOr(&words[k], LW_BIAS);
             atomicOr(&bits[k >> 5], 1u << (k & 31));
@@ -235,7 +243,7 @@ __global__ void __launch_bounds__(NT, 5) process_logits_kernel(LogitsParams P)
     // A drafted entry's word moves to `base` and makes room for the entry's number: the one thread that finds the
     // word unflagged does it.
     for (int i = t; i < P.N; i += NT) {
-        const uint32_t k = (uint32_t)(__ldg(P.tokens + (size_t)b * P.N + i) - v0);
+        const uint32_t k = (uint32_t)((i == t ? draft_t : __ldg(P.tokens + (size_t)b * P.N + i)) - v0);
         if (k < (uint32_t)nw) {
             const uint32_t was = atomicOr(&words[k], LW_DRAFT);
             draft[atomicAdd(&ndraft, 1)] = (uint16_t)i;
@@ -389,8 +397,10 @@ __global__ void __launch_bounds__(NT, 5) process_logits_kernel(LogitsParams P)
 template <auto K, int VEC>
 cudaError_t launch_chunks(LogitsParams& P, int sms, cudaStream_t st)
 {
-    // The run length whose grid leaves the fewest SM slots idle in its last wave; of equal ones the longest, which
-    // reads the history least often.  At least one vector per thread.
+    // The run length with the best of: few SM slots idle in the grid's last wave, and little time per run spent on anything
+    // but its rows (reading the history, barriers, the touched entries: measured as long as some 24 KB of rows).  At
+    // (B, R, V, H) = (64, 6, 128256, 2048) runs of 2048, 4096 and 8192 entries take 67, 65 and 79 us, at (32, 65, 128256, 4000)
+    // 290, 335 and 398 us, at (200, 2, 128256, 2048) 110, 83 and 85 us.
     const auto smem = [&](int chunk) {
         return ((size_t)chunk + 32 + (chunk + 32) / 32 + P.N) * 4 + ((size_t)chunk + 32 + P.N + P.nb + 1) / 2 * 4;
     };
@@ -411,8 +421,9 @@ cudaError_t launch_chunks(LogitsParams& P, int sms, cudaStream_t st)
         const long long slots = (long long)sms * min(per_sm, (int)(220000 / (smem(chunk) + 6144)));
         if (slots < 1) continue;
         const double full = (double)P.V * P.B / ((double)chunk * ((ctas + slots - 1) / slots * slots));
-        if (full > 1.02 * most) {
-            most = full;
+        const double rows = 2.0 * chunk * P.R * (16 / (VEC == 1 ? 8 : VEC)), score = full * rows / (rows + 24576.0 + 4.0 * P.H);
+        if (score > most) {
+            most = score;
             best = chunk;
         }
     }
