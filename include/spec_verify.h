@@ -1,7 +1,7 @@
 /*
  * spec_verify.h -- C ABI of the GB300 (sm_103a) speculative-decoding verify library.
  *
- * Three verify calls, each one pass of the target-side verify step over a batch of B independent
+ * The verify calls, each one pass of the target-side verify step over a batch of B independent
  * requests, entirely on the GPU:
  *
  *   spec_verify        exact speculative sampling with temperature
@@ -13,6 +13,12 @@
  *   tree_verify_sample stochastic verification of a candidate tree (residual update over children)
  *   tree_verify_typical Medusa-style tree verification by typical acceptance (entropy threshold)
  *   smc_verify         the verify side of one SMC-SD round: block weights, extension, resampling
+ *
+ * and, around the verify step of a round:
+ *
+ *   verify_attention   attention of the round's rows over an 8-bit paged key/value cache and the round's own rows
+ *   process_logits     penalties for repeated tokens, biases and a grammar mask on the round's logits
+ *   kv_cache_write     the commit of the accepted rows, quantised as they are written; kv_cache_read reads them back
  *
  * Sources (page title + section):
  *   "M7.1 - Speculative Decoding: Draft, Verify, Accept, Reject": 0x03 (accept probability and
@@ -493,8 +499,9 @@ size_t verify_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
  *   out [B, T, Hq, D] = sum_j softmax(s)_j v_j, dense, 16-byte aligned;  lse [B, T, Hq] (nullable, fp32) = log sum_j exp(s_j)
  * A row that sees nothing gives zeros and -inf.  What a row does not see has no effect on it, whatever it
  * holds.  Scores, softmax and sums are fp32; out is rounded once.  A row of q that holds a NaN or an infinity gives
- * NaN.
- * row_status [B] (nullable): SPEC_ROW_BAD_LENGTH, BAD_PAGE, BAD_PARENT; the request's out and lse are NaN.
+ * NaN, and so does a key of the round that does, for the rows that see it.
+ * row_status [B] (nullable): SPEC_ROW_BAD_LENGTH, BAD_PAGE, BAD_PARENT, and SPEC_ROW_TIMEOUT where more than 16 rows share
+ * a key/value head (T Hq / Hkv; that path waits on mbarriers); the request's out and lse are NaN.
  * workspace: verify_attention_workspace_bytes(...), 16-byte aligned, no initialisation needed.
  */
 spec_status verify_attention(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
@@ -524,7 +531,8 @@ void spec_set_kernel_events(void* start, void* stop);
  * Test aid: the number of polls after which a bounded wait of the streaming kernels gives up.
  *
  * The streaming kernels (spec_verify and its processors, spec_verify_topk, tree_verify_greedy,
- * spec_verify_greedy, tree_verify_typical, smc_verify) wait only inside one CTA, on mbarriers:
+ * spec_verify_greedy, tree_verify_typical, smc_verify, and verify_attention with more than 16 rows per
+ * key/value head) wait only inside one CTA, on mbarriers:
  * for a bulk copy of a chunk to land, for the CTA's consumer warps to free a ring stage, and
  * (top-k) for a segment's first bound and its completion.  Each such wait is bounded.  When one
  * runs out, the CTA stops reading, marks every chunk it has not read, still waits for its copies

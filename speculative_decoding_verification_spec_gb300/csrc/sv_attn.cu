@@ -32,6 +32,7 @@ constexpr int ANT = AW * 32;
 constexpr int SLICE = 16;       // tokens of a warp per tile
 constexpr int TILE = AW * SLICE;
 constexpr int ASTAGES = 4;
+constexpr int MT = 1, MR = MT * 16;  // rows: one 16-row tile of the product
 
 __device__ __forceinline__ uint32_t swz_off(int D, int row, int chunk)
 {
@@ -60,17 +61,17 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
 
 // ---------------------------------------------------------------- the streaming kernel
 
-template <int D, int MT>
+template <int D>
 struct RowState {
     float o[MT][D / 8][4];
     float m[MT][2], l[MT][2];
 };
 
-// One slice of 16 tokens against the CTA's rows.  kf(nt, c, w): the four halves-pairs ... see the two callers.
-// u_scale(nt, j), u_add(nt, j), l_scale(nt, j): per token column (2t + j of n-tile nt); see(mt, hi, nt, j): whether row g
-// (+ 8 hi) of m-tile mt sees the column.
-template <int D, int MT, class KFrag, class VFrag, class Scale, class Add, class LScale, class See>
-__device__ __forceinline__ void slice_step(RowState<D, MT>& S, const uint32_t (&qf)[MT][D / 16][4], const float (&F)[MT][2],
+// One slice of 16 tokens (two n-tiles of 8 columns) against the CTA's rows.  kfrag(nt, cc, kb) and vfrag(q, vb) give the operand
+// pairs of four product steps; u_scale, u_add, l_scale (nt, j): key scale, value exponent and 2^-exponent of column 2 t4 + j of
+// n-tile nt; see(mt, hi, nt, j): whether row g (+ 8 hi) of m-tile mt sees that column.
+template <int D, class KFrag, class VFrag, class Scale, class Add, class LScale, class See>
+__device__ __forceinline__ void slice_step(RowState<D>& S, const uint32_t (&qf)[MT][D / 16][4], const float (&F)[MT][2],
                                            KFrag kfrag, VFrag vfrag, Scale u_scale, Add u_add, LScale l_scale, See see)
 {
     float s[MT][2][4];
@@ -150,10 +151,9 @@ __device__ __forceinline__ void slice_step(RowState<D, MT>& S, const uint32_t (&
 // phase of a fragment load reads lie in different banks for keys and values alike
 __device__ __forceinline__ int col_token(int n) { return n & 1 ? (n - 1) ^ 5 : n; }
 
-template <int DT, int D, int MT>
-__global__ void __launch_bounds__(ANT, MT == 1 ? 3 : 2) attn_rows_kernel(AttnParams P)
+template <int DT, int D>
+__global__ void __launch_bounds__(ANT, 3) attn_rows_kernel(AttnParams P)
 {
-    constexpr int MR = MT * 16;
     constexpr int KB = SLICE * D;        // bytes of a slice's keys (or values)
     constexpr int STAGE = 2 * KB;
     extern __shared__ __align__(128) uint8_t ring[];  // [AW][ASTAGES][STAGE]; at a group's end [AW][MR][D] floats
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(ANT, MT == 1 ? 3 : 2) attn_rows_kernel(AttnPar
         __syncthreads();
         uint32_t qf[MT][D / 16][4];
         float F[MT][2];
-        RowState<D, MT> S;
+        RowState<D> S;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -326,9 +326,9 @@ __global__ void __launch_bounds__(ANT, MT == 1 ? 3 : 2) attn_rows_kernel(AttnPar
             auto uadd = [&](int, int) { return ve; };
             auto lscale = [&](int, int) { return inv; };
             if (left >= SLICE)
-                slice_step<D, MT>(S, qf, F, kfrag, vfrag, uscale, uadd, lscale, [](int, int, int, int) { return true; });
+                slice_step<D>(S, qf, F, kfrag, vfrag, uscale, uadd, lscale, [](int, int, int, int) { return true; });
             else
-                slice_step<D, MT>(S, qf, F, kfrag, vfrag, uscale, uadd, lscale, [&](int, int, int nt, int j) {
+                slice_step<D>(S, qf, F, kfrag, vfrag, uscale, uadd, lscale, [&](int, int, int nt, int j) {
                     return nt * 8 + (j ? (2 * t4) ^ 5 : 2 * t4) < left;
                 });
         }
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(ANT, MT == 1 ? 3 : 2) attn_rows_kernel(AttnPar
                     }
                     if (lane == 0) {
                         if (which) fve[w][i] = (float)e;
-                        else fks[w][i] = exp2_int(e);
+                        else fks[w][i] = fin ? exp2_int(e) : __int_as_float(0x7fc00000);  // a key that is not finite: NaN
                     }
                 }
             }
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(ANT, MT == 1 ? 3 : 2) attn_rows_kernel(AttnPar
             auto vis = [&](int mt, int hi, int nt, int j) {
                 return (smask[mt * 16 + 8 * hi + g] >> (w * SLICE + ctok(nt, j)) & 1ull) != 0;
             };
-            slice_step<D, MT>(S, qf, F, kfrag, vfrag, [&](int nt, int j) { return fks[w][ctok(nt, j)]; },
+            slice_step<D>(S, qf, F, kfrag, vfrag, [&](int nt, int j) { return fks[w][ctok(nt, j)]; },
                               [&](int nt, int j) { return fve[w][ctok(nt, j)]; },
                               [&](int nt, int j) { return exp2_int(-(int)fve[w][ctok(nt, j)]); }, vis);
             // values that are not finite reach the rows that see them
@@ -633,14 +633,13 @@ cudaError_t launch_merge(const AttnParams& P, int ctas, int MR, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, attn_merge_kernel<DT, D>, P, MR);
 }
 
-template <int DT, int D, int MT>
+template <int DT, int D>
 cudaError_t launch_rows(AttnParams& P, int sms, cudaStream_t st)
 {
-    constexpr int MR = MT * 16;
-    P.RT = (P.R + MR - 1) / MR;
+    P.RT = 1;
     const size_t smem = (size_t)AW * ASTAGES * 2 * SLICE * D;
     static_assert((size_t)AW * ASTAGES * 2 * SLICE * D >= (size_t)AW * MR * D * 4, "the ring holds the warps' sums");
-    auto* k = attn_rows_kernel<DT, D, MT>;
+    auto* k = attn_rows_kernel<DT, D>;
     static int per_sm = 0;
     if (per_sm == 0) {
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -661,7 +660,10 @@ cudaError_t launch_rows(AttnParams& P, int sms, cudaStream_t st)
 template <int DT, int D>
 cudaError_t launch_dim(AttnParams& P, int sms, cudaStream_t st)
 {
-    return P.R <= 16 ? launch_rows<DT, D, 1>(P, sms, st) : launch_attention_tc(P, DT, sms, st);
+    // Rows that fill one 16-row tile of mma.sync stay below the memory's pace there.  More rows take the tensor cores' own path:
+    // with 24 rows (B = 32, T = 6, contexts to 8192) two such tiles took 181 us, it takes 139; with 20 or 24 rows of one short
+    // context both are launch and latency.  With 8 to 16 rows it cannot pay, its tiles cost the same from one row to 48.
+    return P.R <= MR ? launch_rows<DT, D>(P, sms, st) : launch_attention_tc(P, DT, sms, st);
 }
 
 }  // namespace

@@ -596,3 +596,16 @@ def test_example_runs_a_whole_round(tree):
         got, want = r["cache_k"][b, :n], k.float()
         lim = 2.0 ** -4 * want.abs() + 2.0 ** -10 * (2 * want.abs().max() / 448 * 2)
         assert bool(((got - want).abs() <= lim).all())
+
+
+@pytest.mark.parametrize("hq,T", [(2, 4), (8, 9)])
+def test_attention_keys_that_are_not_finite(hq, T):
+    """A key of the round with an infinity gives NaN to the rows that see it and to no other, on both paths."""
+    g = torch.Generator().manual_seed(35)
+    p = Pool(g, [0, 40], 1, 16, 128)
+    q, kn, vn = round_inputs(g, 2, T, hq, 1, 128, "bf16")
+    clean = run_attention(p, q, kn, vn)
+    kn[:, 2, 0, 7] = -math.inf
+    r = run_attention(p, q, kn, vn)
+    assert bool(r["out"][:, 2:].isnan().all()) and bool(r["lse"][:, 2:].isnan().all())
+    assert torch.equal(r["out"][:, :2], clean["out"][:, :2]) and torch.equal(r["lse"][:, :2], clean["lse"][:, :2])
