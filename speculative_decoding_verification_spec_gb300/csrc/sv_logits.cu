@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(NT, 5) process_logits_kernel(LogitsParams P)
     const int n = min(P.chunk, P.V - v0);              // entries of the run
     const int nw = min(n + VEC - 1, P.V - v0);         // and those that its last vectors may reach
     const int t = threadIdx.x;
+    const int r_lo = blockIdx.z * P.rows, r_hi = min(P.R, r_lo + P.rows);  // this CTA's rows
     const char* in0 = reinterpret_cast<const char*>(P.logits) + (size_t)b * P.in_b * ES;
     char* out0 = reinterpret_cast<char*>(P.out) + (size_t)b * P.out_b * ES;
     const uint32_t* allowed0 = MASK ? P.allowed + (size_t)b * P.R * P.mwords : nullptr;
@@ -254,20 +255,20 @@ __global__ void __launch_bounds__(NT, 5) process_logits_kernel(LogitsParams P)
                 atomicOr(&bits[k >> 5], 1u << (k & 31));
             }
         }
-        if (P.parents && blockIdx.x == 0) {
+        if (P.parents && blockIdx.x == 0 && blockIdx.z == 0) {
             const int p = __ldg(P.parents + (size_t)b * P.N + i);
             if (p < -1 || p >= i) bad = 1;
         }
     }
     __syncthreads();
-    if (P.row_status && blockIdx.x == 0 && t == 0) P.row_status[b] = bad ? ROW_BAD_PARENT : ROW_OK;
+    if (P.row_status && blockIdx.x == 0 && blockIdx.z == 0 && t == 0) P.row_status[b] = bad ? ROW_BAD_PARENT : ROW_OK;
     const bool masks = ndraft <= LMASK && P.R <= LMASK_ROWS;
     if (masks && ndraft > 0) {
         if (t < ndraft) {
             const int v = __ldg(P.tokens + (size_t)b * P.N + draft[t]);
             atomicOr(reinterpret_cast<unsigned long long*>(&same[words[v - v0] & LW_COUNT]), 1ull << t);
         }
-        for (int r = t; r < P.R; r += NT) {
+        for (int r = r_lo + t; r < r_hi; r += NT) {
             uint64_t m = 0;
             for (int node = r - 1; node >= 0;) {
                 if (!P.parents) {
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(NT, 5) process_logits_kernel(LogitsParams P)
 
     // the copy, with the mask
     if constexpr (VEC == 1) {
-        for (int r = 0; r < P.R; ++r) {
+        for (int r = r_lo; r < r_hi; ++r) {
             const uint32_t* allowed = MASK ? allowed0 + (size_t)r * P.mwords : nullptr;
             for (int v = v0 + t; v < v0 + n; v += NT) {
                 float x = load_one<DT>(in0 + (size_t)r * P.in_r * ES, v);
@@ -303,8 +304,8 @@ __global__ void __launch_bounds__(NT, 5) process_logits_kernel(LogitsParams P)
     } else {
         // slots: the vectors of a row that a thread may own in this run, threads apart
         const int slots = (n + VEC * NT - 1) / (VEC * NT);
-        const char* in = in0;
-        for (int r = 0, slot = 0; r < P.R;) {
+        const char* in = in0 + (size_t)r_lo * P.in_r * ES;
+        for (int r = r_lo, slot = 0; r < r_hi;) {
             uint4 w[LU];
             uint32_t ok[LU];
             char* to[LU];  // null: no vector
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(NT, 5) process_logits_kernel(LogitsParams P)
             for (int j = 0; j < LU; ++j) {
                 to[j] = nullptr;
                 ok[j] = 0xffffffffu;
-                if (r < P.R) {
+                if (r < r_hi) {
                     const int s = lead_in<DT, VEC>(in);
                     const int first = s + ((v0 - s + VEC - 1) & ~(VEC - 1));  // the first vector that starts in the run
                     const int v = first + (slot * NT + t) * VEC;
@@ -340,8 +341,8 @@ __global__ void __launch_bounds__(NT, 5) process_logits_kernel(LogitsParams P)
             }
         }
         // the entries before a row's first boundary and after its last whole vector: at most VEC - 1 each
-        for (int f = t; f < P.R * 2 * VEC; f += NT) {
-            const int r = f / (2 * VEC), e = f % (2 * VEC);
+        for (int f = t; f < (r_hi - r_lo) * 2 * VEC; f += NT) {
+            const int r = r_lo + f / (2 * VEC), e = f % (2 * VEC);
             const char* row = in0 + (size_t)r * P.in_r * ES;
             const int s = min(lead_in<DT, VEC>(row), P.V);
             const int v = e < VEC ? e : s + ((P.V - s) & ~(VEC - 1)) + e - VEC;
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(NT, 5) process_logits_kernel(LogitsParams P)
     q.pres = P.presence ? __ldg(P.presence + b) : 0.0f;
     q.freq = P.frequency ? __ldg(P.frequency + b) : 0.0f;
     const int touched_n = nlist;
-    const long long items = (long long)P.R * touched_n;
+    const long long items = (long long)(r_hi - r_lo) * touched_n;
     constexpr int TU = 4;
     for (long long i0 = t; i0 < items; i0 += TU * NT) {
         float x[TU];
@@ -378,8 +379,8 @@ __global__ void __launch_bounds__(NT, 5) process_logits_kernel(LogitsParams P)
             const long long i = i0 + j * NT;
             at[j] = -1;
             if (i < items) {
-                const int r = row[j] = items < (1LL << 31) ? (int)((uint32_t)i / (uint32_t)touched_n) : (int)(i / touched_n);
-                const int v = v0 + list[(int)(i - (long long)r * touched_n)];
+                const int k = items < (1LL << 31) ? (int)((uint32_t)i / (uint32_t)touched_n) : (int)(i / touched_n);
+                const int r = row[j] = r_lo + k, v = v0 + list[(int)(i - (long long)k * touched_n)];
                 const char* in = in0 + (size_t)r * P.in_r * ES;
                 if (owns<VEC>(v, min(lead_in<DT, VEC>(in), P.V), P.V, v0, n) &&
                     !(MASK && !(__ldg(allowed0 + (size_t)r * P.mwords + (v >> 5)) >> (v & 31) & 1u))) {
@@ -397,7 +398,7 @@ __global__ void __launch_bounds__(NT, 5) process_logits_kernel(LogitsParams P)
 template <auto K, int VEC>
 cudaError_t launch_chunks(LogitsParams& P, int sms, cudaStream_t st)
 {
-    // The run length with the best of: few SM slots idle in the grid's last wave, and little time per run spent on anything
+    // The run length (and groups of rows) with the best of: few SM slots idle in the grid's last wave, and little time per run spent on anything
     // but its rows (reading the history, barriers, the touched entries: measured as long as some 24 KB of rows).  At
     // (B, R, V, H) = (64, 6, 128256, 2048) runs of 2048, 4096 and 8192 entries take 67, 65 and 79 us, at (32, 65, 128256, 4000)
     // 290, 335 and 398 us, at (200, 2, 128256, 2048) 110, 83 and 85 us.
@@ -413,23 +414,32 @@ cudaError_t launch_chunks(LogitsParams& P, int sms, cudaStream_t st)
         if (f != cudaSuccess) return f;
         per_sm = max(1, min(2048 / NT, 65536 / (((a.numRegs + 7) / 8 * 8) * NT)));
     }
-    int best = NT * (VEC == 1 ? 4 : VEC);
-    double most = 0.0;
     constexpr int LEAST = NT * (VEC == 1 ? 4 : VEC);
+    int best = LEAST, groups = 1;
+    double most = 0.0;
     for (int chunk = 8192; chunk >= LEAST; chunk /= 2) {
-        const long long per = (P.V + chunk - 1) / chunk, ctas = per * P.B;
         const long long slots = (long long)sms * min(per_sm, (int)(220000 / (smem(chunk) + 6144)));
         if (slots < 1) continue;
-        const double full = (double)P.V * P.B / ((double)chunk * ((ctas + slots - 1) / slots * slots));
-        const double rows = 2.0 * chunk * P.R * (16 / (VEC == 1 ? 8 : VEC)), score = full * rows / (rows + 24576.0 + 4.0 * P.H);
-        if (score > most) {
-            most = score;
-            best = chunk;
+        const long long per = (long long)((P.V + chunk - 1) / chunk) * P.B;
+        for (int g = 1; g <= 16 && g <= P.R; ++g) {
+            // many rows are shared out where the shortest runs alone leave SMs idle ((4, 65, 128256, 4000): 83 to 48 us); elsewhere more CTAs
+            // only repeat the history
+            if (g > 1 && (chunk > LEAST || per * (g - 1) >= slots)) break;
+            const int rows = (P.R + g - 1) / g;
+            const long long ctas = per * ((P.R + rows - 1) / rows);
+            const double full = (double)P.V * P.B * P.R / ((double)chunk * rows * ((ctas + slots - 1) / slots * slots));
+            const double bytes = 2.0 * chunk * rows * (VEC == 4 ? 4 : 2), score = full * bytes / (bytes + 24576.0 + 4.0 * P.H);
+            if (score > most) {
+                most = score;
+                best = chunk;
+                groups = g;
+            }
         }
     }
+    P.rows = (P.R + groups - 1) / groups;
     P.chunk = best;
     const size_t bytes = smem(best);
-    K<<<dim3((unsigned)((P.V + best - 1) / best), (unsigned)P.B), NT, bytes, st>>>(P);
+    K<<<dim3((unsigned)((P.V + best - 1) / best), (unsigned)P.B, (unsigned)((P.R + P.rows - 1) / P.rows)), NT, bytes, st>>>(P);
     return cudaGetLastError();
 }
 

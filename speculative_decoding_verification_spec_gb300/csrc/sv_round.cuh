@@ -88,7 +88,7 @@ struct LogitsParams {
     const uint32_t* allowed;     // [B, R, mwords]
     int mwords;
     int32_t* row_status;
-    int chunk;                   // vocabulary entries per CTA
+    int chunk, rows;             // vocabulary entries and rows per CTA
 };
 
 cudaError_t launch_process_logits(LogitsParams& P, int dtype, int sms, cudaStream_t st);
