@@ -151,8 +151,10 @@ __device__ __forceinline__ void slice_step(RowState<D>& S, const uint32_t (&qf)[
 // phase of a fragment load reads lie in different banks for keys and values alike
 __device__ __forceinline__ int col_token(int n) { return n & 1 ? (n - 1) ^ 5 : n; }
 
+// Resident CTAs: with 128 channels two of 244 registers a thread run 5% faster than three of 168, which spill (104 to 110 us at
+// B = 32, T = 1, contexts to 8192, four rows a head).
 template <int DT, int D>
-__global__ void __launch_bounds__(ANT, 3) attn_rows_kernel(AttnParams P)
+__global__ void __launch_bounds__(ANT, D == 64 ? 3 : 2) attn_rows_kernel(AttnParams P)
 {
     constexpr int KB = SLICE * D;        // bytes of a slice's keys (or values)
     constexpr int STAGE = 2 * KB;
@@ -180,6 +182,9 @@ __global__ void __launch_bounds__(ANT, 3) attn_rows_kernel(AttnParams P)
     int ltok[2];  // this lane's key token of each n-tile
     ltok[0] = col_token(g);
     ltok[1] = 8 + col_token(g);
+    uint32_t piece[D / 32];  // where this lane's pieces of a slice go
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) piece[k] = swz_off(D, (lane + 32 * k) / (D / 16), (lane + 32 * k) % (D / 16));
     const bool first_cont = ((u - pre) % rq.n) != 0;
     bool first = true;
 
@@ -259,16 +264,24 @@ __global__ void __launch_bounds__(ANT, 3) attn_rows_kernel(AttnParams P)
                     const bool good = (unsigned)page < (unsigned)P.pages;
                     const size_t blk = good ? (size_t)page * P.Hkv + h : 0;
                     const int valid = good ? rq.len - base : 0;
-                    const size_t off = (blk * P.page + (good ? (base & (P.page - 1)) : 0)) * D;
+                    // the slice's tokens are contiguous, 16-byte piece by piece
+                    const size_t off = (blk * P.page + (good ? (base & (P.page - 1)) : 0)) * D + lane * 16;
                     const uint32_t st = my_a + (i % ASTAGES) * STAGE;
+                    if (valid >= SLICE) {
+                        const uint8_t *fk = P.kc + off, *fv = P.vc + off;
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        const int q = lane + 32 * k, row = q / (D / 16), ch = q % (D / 16);
-                        const int bytes = row < valid ? 16 : 0;  // tokens past the length are filled with zeros
-                        const uint32_t o = swz_off(D, row, ch);
-                        const size_t from = bytes ? off + (size_t)row * D + ch * 16 : 0;
-                        cp_async16(st + o, P.kc + from, bytes);
-                        cp_async16(st + KB + o, P.vc + from, bytes);
+                        for (int k = 0; k < D / 32; ++k) {
+                            cp_async16(st + piece[k], fk + k * 512, 16);
+                            cp_async16(st + KB + piece[k], fv + k * 512, 16);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {
+                            const int bytes = (lane + 32 * k) / (D / 16) < valid ? 16 : 0;  // tokens past the length are filled with zeros
+                            const size_t from = bytes ? off + k * 512 : 0;
+                            cp_async16(st + piece[k], P.kc + from, bytes);
+                            cp_async16(st + KB + piece[k], P.vc + from, bytes);
+                        }
                     }
                     if (lane < 2) cp_async4(sc_a + (i % ASTAGES) * 8 + lane * 4, (lane ? P.vs : P.ks) + blk, good ? 4 : 0);
                 }
