@@ -1,6 +1,9 @@
 """GB300 (sm_103a) speculative-decoding verify step: exact speculative sampling, its top-k, top-p
 and grammar-mask variants, greedy and typical-acceptance tree verify, stochastic tree verify and the verify side of an SMC-SD round, as hand-written CUDA behind a C ABI (include/spec_verify.h).
 
+Around the verify step: verify_attention over an 8-bit paged key/value cache, process_logits (penalties, biases, grammar
+masks), kv_cache_write (the commit of the accepted rows) and kv_cache_read.
+
 The binding functions load the compiled library on first use and raise if it is missing: there is
 no CPU fallback.
 """

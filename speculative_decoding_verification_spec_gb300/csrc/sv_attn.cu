@@ -21,6 +21,11 @@
 // group that one CTA covers is written out directly; otherwise its parts (m, l, o) go to the workspace and
 // attn_merge_kernel joins them in a fixed order.  Each of a CTA's four warps streams its own 16 tokens of a
 // tile through a private ring of cp.async stages, so the loop has no barrier; the warps join at the end.
+//
+// What bounds it: a slice is some 500 instructions of one dependent chain (fragments, products, reference, weights, products),
+// and the registers leave eight warps an SM to hide it; DRAM is 29% used.  104 us for 347 MB at T = 1, B = 32, contexts to
+// 8192, four rows a head (3.3 TB/s, half of a copy's rate); one context of 131071 tokens, ten rows a head, D = 64: 33 MB in
+// 44 us, the launch of the joining kernel among them.
 #include "sv_attn.cuh"
 
 namespace sv {

@@ -8,19 +8,27 @@
 //       two for bf16 (4 bits each, the residual's sign the ninth: exact for elements above 2^-10 of the largest, off by at
 //       most 2^-17 of it below) and three for halfs, whose products accumulate.
 //   O^T [D, rows] += V^T [D, 128] P^T:   halfs; six warps widen the codes of V into shared memory, and the weights are
-//       rounded to halfs (half a step, 2^-11, under the output's own rounding).
+//       rounded to halfs (half a step, 2^-11, under the output's own rounding; a weight below 2^-14 is off by 2^-25
+//       absolute, 2^-28 of the row's largest, as HEAD says).
 // The round's own rows come last, as tiles of their own: keys and values as halfs scaled by a power of two per token, and a
 // copy of q as halfs.
 //
 // One CTA per SM works through an equal run of all groups' tiles (as in sv_attn.cu), with a role per warp:
-//   0      copies: the pages' codes by TMA into a ring of stages, the pages' scales beside them
+//   0      copies: the keys' codes by TMA into a ring of stages, the pages' numbers and scales beside them; the values' codes
+//          it only calls into L2 by then
 //   1      products: one lane issues them; S is double-buffered, so S of the next tile runs under this tile's softmax
-//   2 - 7  values to halfs
+//   2 - 7  values: the next tile's codes from L2 into registers while this tile's are widened into shared memory
 //   8 - 15 softmax, two groups of four warps; a thread is a token, a group takes half of the columns.  The sums l stay in
 //          tensor memory beside S^T and O^T, one per token lane and column, so a thread holds 16 columns at a time.  The
 //          weights are taken against the reference as it stands; only when one passes 2^15 (the first tile of a group, and
 //          rarely after) does the group find the columns' maxima, move the reference, rescale its part of O^T and l and
 //          repeat the tile.
+// What bounds it: neither memory nor the tensor cores, but the chain that each tile goes through (S^T, softmax, P, O^T): some
+// 2000 to 2800 cycles up to 48 rows and 3600 at 87, of which a product takes about 100 whatever its columns, and some 10000
+// more where a CTA changes the group (q, the first reference, the outputs).  The issue slots are 43% used, DRAM 24%.  Contexts
+// to 8192, B = 32, T = 6, four query heads a head: 139 us for 347 MB (2.5 TB/s); to 4096, T = 65 (three row tiles of 87): 459 us
+// for 89 GFLOP (194 TFLOP/s).  A third softmax group (spills), S^T fetched a chunk ahead, and both terms of q stacked into one
+// product of twice the columns were slower: 202, 142 and 147 us where this took 139.
 // Every wait on an mbarrier is bounded; when one runs out the CTA's remaining groups report SPEC_ROW_TIMEOUT.  Between named
 // barriers the threads of a softmax group never part: what a wait returned is agreed on before anyone acts on it.
 #include <cuda.h>
@@ -165,9 +173,8 @@ struct Shared {
     Place place;
 };
 
-// Bounded wait; ends early once another role has given up.  Out of line, as are a group's bookkeeping and the first pass over
-// a round's own rows: with everything inline the roles' loops together outgrow the instruction cache, and every step waits
-// for its code.
+// Bounded wait; ends early once another role has given up.  Out of line, as the path that is seldom taken; the rest is inline,
+// since what a call takes by reference lives in local memory, and beside this much shared memory hardly any L1 is left for it.
 __device__ __noinline__ bool wait_on(Shared& sh, uint64_t* bar, uint32_t parity, int limit)
 {
     const uint32_t a = smem_addr(bar);
@@ -671,8 +678,7 @@ __device__ __forceinline__ void token_terms(const Shared& sh, const Lane& L, int
 
 // The softmax over tiles that have a reference: tiles of the cache in a row, or (own) one of the round's rows.  One pass per
 // tile; the run ends where a weight passes the window (for any thread of the group) or a wait runs out.  `take`: chunks whose
-// sums the first tile adds to l.  A function of its own, as compact as it can be: it is nearly all of the kernel's time, and
-// what does not fit the instruction cache waits for its code at every step.
+// sums the first tile adds to l.  Nearly all of the kernel's time goes through this loop.
 __device__ __forceinline__ RunEnd softmax_run(const TcParams& T, Shared& sh, const Lane L, const float4* fr, int it, int s_at, int tile, int end, int len,
                                            bool own, uint64_t see_own, uint32_t take)
 {

@@ -6,10 +6,14 @@
 // A <= 448 * 2^e; a block that already holds tokens of the request (its length ends inside the page)
 // keeps the larger of that and its old scale, and its earlier codes move to the new one.  A block begun by the
 // call ignores whatever scale the page had.  One CTA per block: the rows are read once, into registers,
-// reduced to A, scaled (exactly) and rounded.  Bound by HBM for prompts, by the launch and a chain of four dependent
-// loads (length, page, rows, scale) for a round's few rows.
+// reduced to A, scaled (exactly) and rounded.  For a prompt two thirds of the time are the memory's: 200 MB (four of up to 8191
+// bf16 tokens, eight heads of 128 channels) in 43 us, 4.6 TB/s, with 78% of the issue slots used, so the magnitudes are folded
+// as pairs of 16-bit integers and the codes come two to a conversion.  A round's few rows are bound by the launch and a chain
+// of four dependent loads (length, page, rows, scale).
 //
-// Read.  One 16-byte vector of codes per thread and step, scaled and rounded once to the type asked for.
+// Read.  One 16-byte vector of codes per thread and step, scaled and rounded once to the type asked for.  Bound by the writes:
+// 805 MB of bf16 from 255 MB of codes in 213 us, and a fill of the output alone takes 203 (3.96 TB/s, where a copy of as many
+// bytes in all moves 6.7).
 #include <cuda_bf16.h>
 
 #include <algorithm>
