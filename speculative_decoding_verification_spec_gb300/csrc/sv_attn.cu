@@ -23,9 +23,10 @@
 // tile through a private ring of cp.async stages, so the loop has no barrier; the warps join at the end.
 //
 // What bounds it: a slice is some 500 instructions of one dependent chain (fragments, products, reference, weights, products),
-// and the registers leave eight warps an SM to hide it; DRAM is 29% used.  104 us for 347 MB at T = 1, B = 32, contexts to
-// 8192, four rows a head (3.3 TB/s, half of a copy's rate); one context of 131071 tokens, ten rows a head, D = 64: 33 MB in
-// 44 us, the launch of the joining kernel among them.
+// and the registers leave eight warps an SM to hide it; DRAM is 30% used.  At B = 32, contexts to 8192, four rows a head: 91 us
+// for 343 MB at T = 1 (3.8 TB/s, over half of a copy's rate), 101 us at T = 4.  A group's start and its own rows cost latency
+// alone: with the first slices called before q is read, and the rows of q and of the round loaded together, 91 and 101 us are
+// what had been 104 and 122.
 #include "sv_attn.cuh"
 
 namespace sv {
@@ -156,7 +157,7 @@ __device__ __forceinline__ void slice_step(RowState<D>& S, const uint32_t (&qf)[
 // phase of a fragment load reads lie in different banks for keys and values alike
 __device__ __forceinline__ int col_token(int n) { return n & 1 ? (n - 1) ^ 5 : n; }
 
-// Resident CTAs: with 128 channels two of 244 registers a thread run 5% faster than three of 168, which spill (104 to 110 us at
+// Resident CTAs: with 128 channels two of 242 registers a thread run 5% faster than three of 168, which spill (104 to 110 us at
 // B = 32, T = 1, contexts to 8192, four rows a head).
 template <int DT, int D>
 __global__ void __launch_bounds__(ANT, D == 64 ? 3 : 2) attn_rows_kernel(AttnParams P)
@@ -200,61 +201,11 @@ __global__ void __launch_bounds__(ANT, D == 64 ? 3 : 2) attn_rows_kernel(AttnPar
         const int tile1 = (int)min((long long)rq.n, tile0 + (u1 - u));
         const bool whole = tile0 == 0 && tile1 == rq.n;
 
-        // ---- the rows of q
+        // ---- the first slices of the cache, which arrive while q is looked at
         __syncthreads();  // the previous group's use of the shared arrays is over
-        if (tid == 0) sstatus = rq.status;
-        for (int i = w; i < MR; i += AW) {
-            const int r = rt * MR + i, t = r / P.G;
-            float x[D / 32], amax = 0.0f;
-            const bool live = r < P.R && t < rq.rows;
-            const int64_t base = live ? (int64_t)b * P.qb + (int64_t)t * P.qt + (int64_t)(h * P.G + r % P.G) * P.qh : 0;
-            bool fin = true;
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-                x[k] = live ? load_elem<DT>(P.q, base + lane + 32 * k) : 0.0f;
-                fin = fin && fabsf(x[k]) < __int_as_float(0x7f800000);
-                amax = fmaxf(amax, fabsf(x[k]));
-            }
-            fin = __all_sync(0xffffffffu, fin);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const int e = fin ? min(max(14 - exponent_of(amax), -113), 126) : 0;
-            const float mul = exp2_int(e);
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) sq[i][lane + 32 * k] = __float2half_rn(x[k] * mul);
-            // a row of q with a NaN or an infinity has no scores
-            if (lane == 0) sf[i] = fin ? P.scale * LOG2E * exp2_int(-e) : __int_as_float(0x7fc00000);
-        }
-        __syncthreads();
-        uint32_t qf[MT][D / 16][4];
-        float F[MT][2];
-        RowState<D> S;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int hi = 0; hi < 2; ++hi) {
-                F[mt][hi] = sf[mt * 16 + 8 * hi + g];
-                S.m[mt][hi] = NEG_INF;
-                S.l[mt][hi] = 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) S.o[mt][i][k] = 0.0f;
-            // product step cc * 4 + k takes channels 16 (t4 + 4 cc) + 4 k .. + 3 of this lane's rows
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-                for (int hi = 0; hi < 2; ++hi) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(&sq[mt * 16 + 8 * hi + g][16 * (t4 + 4 * (c >> 2)) + 4 * (c & 3)]);
-                    qf[mt][c][hi] = v.x;
-                    qf[mt][c][2 + hi] = v.y;
-                }
-        }
-
-        // ---- the cache
         const int c0 = min(tile0, rq.ncache), c1 = min(tile1, rq.ncache), nc = c1 - c0;
         const int32_t* table = P.page_table + (size_t)b * P.table_width;
+        bool bad_page = false;
         int page_reg = 0;  // lane k holds the page of the slice c0 + 32 i + k
         auto fetch = [&](int i) {
             if (i < nc) {
@@ -262,7 +213,7 @@ __global__ void __launch_bounds__(ANT, D == 64 ? 3 : 2) attn_rows_kernel(AttnPar
                 if ((i & 31) == 0) {
                     const long long tk = (long long)(c0 + i + lane) * TILE + w * SLICE;
                     page_reg = tk < rq.len ? __ldg(table + (tk >> P.page_shift)) : 0;
-                    if (tk < rq.len && c0 + i + lane < c1 && (unsigned)page_reg >= (unsigned)P.pages) sstatus = ROW_BAD_PAGE;
+                    if (tk < rq.len && c0 + i + lane < c1 && (unsigned)page_reg >= (unsigned)P.pages) bad_page = true;
                 }
                 const int page = __shfl_sync(0xffffffffu, page_reg, i & 31);
                 if (base < rq.len) {
@@ -295,6 +246,65 @@ __global__ void __launch_bounds__(ANT, D == 64 ? 3 : 2) attn_rows_kernel(AttnPar
         };
 #pragma unroll
         for (int i = 0; i < ASTAGES - 1; ++i) fetch(i);
+
+        // ---- the rows of q: those of a warp are all on their way before the first is needed
+        if (tid == 0) sstatus = rq.status;
+        float x[MR / AW][D / 32];
+#pragma unroll
+        for (int j = 0; j < MR / AW; ++j) {
+            const int r = rt * MR + w + j * AW, t = r / P.G;
+            const bool live = r < P.R && t < rq.rows;
+            const int64_t base = live ? (int64_t)b * P.qb + (int64_t)t * P.qt + (int64_t)(h * P.G + r % P.G) * P.qh : 0;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) x[j][k] = live ? load_elem<DT>(P.q, base + lane + 32 * k) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < MR / AW; ++j) {
+            const int i = w + j * AW;
+            float amax = 0.0f;
+            bool fin = true;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                fin = fin && fabsf(x[j][k]) < __int_as_float(0x7f800000);
+                amax = fmaxf(amax, fabsf(x[j][k]));
+            }
+            fin = __all_sync(0xffffffffu, fin);
+            amax = redux_max(amax);
+            const int e = fin ? min(max(14 - exponent_of(amax), -113), 126) : 0;
+            const float mul = exp2_int(e);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) sq[i][lane + 32 * k] = __float2half_rn(x[j][k] * mul);
+            // a row of q with a NaN or an infinity has no scores
+            if (lane == 0) sf[i] = fin ? P.scale * LOG2E * exp2_int(-e) : __int_as_float(0x7fc00000);
+        }
+        __syncthreads();
+        uint32_t qf[MT][D / 16][4];
+        float F[MT][2];
+        RowState<D> S;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                F[mt][hi] = sf[mt * 16 + 8 * hi + g];
+                S.m[mt][hi] = NEG_INF;
+                S.l[mt][hi] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) S.o[mt][i][k] = 0.0f;
+            // product step cc * 4 + k takes channels 16 (t4 + 4 cc) + 4 k .. + 3 of this lane's rows
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+                for (int hi = 0; hi < 2; ++hi) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(&sq[mt * 16 + 8 * hi + g][16 * (t4 + 4 * (c >> 2)) + 4 * (c & 3)]);
+                    qf[mt][c][hi] = v.x;
+                    qf[mt][c][2 + hi] = v.y;
+                }
+        }
+
+        // ---- the cache
         for (int i = 0; i < nc; ++i) {
             asm volatile("cp.async.wait_group %0;" :: "n"(ASTAGES - 2) : "memory");
             __syncwarp();  // every lane's copies of stage i have landed, and stage i - 1 is read to the end
@@ -351,6 +361,7 @@ __global__ void __launch_bounds__(ANT, D == 64 ? 3 : 2) attn_rows_kernel(AttnPar
                 });
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        if (bad_page) sstatus = ROW_BAD_PAGE;
 
         // ---- the round's own rows
         for (int tile = max(tile0, rq.ncache); P.kn && tile < tile1; ++tile) {
@@ -389,36 +400,53 @@ __global__ void __launch_bounds__(ANT, D == 64 ? 3 : 2) attn_rows_kernel(AttnPar
             __half* fk = reinterpret_cast<__half*>(my);
             __half* fv = fk + SLICE * D;
             unsigned bad = 0;  // rows of the slice whose values hold a NaN or an infinity
-            for (int i = 0; i < SLICE; ++i) {
-                const int j = jw + i;
-                const bool live = j < rq.rows;
+            constexpr int FU = 4;  // rows in flight
+            const int live = min(rq.rows - jw, SLICE);
+            for (int i = lane; i < 2 * (SLICE - live) * D / 8; i += 32) {
+                const int n = (SLICE - live) * D / 8;
+                reinterpret_cast<uint4*>((i < n ? fk : fv) + live * D)[i < n ? i : i - n] = make_uint4(0, 0, 0, 0);
+            }
+            if (lane >= live && lane < SLICE) fks[w][lane] = 1.0f, fve[w][lane] = 0.0f;
+#pragma unroll 1
+            for (int i0 = 0; i0 < live; i0 += FU) {
+                float x[FU][2][D / 32];
 #pragma unroll
-                for (int which = 0; which < 2; ++which) {
-                    const void* src = which ? P.vn : P.kn;
-                    const int64_t base = !live ? 0 : which ? b * P.vb + j * P.vt + h * P.vh : b * P.kb + j * P.kt + h * P.kh;
-                    float x[D / 32], amax = 0.0f;
-                    bool fin = true;
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        x[k] = live ? load_elem<DT>(src, base + lane + 32 * k) : 0.0f;
-                        if (fabsf(x[k]) < __int_as_float(0x7f800000)) amax = fmaxf(amax, fabsf(x[k]));
-                        else fin = false;
-                    }
-                    fin = __all_sync(0xffffffffu, fin);
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                    const int e = min(max(exponent_of(amax), CACHE_E_MIN), 126) - 14;
-                    const float mul = exp2_int(-e);
-                    if (which && !fin) bad |= 1u << i;
+                for (int f = 0; f < FU; ++f) {
+                    const int64_t j = jw + i0 + f;
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k) {
-                        // a value that only some rows see must not meet the others' zero weights as NaN
-                        const bool drop = which && !(fabsf(x[k]) < __int_as_float(0x7f800000));
-                        (which ? fv : fk)[i * D + lane + 32 * k] = __float2half_rn(drop ? 0.0f : x[k] * mul);
+                        x[f][0][k] = i0 + f < live ? load_elem<DT>(P.kn, b * P.kb + j * P.kt + h * P.kh + lane + 32 * k) : 0.0f;
+                        x[f][1][k] = i0 + f < live ? load_elem<DT>(P.vn, b * P.vb + j * P.vt + h * P.vh + lane + 32 * k) : 0.0f;
                     }
-                    if (lane == 0) {
-                        if (which) fve[w][i] = (float)e;
-                        else fks[w][i] = fin ? exp2_int(e) : __int_as_float(0x7fc00000);  // a key that is not finite: NaN
+                }
+#pragma unroll
+                for (int f = 0; f < FU; ++f) {
+                    const int i = i0 + f;
+                    if (i >= live) break;
+#pragma unroll
+                    for (int which = 0; which < 2; ++which) {
+                        float amax = 0.0f;
+                        bool fin = true;
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {
+                            if (fabsf(x[f][which][k]) < __int_as_float(0x7f800000)) amax = fmaxf(amax, fabsf(x[f][which][k]));
+                            else fin = false;
+                        }
+                        fin = __all_sync(0xffffffffu, fin);
+                        amax = redux_max(amax);
+                        const int e = min(max(exponent_of(amax), CACHE_E_MIN), 126) - 14;
+                        const float mul = exp2_int(-e);
+                        if (which && !fin) bad |= 1u << i;
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {
+                            // a value that only some rows see must not meet the others' zero weights as NaN
+                            const bool drop = which && !(fabsf(x[f][which][k]) < __int_as_float(0x7f800000));
+                            (which ? fv : fk)[i * D + lane + 32 * k] = __float2half_rn(drop ? 0.0f : x[f][which][k] * mul);
+                        }
+                        if (lane == 0) {
+                            if (which) fve[w][i] = (float)e;
+                            else fks[w][i] = fin ? exp2_int(e) : __int_as_float(0x7fc00000);  // a key that is not finite: NaN
+                        }
                     }
                 }
             }

@@ -38,6 +38,13 @@ __device__ __forceinline__ float load_elem(const void* p, int64_t i)
         return __half2float(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(p) + i)));
 }
 
+__device__ __forceinline__ float redux_max(float x)
+{
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // the exponent x of a finite a >= 0, a = f * 2^x with f in [1, 2), -127 below the normal range
 __device__ __forceinline__ int exponent_of(float a) { return (int)(__float_as_uint(a) >> 23) - 127; }
 

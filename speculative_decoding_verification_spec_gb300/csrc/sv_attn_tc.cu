@@ -425,13 +425,6 @@ __device__ void role_mma(const TcParams& T, Shared& sh, const Place& at, uint32_
     (void)mbar_wait(&sh.done, 0, MBAR_SPIN_LIMIT);
 }
 
-__device__ __forceinline__ float warp_max(float x)
-{
-    float r;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // byte offset of channel d of a row of q in a term's tile (swizzled over 128 or 64 bytes, a row)
 template <int D>
 __device__ __forceinline__ uint32_t q_off(int col, int d)
@@ -554,7 +547,7 @@ __device__ __forceinline__ bool own_rows(const TcParams& T, Shared& sh, uint8_t*
                 else fin = false, x[which][k] = 0.0f;
             }
             fin = __all_sync(0xffffffffu, fin);
-            amax = warp_max(amax);
+            amax = redux_max(amax);
             const int e = min(max(exponent_of(amax), CACHE_E_MIN), 126) - 14;
             const float mul = exp2_int(-e);
             uint8_t* to = (which ? vb : kb) + half_off(i, lane * EPL);
@@ -801,7 +794,7 @@ __device__ __forceinline__ bool move_reference(const TcParams& T, Shared& sh, co
             for (int j = 0; j < 4; ++j) {
                 const float F = reinterpret_cast<const float*>(&fr[(c + j) >> 1])[j & 1];
                 const float x = see >> (c + j) & 1ull ? fmaf(__uint_as_float(s[j]) * F, ks, ve) : NEG_INF;
-                const float m = warp_max(x);
+                const float m = redux_max(x);
                 if (L.lane == 0) sh.wred[L.g][L.quad][c + j] = m;
             }
         }
