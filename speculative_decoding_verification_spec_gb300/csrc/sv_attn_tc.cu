@@ -115,15 +115,10 @@ __device__ __forceinline__ void tmem_ld16_nowait(uint32_t addr, uint32_t (&r)[16
                    "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                  : "r"(addr));
 }
-// 4 columns
-__device__ __forceinline__ void tmem_ld4(uint32_t addr, uint32_t (&r)[4])
+// one column
+__device__ __forceinline__ void tmem_ld1(uint32_t addr, uint32_t& r)
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4]; tcgen05.wait::ld.sync.aligned;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void tmem_st4(uint32_t addr, const uint32_t (&r)[4])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1]; tcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -787,16 +782,19 @@ __device__ __forceinline__ bool move_reference(const TcParams& T, Shared& sh, co
         uint64_t see;
         token_terms(sh, L, it, s_at, T.A.page_shift, left, own, see_own, ks, ve, see);
 #pragma unroll 1
-        for (int c = 0; c < cw; c += 4) {
-            uint32_t s[4];
-            tmem_ld4(t_s + c, s);
+        for (int c = 0; c < cw; c += 16) {
+            uint32_t s[16];
+            tmem_ld16_nowait(t_s + c, s);
+            tmem_wait_ld();
+            float mine = NEG_INF;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 16; ++j) {
                 const float F = reinterpret_cast<const float*>(&fr[(c + j) >> 1])[j & 1];
                 const float x = see >> (c + j) & 1ull ? fmaf(__uint_as_float(s[j]) * F, ks, ve) : NEG_INF;
                 const float m = redux_max(x);
-                if (L.lane == 0) sh.wred[L.g][L.quad][c + j] = m;
+                if (L.lane == j) mine = m;
             }
+            if (L.lane < 16) sh.wred[L.g][L.quad][c + L.lane] = mine;
         }
     }
     if (group_any(L.bar_id, !ok)) return false;
@@ -818,16 +816,17 @@ __device__ __forceinline__ bool move_reference(const TcParams& T, Shared& sh, co
     group_sync(L.bar_id);
     // a group's first tile: l starts from zero, and O^T's first product overwrites it
 #pragma unroll 1
-    for (int c = first ? cw : 0; c < 2 * cw; c += 4) {
+    for (int c = first ? cw : 0; c < 2 * cw; c += 16) {
         const uint32_t a = c < cw ? t_o + c : t_l + c - cw;
         const float4* f = &sh.col[L.g][c < cw ? c : c - cw];
-        uint32_t o[4] = {0u, 0u, 0u, 0u};
+        uint32_t o[16];
         if (!first) {
-            tmem_ld4(a, o);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[j].x);
+            tmem_ld16_nowait(a, o);
+            tmem_wait_ld();
         }
-        tmem_st4(a, o);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j] = first ? 0u : __float_as_uint(__uint_as_float(o[j]) * f[j].x);
+        tmem_st16_nowait(a, o);
     }
     tmem_wait_st();
     return true;
@@ -840,11 +839,11 @@ __device__ __forceinline__ void load_q(const TcParams& T, Shared& sh, const Lane
     const AttnParams& P = T.A;
     constexpr int TERMS = DT == DT_BF16 ? 2 : 3, LPR = D / 16, RPW = 32 / LPR;  // lanes of a row, rows of a warp
     const int cw = L.nch * 16, d = (L.lane % LPR) * 16;
-#pragma unroll 1
-    for (int c = L.quad * RPW + L.lane / LPR; c < cw; c += 4 * RPW) {
+    const auto load = [&](int c, uint32_t (&u)[8]) {
         const int col = L.col0 + c, r = rt * T.MR + col, t = row_token(T, r);
-        uint32_t u[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-        if (col < T.MR && r < P.R && t < rows) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] = 0u;
+        if (c < cw && col < T.MR && r < P.R && t < rows) {
             const uint16_t* q = reinterpret_cast<const uint16_t*>(P.q) + (int64_t)b * P.qb + (int64_t)t * P.qt + (int64_t)(h * P.G + r - t * P.G) * P.qh + d;
             if (T.qvec) {
                 const uint4 v = __ldg(reinterpret_cast<const uint4*>(q)), z = __ldg(reinterpret_cast<const uint4*>(q) + 1);
@@ -855,6 +854,17 @@ __device__ __forceinline__ void load_q(const TcParams& T, Shared& sh, const Lane
                 for (int k = 0; k < 8; ++k) u[k] = (uint32_t)__ldg(q + 2 * k) | (uint32_t)__ldg(q + 2 * k + 1) << 16;
             }
         }
+    };
+    // the next rows are on their way while these are split
+    const int c0 = L.quad * RPW + L.lane / LPR;
+    uint32_t u[8], next[8];
+    load(c0, next);
+#pragma unroll 1
+    for (int c = c0; c < cw; c += 4 * RPW) {
+        const int col = L.col0 + c;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] = next[k];
+        load(c + 4 * RPW, next);
         float x[16], amax = 0.0f;
         bool fin = true;
 #pragma unroll
@@ -916,9 +926,32 @@ __device__ __forceinline__ bool own_tile(const TcParams& T, Shared& sh, const La
     constexpr int TERMS = DT == DT_BF16 ? 2 : 3;
     const int cw = L.nch * 16;
     uint8_t* pb = L.smem + T.o_p + (T.np == 2 ? it & 1 : 0) * T.p_buf;
+    bool badp = false;
+    if (j0 > 0) group_sync(L.bar_id);  // the masks of the tile before have been read (another group's before its outputs)
+    if (L.tok < cw) {
+        // a thread per column: the rows on its row's path, as bits of the tile's 128 tokens
+        const int t = row_token(T, rt * T.MR + L.col0 + L.tok);
+        uint32_t* m = sh.mask[L.col0 + L.tok];
+        m[0] = m[1] = m[2] = m[3] = 0u;
+        if (P.kn && t < rows) {
+#pragma unroll 1
+            for (int cur = t;;) {
+                if ((unsigned)(cur - j0) < (unsigned)TT) m[(cur - j0) >> 5] |= 1u << ((cur - j0) & 31);
+                if (cur == 0) break;
+                const int p = P.parents ? __ldg(P.parents + (size_t)b * (P.T - 1) + cur - 1) : cur - 2;
+                if (p < -1 || p >= cur - 1) break;  // reported below; the walk always ends
+                cur = p + 1;
+            }
+        }
+    }
+    if (P.parents)
+#pragma unroll 1
+        for (int i = L.tok; i < rows - 1; i += 128) {
+            const int p = __ldg(P.parents + (size_t)b * (P.T - 1) + i);
+            badp = badp || p < -1 || p >= i;
+        }
     // (the kernel's first tile asks for a phase before the first, which counts as over)
     const bool ok = wait_warp(sh, &sh.pv[(it + 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit);
-    bool badp = false;
     if (ok) {
 #pragma unroll 1
         for (int i = L.tok; i < cw * (D / 8); i += 128) {
@@ -938,28 +971,6 @@ __device__ __forceinline__ bool own_tile(const TcParams& T, Shared& sh, const La
             *reinterpret_cast<uint4*>(pb + (size_t)(d >> 6) * T.RN * 128 + col * 128 + ((((d & 63) >> 3) ^ (col & 7)) << 4)) =
                 *reinterpret_cast<const uint4*>(x);
         }
-        if (L.tok < cw) {
-            // a thread per column: the rows on its row's path, as bits of the tile's 128 tokens
-            const int t = row_token(T, rt * T.MR + L.col0 + L.tok);
-            uint32_t* m = sh.mask[L.col0 + L.tok];
-            m[0] = m[1] = m[2] = m[3] = 0u;
-            if (P.kn && t < rows) {
-#pragma unroll 1
-                for (int cur = t;;) {
-                    if ((unsigned)(cur - j0) < (unsigned)TT) m[(cur - j0) >> 5] |= 1u << ((cur - j0) & 31);
-                    if (cur == 0) break;
-                    const int p = P.parents ? __ldg(P.parents + (size_t)b * (P.T - 1) + cur - 1) : cur - 2;
-                    if (p < -1 || p >= cur - 1) break;  // reported below; the walk always ends
-                    cur = p + 1;
-                }
-            }
-        }
-        if (P.parents)
-#pragma unroll 1
-            for (int i = L.tok; i < rows - 1; i += 128) {
-                const int p = __ldg(P.parents + (size_t)b * (P.T - 1) + i);
-                badp = badp || p < -1 || p >= i;
-            }
         fence_proxy_async_smem();
     }
     *bad = group_any(L.bar_id, badp);
@@ -1028,6 +1039,29 @@ __device__ __forceinline__ void put_outputs(const TcParams& T, Shared& sh, const
     }
     group_sync(L.bar_id);
     uint16_t* out = reinterpret_cast<uint16_t*>(P.out) + (size_t)b * P.T * P.Hq * D + L.tok;
+    const auto put = [&](int c, float x) {
+        const float2 q = *reinterpret_cast<const float2*>(&sh.col[L.g][c]);
+        // a dead row's sums are zeros that no token touched; with a status they become NaN
+        const float y = q.x == 0.0f ? 0.0f : x * q.x;
+        if (__float_as_int(q.y) >= 0)
+            out[(size_t)__float_as_int(q.y) * D] = DT == DT_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : __half_as_ushort(__float2half_rn(y));
+    };
+    const auto put_part = [&](int c, float x) {
+        if (__float_as_int(sh.col[L.g][c].y) >= 0) part[(size_t)(L.col0 + c) * D + L.tok] = x;
+    };
+    if (vbad && !dead) {
+#pragma unroll 1
+        for (int c = 0; c < cw; ++c) {
+            uint32_t o;
+            tmem_ld1(t_o + c, o);
+            if (L.tok >= D) continue;
+            const float4 q = sh.col[L.g][c];
+            float x = __uint_as_float(o);
+            if (__float_as_int(q.y) >= 0 && __float_as_int(q.z) < rows) x += unfinite_values<DT>(P, b, h, __float_as_int(q.z), L.tok);
+            if (whole) put(c, x);
+            else put_part(c, x);
+        }
+    } else
 #pragma unroll 1
     for (int c = 0; c < cw; c += 16) {
         uint32_t o[16];
@@ -1035,19 +1069,14 @@ __device__ __forceinline__ void put_outputs(const TcParams& T, Shared& sh, const
         tmem_wait_ld();
         if (L.tok >= D) continue;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float4 q = sh.col[L.g][c + j];
-            const int row = __float_as_int(q.y);
-            if (row < 0) continue;
-            float x = dead ? 0.0f : __uint_as_float(o[j]);
-            if (vbad && __float_as_int(q.z) < rows) x += unfinite_values<DT>(P, b, h, __float_as_int(q.z), L.tok);
-            if (whole) {
-                // a dead row's sums are zeros that no token touched; with a status they become NaN
-                const float y = q.x == 0.0f ? 0.0f : x * q.x;
-                out[(size_t)row * D] = DT == DT_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : __half_as_ushort(__float2half_rn(y));
-            } else {
-                part[(size_t)(L.col0 + c + j) * D + L.tok] = x;
-            }
+        for (int j = 0; j < 16; ++j)
+            if (dead) o[j] = 0u;
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) put(c + j, __uint_as_float(o[j]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) put_part(c + j, __uint_as_float(o[j]));
         }
     }
     tc_fence_before();
