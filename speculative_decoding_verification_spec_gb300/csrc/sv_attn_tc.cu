@@ -589,6 +589,9 @@ __device__ void role_values(const TcParams& T, Shared& sh, const Place& at, uint
             if (tile + 1 < w.tile1) fetch(tile + 1);
             // the buffer's last use (the first ones ask for a phase before the first, which counts as over)
             ok = ok && wait_warp(sh, &sh.pv[(it + T.nv) & 1], ((it - T.nv) >> 1) & 1, T.wait_limit);
+            // the keys of a round's rows have one buffer: S^T of the tile before has to be done with it.  (S^T two tiles on, whose
+            // commit ends the next phase, follows the O^T that waits for this tile's values.)
+            if (own) ok = ok && wait_warp(sh, &sh.sfull[(it + 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit);
             if (!ok) break;
             if (own) {
                 const bool vbad = own_rows<DT, D>(T, sh, smem + T.o_kh, vb, it, w.b, w.h, (tile - w.rq.ncache) * TT, w.rq.rows);

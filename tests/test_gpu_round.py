@@ -301,6 +301,18 @@ def test_attention_tree(T, hq, hkv, D):
     check_attention(p, q, kn, vn, parents)
 
 
+@pytest.mark.parametrize("T,hq,hkv,D", [(130, 2, 1, 64), (140, 1, 1, 128), (256, 1, 1, 64)])
+def test_attention_many_rows_tiles_follow_each_other(T, hq, hkv, D):
+    # so many requests that one CTA takes all tiles of a request's own rows, and the next request's after them
+    g = torch.Generator().manual_seed(T)
+    lens = [0, 0, 0, 40] * 30
+    p = Pool(g, lens, hkv, 32, D)
+    q, kn, vn = round_inputs(g, len(lens), T, hq, hkv, D, "bf16")
+    parents = torch.stack([R.random_parents(g, T - 1) for _ in lens])
+    check_attention(p, q, kn, vn, parents)
+    check_attention(p, q, kn, vn)
+
+
 @pytest.mark.parametrize("T,hq,hkv", [(1, 1, 1), (1, 32, 8), (4, 32, 4), (9, 16, 2)])
 def test_attention_long_context(T, hq, hkv):
     """Long and ragged contexts: parts of many CTAs are joined."""
