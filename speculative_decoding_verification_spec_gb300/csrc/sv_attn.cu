@@ -191,12 +191,18 @@ __global__ void __launch_bounds__(ANT, D == 64 ? 3 : 2) attn_rows_kernel(AttnPar
     uint32_t piece[D / 32];  // where this lane's pieces of a slice go
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) piece[k] = swz_off(D, (lane + 32 * k) / (D / 16), (lane + 32 * k) % (D / 16));
-    const bool first_cont = ((u - pre) % rq.n) != 0;
-    bool first = true;
 
     while (u < u1) {
+        while (u >= pre + (long long)rq.span * P.Hkv * P.RT) {
+            pre += (long long)rq.span * P.Hkv * P.RT;
+            rq = req_info<TILE>(P, ++b);
+        }
         const long long rem = u - pre;
-        const int grp = (int)(rem / rq.n), tile0 = (int)(rem % rq.n);
+        const int grp = (int)(rem / rq.span), tile0 = (int)(rem % rq.span);
+        if (tile0 >= rq.n) {
+            u += rq.span - tile0;
+            continue;
+        }
         const int h = grp / P.RT, rt = grp % P.RT;
         const int tile1 = (int)min((long long)rq.n, tile0 + (u1 - u));
         const bool whole = tile0 == 0 && tile1 == rq.n;
@@ -521,7 +527,7 @@ __global__ void __launch_bounds__(ANT, D == 64 ? 3 : 2) attn_rows_kernel(AttnPar
             }
         __syncthreads();
         const int status = sstatus;
-        float* part = P.parts + ((size_t)blockIdx.x * 2 + (first && first_cont ? 0 : 1)) * part_floats(MR, D);
+        float* part = P.parts + ((size_t)blockIdx.x * 2 + (tile0 != 0 ? 0 : 1)) * part_floats(MR, D);
         for (int i = tid; i < MR * (D / 4); i += ANT) {
             const int row = i / (D / 4), d = i % (D / 4) * 4;
             const int r = rt * MR + row;
@@ -561,12 +567,7 @@ __global__ void __launch_bounds__(ANT, D == 64 ? 3 : 2) attn_rows_kernel(AttnPar
                 if (tile0 == 0) P.joins[blockIdx.x] = {parts_of(at.total, blockIdx.x, at.ctas, u + rq.n), b, h, rt, rq.rows};
             }
         }
-        first = false;
         u += tile1 - tile0;
-        while (u < u1 && u >= pre + (long long)rq.n * P.Hkv * P.RT) {
-            pre += (long long)rq.n * P.Hkv * P.RT;
-            rq = req_info<TILE>(P, ++b);
-        }
     }
 }
 

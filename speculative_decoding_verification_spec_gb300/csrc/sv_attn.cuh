@@ -50,11 +50,20 @@ __device__ __forceinline__ int exponent_of(float a) { return (int)(__float_as_ui
 
 // ---------------------------------------------------------------- schedule
 
+// The units that a group takes beside its tiles, at its end: what its own rows, its q, its first reference and its outputs cost
+// beside a tile, so that a CTA that ends one group and begins the next gets fewer tiles.  A run that starts in them begins
+// with the next group.  In tiles of 128 tokens on the many-rows path (B = 32: 65 rows a round 402, 376 and 376 us with 3, 6 and
+// 10 units; 48 rows a head 176, 171 and 175 us; none: 447 and 183), of 64 on the few-rows path (T = 4: 101, 97, 95 and 95 us with
+// none, 6, 8 and 10).
+template <int TILE>
+constexpr int REST = TILE == 128 ? 6 : 8;
+
 struct ReqInfo {
     int len;     // committed tokens (0 when the length is bad)
     int rows;    // live rows
     int ncache;  // tiles of the cache
     int n;       // tiles of a group, at least one: a group without tokens still writes its outputs
+    int span;    // its units
     int status;
 };
 
@@ -72,14 +81,15 @@ __device__ __forceinline__ ReqInfo req_info(const AttnParams& P, int b)
     q.ncache = (q.len + TILE - 1) / TILE;
     const int fresh = P.kn ? (q.rows + TILE - 1) / TILE : 0;
     q.n = max(1, q.ncache + fresh);
+    q.span = q.n + REST<TILE>;
     return q;
 }
 
-// total units (tiles of all groups), and the request that unit `u0(total)` falls into; every thread of the CTA calls
+// total units of all groups, and the request that unit `u0(total)` falls into; every thread of the CTA calls
 // it, warp 0 works
 struct Place {
     long long total, pre;  // pre: units of the requests before b
-    int b, ctas;           // CTAs that work: no more than there are units, so none of them is empty
+    int b, ctas;           // CTAs that work: no more than there are units
 };
 
 template <int TILE>
@@ -90,7 +100,7 @@ __device__ Place find_place(const AttnParams& P, int cta, int ctas, Place* sh)
         const long long per = (long long)P.Hkv * P.RT;
         long long total = 0;
         for (int b0 = 0; b0 < P.B; b0 += 32) {
-            long long v = b0 + lane < P.B ? req_info<TILE>(P, b0 + lane).n * per : 0;
+            long long v = b0 + lane < P.B ? req_info<TILE>(P, b0 + lane).span * per : 0;
 #pragma unroll
             for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
             total += v;
@@ -100,7 +110,7 @@ __device__ Place find_place(const AttnParams& P, int cta, int ctas, Place* sh)
         long long pre = 0;
         int found = P.B;
         for (int b0 = 0; b0 < P.B; b0 += 32) {
-            long long v = b0 + lane < P.B ? req_info<TILE>(P, b0 + lane).n * per : 0, s = v;
+            long long v = b0 + lane < P.B ? req_info<TILE>(P, b0 + lane).span * per : 0, s = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long x = __shfl_up_sync(0xffffffffu, s, o);

@@ -208,7 +208,7 @@ struct Walk {
     ReqInfo rq;
     // the current group
     int h, rt, tile0, tile1;
-    bool whole, first;
+    bool whole;
 
     __device__ __forceinline__ Walk(const AttnParams& P, const Place& at)
     {
@@ -218,28 +218,30 @@ struct Walk {
         b = at.b;
         RT = P.RT;
         rq = req_info<TT>(P, b);
-        first = true;
     }
-    __device__ bool more() const { return u < u1; }
-    __device__ __forceinline__ void open()
+    // the group at u, or the next one where u lies past a group's tiles; false where the run has ended
+    __device__ __forceinline__ bool open(const AttnParams& P)
     {
-        const long long rem = u - pre;
-        const int grp = (int)(rem / rq.n);
-        tile0 = (int)(rem % rq.n);
-        h = grp / RT;
-        rt = grp % RT;
-        tile1 = (int)min((long long)rq.n, tile0 + (u1 - u));
-        whole = tile0 == 0 && tile1 == rq.n;
-    }
-    __device__ __forceinline__ void next(const AttnParams& P)
-    {
-        first = false;
-        u += tile1 - tile0;
-        while (u < u1 && u >= pre + (long long)rq.n * P.Hkv * RT) {
-            pre += (long long)rq.n * P.Hkv * RT;
-            rq = req_info<TT>(P, ++b);
+        while (u < u1) {
+            while (u >= pre + (long long)rq.span * P.Hkv * RT) {
+                pre += (long long)rq.span * P.Hkv * RT;
+                rq = req_info<TT>(P, ++b);
+            }
+            const long long rem = u - pre;
+            const int grp = (int)(rem / rq.span);
+            tile0 = (int)(rem % rq.span);
+            if (tile0 < rq.n) {
+                h = grp / RT;
+                rt = grp % RT;
+                tile1 = (int)min((long long)rq.n, tile0 + (u1 - u));
+                whole = tile0 == 0 && tile1 == rq.n;
+                return true;
+            }
+            u += rq.span - tile0;
         }
+        return false;
     }
+    __device__ __forceinline__ void next() { u += tile1 - tile0; }
 };
 
 // ---------------------------------------------------------------- roles
@@ -255,8 +257,7 @@ __device__ void role_copy(const TcParams& T, Shared& sh, const Place& at, uint32
     constexpr uint32_t KB = TT * D;
     int it = 0, s = 0, par = 1;  // tiles so far, the next stage and the parity of its last use's end
     bool ok = true;
-    for (Walk w(P, at); ok && w.more(); w.next(P)) {
-        w.open();
+    for (Walk w(P, at); ok && w.open(P); w.next()) {
         const int32_t* table = P.page_table + (size_t)w.b * P.table_width;
         const int c0 = min(w.tile0, w.rq.ncache), c1 = min(w.tile1, w.rq.ncache), len = w.rq.len;
         // Lane k holds page k of a batch of `per` tiles with its scales.  Two batches ahead the page numbers are loaded, one
@@ -358,8 +359,7 @@ __device__ void role_mma(const TcParams& T, Shared& sh, const Place& at, uint32_
         return 1;
     };
 
-    for (Walk w(P, at); ok && w.more(); w.next(P), ++seg) {
-        w.open();
+    for (Walk w(P, at); ok && w.open(P); w.next(), ++seg) {
         const int tile0 = uni(w.tile0), tile1 = uni(w.tile1), ncache = uni(w.rq.ncache);
         for (int tile = tile0; tile < tile1; ++tile) {
             const bool fresh = tile >= ncache, first = tile == tile0;
@@ -569,8 +569,7 @@ __device__ void role_values(const TcParams& T, Shared& sh, const Place& at, uint
     const int ct = threadIdx.x - VW0 * 32, wv = ct >> 5, lane = ct & 31;
     int it = 0, s = 0, par = 0;  // s, par: stage and phase of the tile after the loaded one
     bool ok = true;
-    for (Walk w(P, at); ok && w.more(); w.next(P)) {
-        w.open();
+    for (Walk w(P, at); ok && w.open(P); w.next()) {
         Codes<D> c;
         const auto fetch = [&](int tile) {
             ok = ok && wait_warp(sh, &sh.info[s], par, T.wait_limit);
@@ -1103,8 +1102,7 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
     L.nch = (L.g + 1) * chunks / NG - L.g * chunks / NG;
     int it = 0, s_at = 0, rb = 0;
     bool dead = false;
-    for (Walk w(P, at); w.more(); w.next(P)) {
-        w.open();
+    for (Walk w(P, at); w.open(P); w.next()) {
         int status = w.rq.status;
         bool vbad = false;
         if (!dead) load_q<DT, D>(T, sh, L, w.b, w.h, w.rt, w.rq.rows);
@@ -1147,7 +1145,7 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
         }
         if (!dead) dead = group_any(L.bar_id, !wait_warp(sh, &sh.pv[(it - 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit));
         if (dead) status = ROW_TIMEOUT;
-        float* part = P.parts + ((size_t)blockIdx.x * 2 + (w.first && w.tile0 != 0 ? 0 : 1)) * part_floats(T.MR, D);
+        float* part = P.parts + ((size_t)blockIdx.x * 2 + (w.tile0 != 0 ? 0 : 1)) * part_floats(T.MR, D);
         put_outputs<DT, D>(T, sh, L, rb, w.b, w.h, w.rt, w.rq.rows, w.whole, part, status, dead, vbad);
         if (threadIdx.x == SMW0 * 32) {
             if (w.whole) {
