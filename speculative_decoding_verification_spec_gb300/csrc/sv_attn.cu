@@ -23,10 +23,10 @@
 // tile through a private ring of cp.async stages, so the loop has no barrier; the warps join at the end.
 //
 // What bounds it: a slice is some 500 instructions of one dependent chain (fragments, products, reference, weights, products),
-// and the registers leave eight warps an SM to hide it; DRAM is 30% used.  At B = 32, contexts to 8192, four rows a head: 91 us
-// for 343 MB at T = 1 (3.8 TB/s, over half of a copy's rate), 101 us at T = 4.  A group's start and its own rows cost latency
-// alone: with the first slices called before q is read, and the rows of q and of the round loaded together, 91 and 101 us are
-// what had been 104 and 122.
+// and the registers leave eight warps an SM to hide it; DRAM is 41% used.  At B = 32, contexts to 8192, four rows a head: 88 us
+// for 343 MB at T = 1 (3.9 TB/s, over half of a copy's rate), 95 us at T = 4.  A group's start and its own rows cost latency
+// alone: calling the first slices before q is read, and loading the rows of q and of the round together, took 102 to 91 us and
+// 122 to 101; the schedule's units for a group's change the rest.
 #include "sv_attn.cuh"
 
 namespace sv {
@@ -708,7 +708,7 @@ template <int DT, int D>
 cudaError_t launch_dim(AttnParams& P, int sms, cudaStream_t st)
 {
     // Rows that fill one 16-row tile of mma.sync stay below the memory's pace there.  More rows take the tensor cores' own path:
-    // with 24 rows (B = 32, T = 6, contexts to 8192) two such tiles took 181 us, it takes 139; with 20 or 24 rows of one short
+    // with 24 rows (B = 32, T = 6, contexts to 8192) two such tiles took 181 us where it took 139 (now 129); with 20 or 24 rows of one short
     // context both are launch and latency.  With 8 to 16 rows it cannot pay, its tiles cost the same from one row to 48.
     return P.R <= MR ? launch_rows<DT, D>(P, sms, st) : launch_attention_tc(P, DT, sms, st);
 }

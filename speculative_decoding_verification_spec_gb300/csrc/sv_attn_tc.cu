@@ -24,11 +24,11 @@
 //          rarely after) does the group find the columns' maxima, move the reference, rescale its part of O^T and l and
 //          repeat the tile.
 // What bounds it: neither memory nor the tensor cores, but the chain that each tile goes through (S^T, softmax, P, O^T): some
-// 2000 to 2800 cycles up to 48 rows and 3600 at 87, of which a product takes about 100 whatever its columns, and some 10000
-// more where a CTA changes the group (q, the first reference, the outputs).  The issue slots are 43% used, DRAM 24%.  Contexts
-// to 8192, B = 32, T = 6, four query heads a head: 139 us for 347 MB (2.5 TB/s); to 4096, T = 65 (three row tiles of 87): 459 us
-// for 89 GFLOP (194 TFLOP/s).  A third softmax group (spills), S^T fetched a chunk ahead, and both terms of q stacked into one
-// product of twice the columns were slower: 202, 142 and 147 us where this took 139.
+// 2000 to 2800 cycles up to 48 rows and 3600 at 87, of which a product takes about 100 whatever its columns, and some 12000
+// to 20000 more where a CTA changes the group (q, the first reference, the round's own rows, the outputs).  The issue slots are
+// 44% used, DRAM 27%.  B = 32, contexts to 8192, T = 6, four query heads a head: 129 us for 347 MB (2.7 TB/s); to 4096, T = 65
+// (three row tiles of 87): 375 us for 89 GFLOP (238 TFLOP/s).  A third softmax group (spills), S^T fetched a chunk ahead, and
+// both terms of q stacked into one product of twice the columns were slower: 202, 142 and 147 us where this took 139.
 // Every wait on an mbarrier is bounded; when one runs out the CTA's remaining groups report SPEC_ROW_TIMEOUT.  Between named
 // barriers the threads of a softmax group never part: what a wait returned is agreed on before anyone acts on it.
 #include <cuda.h>
