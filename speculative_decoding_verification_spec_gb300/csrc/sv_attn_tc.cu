@@ -52,8 +52,10 @@ constexpr int MAXSTAGES = 6;
 constexpr float WINDOW = 15.0f;  // a weight may reach 2^WINDOW (the largest half is near 2^16)
 constexpr float HEAD = 3.0f;     // a moved reference leaves the maximum at 2^HEAD: a move repeats a tile, so the room above
                                  // is kept large; a weight 2^-28 of the largest is then the least that a half still holds
-constexpr float FAR = 40.0f;     // log2 of a weight that the first pass keeps out of l: with the 2^74 of a scale it could soon
-                                 // leave fp32's range
+constexpr float LATE = 5.0f;     // where a move is due, columns past 2^LATE move with it: later repeats are fewer (B = 32, T = 65:
+                                 // 362 us, 386 with 14; T = 6, eight query heads a head: 169 and 187).  Under WINDOW by more than the
+                                 // two passes' roundings differ, so that a weight past it does move
+constexpr float HOLD = 14.0f;    // where a weight is put that no reference brings under the window
 constexpr size_t TC_SMEM = 214 * 1024;  // dynamic shared memory; the static arrays take the rest of the SM's 227 KB
 
 struct TcParams {
@@ -640,7 +642,7 @@ struct Lane {
 struct RunEnd {
     int n;              // tiles done
     int status;
-    uint32_t left_out;  // of the tile it stopped at: the 16-column chunks whose sums this warp has not taken
+    uint32_t left_out;  // of the tile it stopped at: the 16-column chunks whose sums this warp has not taken: those past the window
     bool stopped, fail;
 };
 
@@ -668,7 +670,8 @@ __device__ __forceinline__ void token_terms(const Shared& sh, const Lane& L, int
 
 // The softmax over tiles that have a reference: tiles of the cache in a row, or (own) one of the round's rows.  One pass per
 // tile; the run ends where a weight passes the window (for any thread of the group) or a wait runs out.  `take`: chunks whose
-// sums the first tile adds to l.  Nearly all of the kernel's time goes through this loop.
+// sums the first tile adds to l.  The difference to the reference comes before the exponent of the values: near the maximum it is
+// exact, however large the scores.  Nearly all of the kernel's time goes through this loop.
 __device__ __forceinline__ RunEnd softmax_run(const TcParams& T, Shared& sh, const Lane L, const float4* fr, int it, int s_at, int tile, int end, int len,
                                            bool own, uint64_t see_own, uint32_t take)
 {
@@ -710,7 +713,7 @@ __device__ __forceinline__ RunEnd softmax_run(const TcParams& T, Shared& sh, con
                     const unsigned long long x = f2_mul(f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])),
                                                         f2_pack(__uint_as_float(f[j].x), __uint_as_float(f[j].y)));
                     float a, b;
-                    f2_unpack(f2_fma(x, ks2, f2_add(ve2, f2_pack(__uint_as_float(f[j].z), __uint_as_float(f[j].w)))), a, b);
+                    f2_unpack(f2_add(f2_fma(x, ks2, f2_pack(__uint_as_float(f[j].z), __uint_as_float(f[j].w))), ve2), a, b);
                     s[2 * j] = __float_as_uint(a);
                     s[2 * j + 1] = __float_as_uint(b);
                 }
@@ -725,8 +728,8 @@ __device__ __forceinline__ RunEnd softmax_run(const TcParams& T, Shared& sh, con
                 for (int j = 0; j < 8; ++j) t8[j] = fmaxf(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
                 const float top = fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])), fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
                 vmax = fmaxf(vmax, top);
-                const bool far = __any_sync(0xffffffffu, top > FAR);
-                if (far) r.left_out |= 1u << ch;
+                const bool far = __any_sync(0xffffffffu, top > WINDOW);
+                if (far) r.left_out |= take & 1u << ch;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) s[j] = __float_as_uint(ex2(__uint_as_float(s[j])));
 #pragma unroll
@@ -767,9 +770,34 @@ __device__ __forceinline__ RunEnd softmax_run(const TcParams& T, Shared& sh, con
     return r;
 }
 
-// The reference of the columns that tile `it` takes past the window (or that have none): at 2^HEAD under the maximum; the sums so
-// far follow.  False when a wait ran out.  All of the group calls it.
-__device__ __forceinline__ bool move_reference(const TcParams& T, Shared& sh, const Lane L, int rb, int it, int s_at, int left, bool own, uint64_t see_own, bool first)
+// A tile whose weights pass the window even against the reference that was set for it: its scores are replaced by their differences
+// to the reference over the scale of the keys (softmax_run then takes factors of one and no reference, and computes what it did),
+// and those past the window put under it.
+__device__ __noinline__ void hold_scores(const float4* fr, uint32_t t_s, int cw, float ks, float ve)
+{
+#pragma unroll 1
+    for (int c = 0; c < cw; c += 16) {
+        uint32_t s[16];
+        tmem_ld16_nowait(t_s + c, s);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float* f = reinterpret_cast<const float*>(&fr[(c + j) >> 1]);
+            float d = __fmaf_rn(__fmul_rn(__uint_as_float(s[j]), f[j & 1]), ks, f[2 + (j & 1)]);
+            if (__fadd_rn(d, ve) > WINDOW) d = HOLD - ve;
+            s[j] = __float_as_uint(d / ks);
+        }
+        tmem_st16_nowait(t_s + c, s);
+    }
+    tmem_wait_st();
+}
+
+// The reference of the columns that tile `it` takes past the window (or that have none): at 2^HEAD under the maximum, rounded down,
+// so that no rounding takes the maximum's own weight under 2^HEAD.  (From |u| = 2^27 on neighbouring floats are 16 and more apart,
+// so the weight may still come out above the window; scores that near are equal to within their own rounding.)  The sums so far
+// follow.  `hold`: that has happened, and the tile's weights are held at the window, by scores and factors (in the other copy) of
+// their own.  False when a wait ran out.  All of the group calls it.
+__device__ __forceinline__ bool move_reference(const TcParams& T, Shared& sh, const Lane L, int rb, int it, int s_at, int left, bool own, uint64_t see_own, bool first, bool hold)
 {
     const float4* fr = &sh.fr[rb][L.col0 / 2];
     float4* to = &sh.fr[rb ^ 1][L.col0 / 2];
@@ -783,16 +811,18 @@ __device__ __forceinline__ bool move_reference(const TcParams& T, Shared& sh, co
         float ks, ve;
         uint64_t see;
         token_terms(sh, L, it, s_at, T.A.page_shift, left, own, see_own, ks, ve, see);
+        if (hold) hold_scores(fr, t_s, cw, ks, ve);
 #pragma unroll 1
-        for (int c = 0; c < cw; c += 16) {
+        for (int c = hold ? cw : 0; c < cw; c += 16) {
             uint32_t s[16];
             tmem_ld16_nowait(t_s + c, s);
             tmem_wait_ld();
             float mine = NEG_INF;
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const float F = reinterpret_cast<const float*>(&fr[(c + j) >> 1])[j & 1];
-                const float x = see >> (c + j) & 1ull ? fmaf(__uint_as_float(s[j]) * F, ks, ve) : NEG_INF;
+                const float* f = reinterpret_cast<const float*>(&fr[(c + j) >> 1]);
+                const float d = __fadd_rd(__fmaf_rd(__uint_as_float(s[j]) * f[j & 1], ks, first ? 0.0f : f[2 + (j & 1)]), ve);
+                const float x = see >> (c + j) & 1ull ? d : NEG_INF;
                 const float m = redux_max(x);
                 if (L.lane == j) mine = m;
             }
@@ -800,6 +830,11 @@ __device__ __forceinline__ bool move_reference(const TcParams& T, Shared& sh, co
         }
     }
     if (group_any(L.bar_id, !ok)) return false;
+    if (hold) {
+        if (L.tok < cw / 2) to[L.tok] = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+        group_sync(L.bar_id);
+        return true;
+    }
     if (L.tok < cw) {
         const float(*w)[MAXC] = sh.wred[L.g];
         const float top = fmaxf(fmaxf(w[0][L.tok], w[1][L.tok]), fmaxf(w[2][L.tok], w[3][L.tok]));
@@ -808,8 +843,8 @@ __device__ __forceinline__ bool move_reference(const TcParams& T, Shared& sh, co
         float* n = reinterpret_cast<float*>(&to[L.tok >> 1]);
         const float was = first ? 0.0f : -f[2 + (L.tok & 1)];
         const bool none = first || sh.unseen[L.g][L.tok] != 0.0f;
-        const bool move = none ? top > NEG_INF : top > was + WINDOW;
-        const float now = move ? top - HEAD : was;
+        const bool move = none ? top > NEG_INF : top > LATE;
+        const float now = move ? __fadd_rd(was, __fadd_rd(top, -HEAD)) : was;
         n[L.tok & 1] = f[L.tok & 1];
         n[2 + (L.tok & 1)] = -now;
         sh.col[L.g][L.tok].x = first ? 0.0f : move && !none ? ex2(was - now) : 1.0f;  // of the sums so far
@@ -1115,19 +1150,24 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
                 fail = own_tile<DT, D>(T, sh, L, it, w.b, w.rt, w.rq.rows, (tile - w.rq.ncache) * TT, &see, &bad);
                 if (bad) status = ROW_BAD_PARENT;
             }
-            // a group's first tile has no reference yet; another's may turn out too low, and the tile is repeated
-            bool first = tile == w.tile0, again = first;
+            // A group's first tile has no reference yet; another's may turn out too low, and the tile is repeated.  `stops`: how
+            // often the present tile has passed the window: it gets a reference, then weights held at the window; a third time
+            // would end the CTA's work as a wait that ran out does, so no tile can keep the loop running, whatever its scores are.
+            bool first = tile == w.tile0;
+            int stops = first ? 1 : 0;
             uint32_t take = ~0u;
             const int end = own ? tile + 1 : min(w.tile1, w.rq.ncache);
             while (tile < end) {
-                if (again) {
-                    if (!move_reference(T, sh, L, rb, it, s_at, w.rq.len - tile * TT, own, see, first)) {
+                if (stops > 0) {
+                    if (stops > 2 || !move_reference(T, sh, L, rb, it, s_at, w.rq.len - tile * TT, own, see, first, stops == 2)) {
+                        *reinterpret_cast<volatile int*>(&sh.fail) = 1;
                         dead = true;
                         break;
                     }
-                    rb ^= 1;
+                    if (stops == 1) rb ^= 1;
                 }
-                const RunEnd r = softmax_run(T, sh, L, &sh.fr[rb][L.col0 / 2], it, s_at, tile, end, w.rq.len, own, see, take);
+                const bool hold = stops == 2;
+                const RunEnd r = softmax_run(T, sh, L, &sh.fr[hold ? rb ^ 1 : rb][L.col0 / 2], it, s_at, tile, hold ? tile + 1 : end, w.rq.len, own, see, take);
                 status = max(status, r.status);
                 tile += r.n;
                 it += r.n;
@@ -1136,9 +1176,9 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
                     dead = true;
                     break;
                 }
-                again = r.stopped;
+                stops = !r.stopped ? 0 : r.n > 0 ? 1 : stops + 1;
                 first = false;
-                take = r.left_out;
+                take = r.stopped ? r.left_out : ~0u;
             }
             if (own && !dead)
                 for (int k = 0; k < VWN; ++k) vbad = vbad || sh.vbad[(it - 1) & 3][k];

@@ -1,0 +1,99 @@
+"""The calls around the verify step where they can go wrong: scores past 2^24, waits that run out in one CTA, long prompts,
+streams, captures, and both attention kernels (T Hq / Hkv up to 16 rows, and more) on the same inputs."""
+import math
+
+import pytest
+import torch
+
+import speculative_decoding_verification_spec_gb300 as sv
+from speculative_decoding_verification_spec_gb300 import binding as B_
+
+import round_ref as R
+from test_gpu_round import DT, Pool, check_attention, round_inputs, run_attention, same
+
+pytestmark = pytest.mark.gpu
+
+
+def copies(p, n):
+    """The pool's requests n times over (they share their pages), so that a CTA works through a request's tiles one after another."""
+    p.dtable, p.dlens = p.dtable.repeat(n, 1), p.dlens.repeat(n)
+
+
+# ------------------------------------------------------------------ scores past 2^24
+
+def in_hull(out, v):
+    """Whether every output lies between the least and the largest value of its head, to its type's rounding."""
+    lo, hi = v.amin(0), v.amax(0)  # [heads, D]
+    room = 2.0 ** -10 * torch.maximum(lo.abs(), hi.abs())
+    G = out.shape[1] // v.shape[1]
+    lo, hi, room = (x.repeat_interleave(G, 0) for x in (lo, hi, room))
+    return bool(((out >= lo - room) & (out <= hi + room)).all())
+
+
+@pytest.mark.parametrize("later,ve", [(1.0, (-8, -8)), (0.0, (-12, 0)), (0.0, (-8, 8)), (0.0, (8, -40))])
+@pytest.mark.parametrize("T,hq", [(6, 16)])
+def test_attention_neighbouring_scores_past_2_27(T, hq, later, ve):
+    """Scores (or their sums with the values' exponents) that are neighbouring floats, 16 apart, with the larger ones later: the
+    reference cannot lie between them."""
+    g = torch.Generator().manual_seed(41)
+    D, page, n = 128, 64, 512
+    p = Pool(g, [n], 1, page, D)
+    for j in range(n // page):
+        k = torch.full((1, page, D), 1.5)
+        late = j >= n // page // 2
+        k[..., -1] = later if late else 0.0
+        i = int(p.table[0, j])
+        p.codes[0][i] = k.to(R.FP8)
+        p.scales[0][i] = 1.0
+        p.scales[1][i] = 2.0 ** ve[late]
+    p.cache.k.view(torch.uint8).copy_(p.codes[0].view(torch.uint8).cuda())
+    p.cache.k_scale.copy_(p.scales[0])
+    p.cache.v_scale.copy_(p.scales[1])
+    q = torch.full((1, T, hq, D), 2.0 ** 20)
+    q[..., -1] = 2.0 ** 4                      # log2(e) s = 190.5 2^20, and 16 more
+    more = torch.exp2(torch.arange(T * hq) % 4.0).view(T, hq)
+    q = (q * more[None, ..., None]).bfloat16()
+    copies(p, 320)
+    r = run_attention(p, q.repeat(320, 1, 1, 1), None, None, scale=math.log(2.0))
+    assert r["row_status"].tolist() == [0] * 320
+    top = 190.5 * 2.0 ** 20 * more * math.log(2.0)
+    for b in range(320):
+        assert in_hull(r["out"][b].double(), p.line(1, 0)), b
+        assert bool(((r["lse"][b] / top - 1).abs() <= 2.0 ** -20).all()), b
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,hq", [(1, 4), (3, 5), (3, 8), (9, 16)])
+@pytest.mark.parametrize("e", [11, 16, 17, 18, 19, 22, 30, 60])
+def test_attention_huge_scores(T, hq, dtype, e):
+    """|log2(e) s| from 2^20 to 2^70, values of pages with several exponents: every tile is left after one repeat, and where one token
+    stands clear of the scores' own rounding the output is its value."""
+    g = torch.Generator().manual_seed(100 * T + e)
+    D = 128
+    p = Pool(g, [700, 130], 1, 16, D)
+    p.codes[0] = p.codes[0].float().abs().to(R.FP8)
+    p.scales[0][:] = 2.0 ** e
+    p.cache.k.view(torch.uint8).copy_(p.codes[0].view(torch.uint8).cuda())
+    p.cache.k_scale.copy_(p.scales[0])
+    q, kn, vn = round_inputs(g, 2, T, hq, 1, D, dtype)
+    q = (q.abs() + 0.5).to(DT[dtype])
+    n = 160
+    copies(p, n)
+    r = run_attention(p, *(x.repeat(n, 1, 1, 1) for x in (q, kn, vn)))
+    assert r["row_status"].tolist() == [0] * (2 * n)
+    clear = 0
+    for b in range(2):
+        kc, vc = p.line(0, b), p.line(1, b)
+        out, lse, absv, seen, size = R.attention_ref(q[b], kc, vc, kn[b], vn[b], None, T, D ** -0.5)
+        vmax = float(max(vc.abs().max(), vn.abs().max()))
+        tol, _ = R.attention_tolerance(out, lse, absv, seen, torch.zeros_like(size), vmax, D, q.dtype)
+        ds = D * 2.0 ** -23 * size
+        s = torch.einsum("thd,jd->thj", q[b].double(), kc[:, 0]) * D ** -0.5
+        best = s.topk(2).values
+        ok = best[..., 0] - best[..., 1] > 4 * ds + 64
+        clear += int(ok.sum())
+        for c in range(b, 2 * n, 2):
+            assert in_hull(r["out"][c].double(), torch.cat([vc, vn[b].double()])), c
+            assert bool(((r["lse"][c].double() - lse).abs() <= 2 * ds + 2.0 ** -22 * lse.abs() + 1e-3).all()), c
+            assert bool(((r["out"][c].double() - out).abs() <= tol)[ok].all()), c
+    assert clear >= T * hq
