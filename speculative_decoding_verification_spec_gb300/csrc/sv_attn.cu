@@ -116,8 +116,9 @@ __device__ __forceinline__ void slice_step(RowState<D>& S, const uint32_t (&qf)[
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             float m = S.m[mt][hi];
-            // the reference moves only when the maximum has left its 2^8 window, so the sums are rarely rescaled
-            const bool move = top > m + 15.0f;
+            // the reference moves only when the maximum has left its 2^8 window, so the sums are rarely rescaled (the difference,
+            // not the sum: from |u| = 2^27 on m + 15 rounds to the next float, 16 away, and a weight of 2^16 is no half)
+            const bool move = top - m > 15.0f;
             if (__any_sync(0xffffffffu, move)) {
                 const float now = move ? top - 7.0f : m;
                 const float f = move ? (m == NEG_INF ? 0.0f : ex2(m - now)) : 1.0f;

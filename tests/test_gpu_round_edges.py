@@ -31,7 +31,7 @@ def in_hull(out, v):
 
 
 @pytest.mark.parametrize("later,ve", [(1.0, (-8, -8)), (0.0, (-12, 0)), (0.0, (-8, 8)), (0.0, (8, -40))])
-@pytest.mark.parametrize("T,hq", [(6, 16)])
+@pytest.mark.parametrize("T,hq", [(2, 4), (6, 16)])
 def test_attention_neighbouring_scores_past_2_27(T, hq, later, ve):
     """Scores (or their sums with the values' exponents) that are neighbouring floats, 16 apart, with the larger ones later: the
     reference cannot lie between them."""
