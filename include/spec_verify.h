@@ -500,8 +500,9 @@ size_t verify_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
  * A row that sees nothing gives zeros and -inf.  What a row does not see has no effect on it, whatever it
  * holds.  Scores, softmax and sums are fp32; out is rounded once.  A row of q that holds a NaN or an infinity gives
  * NaN, and so does a key of the round that does, for the rows that see it.
- * row_status [B] (nullable): SPEC_ROW_BAD_LENGTH, BAD_PAGE, BAD_PARENT, and SPEC_ROW_TIMEOUT where more than 16 rows share
- * a key/value head (T Hq / Hkv; that path waits on mbarriers); the request's out and lse are NaN.
+ * row_status [B] (nullable): SPEC_ROW_BAD_LENGTH, BAD_PAGE, BAD_PARENT: the request's out and lse are NaN.
+ * SPEC_ROW_TIMEOUT where more than 16 rows share a key/value head (T Hq / Hkv; that path waits on mbarriers): what the wait
+ * that ran out kept from being computed, of any head, is NaN.
  * workspace: verify_attention_workspace_bytes(...), 16-byte aligned, no initialisation needed.
  */
 spec_status verify_attention(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,

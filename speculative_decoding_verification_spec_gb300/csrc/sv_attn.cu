@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(ANT, D == 64 ? 3 : 2) attn_rows_kernel(AttnPar
 
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const Place at = find_place<TILE>(P, blockIdx.x, gridDim.x, &place);
-    if (tid == 0) P.joins[blockIdx.x].parts = 0;
+    if (tid == 0) P.joins[blockIdx.x] = {};
     launch_dependents();
     if ((int)blockIdx.x >= at.ctas) return;
     long long u = at.total * blockIdx.x / at.ctas;
@@ -560,9 +560,8 @@ __global__ void __launch_bounds__(ANT, D == 64 ? 3 : 2) attn_rows_kernel(AttnPar
             }
         }
         if (tid == 0) {
-            if (whole) {
-                if (P.row_status && h == 0 && rt == 0) P.row_status[b] = status;
-            } else {
+            begin_status(P, b, h, rt, tile0, status);
+            if (!whole) {
                 part[MR * D + 2 * MR] = __int_as_float(status);
                 // the group's first part: tell the joining kernel how far the group reaches
                 if (tile0 == 0) P.joins[blockIdx.x] = {parts_of(at.total, blockIdx.x, at.ctas, u + rq.n), b, h, rt, rq.rows};
@@ -583,6 +582,8 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(AttnParams P, int MR)
     __shared__ int ss[8];
     depend_wait();
     const AttnJoin J = P.joins[blockIdx.x];
+    if (blockIdx.y == 0)
+        for (int b = max(J.lost0, 0) + threadIdx.x; b < min(J.lost1, P.B); b += blockDim.x) raise_status(P, b, ROW_TIMEOUT);
     if (J.parts == 0) return;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, q = w & 3;
     const size_t pf = part_floats(MR, D);
@@ -599,6 +600,8 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(AttnParams P, int MR)
                 const float* part = part_of(k);
                 m = fmaxf(m, part[(size_t)MR * D + row]);
                 status = max(status, __float_as_int(part[(size_t)MR * D + 2 * MR]));
+                const AttnJoin& c = P.joins[blockIdx.x + k];
+                if (c.lost0 <= J.b && J.b < c.lost1) status = max(status, (int)ROW_TIMEOUT);
             }
 #pragma unroll
             for (int s = 16; s; s >>= 1) {
@@ -659,7 +662,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(AttnParams P, int MR)
                 O.w = fmaf(x.w, f, O.w);
             }
             if (lane < D / 4) finish_row4<DT>(P, J.b, J.h, r, J.rows, status, lane * 4, O, M, L);
-            if (row == 0 && lane == 0 && P.row_status && J.h == 0 && J.rt == 0) P.row_status[J.b] = status;
+            if (row == 0 && lane == 0) raise_status(P, J.b, status);
         }
         __syncthreads();
     }

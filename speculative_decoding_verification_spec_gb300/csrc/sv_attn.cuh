@@ -11,6 +11,17 @@ constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 // is read in vectors
 __host__ __device__ constexpr size_t part_floats(int MR, int D) { return ((size_t)MR * D + 2 * MR + 1 + 3) / 4 * 4; }
 
+// The status of a request: the CTA that begins its first group (head 0, row tile 0) writes what it knows, and attn_merge_kernel,
+// which runs after all of them, raises it where a joined group or a wait that ran out (AttnJoin::lost0) says more.
+__device__ __forceinline__ void begin_status(const AttnParams& P, int b, int h, int rt, int tile0, int status)
+{
+    if (P.row_status && h == 0 && rt == 0 && tile0 == 0) P.row_status[b] = status;
+}
+__device__ __forceinline__ void raise_status(const AttnParams& P, int b, int status)
+{
+    if (P.row_status && status != ROW_OK) atomicMax(P.row_status + b, status);
+}
+
 // parts of the group that starts in CTA c and ends at unit `end`: CTA k holds units [total k / ctas, total (k + 1) / ctas)
 __device__ __forceinline__ int parts_of(long long total, int c, int ctas, long long end)
 {

@@ -166,6 +166,7 @@ struct Shared {
     float fks[2][TT], fve[2][TT]; // round's rows: scale of the keys and exponent of the values, per token
     int vbad[4][VWN];               // round's rows: a tile's values hold a NaN or an infinity, per warp
     int fail;
+    int lost[NG][2];              // requests that a softmax group left without outputs: first and one past the last
     uint32_t tmem;
     Place place;
 };
@@ -1184,13 +1185,19 @@ __device__ void role_softmax(const TcParams& T, Shared& sh, const Place& at, uin
                 for (int k = 0; k < VWN; ++k) vbad = vbad || sh.vbad[(it - 1) & 3][k];
         }
         if (!dead) dead = group_any(L.bar_id, !wait_warp(sh, &sh.pv[(it - 1) & 1], ((it - 1) >> 1) & 1, T.wait_limit));
-        if (dead) status = ROW_TIMEOUT;
+        if (dead) {
+            status = ROW_TIMEOUT;
+            if (L.tok == 0) {
+                if (sh.lost[L.g][1] == 0) sh.lost[L.g][0] = w.b;
+                sh.lost[L.g][1] = w.b + 1;
+            }
+        }
         float* part = P.parts + ((size_t)blockIdx.x * 2 + (w.tile0 != 0 ? 0 : 1)) * part_floats(T.MR, D);
         put_outputs<DT, D>(T, sh, L, rb, w.b, w.h, w.rt, w.rq.rows, w.whole, part, status, dead, vbad);
+        // (but for waits that ran out, which `lost` tells of, the softmax groups' statuses are the same)
         if (threadIdx.x == SMW0 * 32) {
-            if (w.whole) {
-                if (P.row_status && w.h == 0 && w.rt == 0) P.row_status[w.b] = status;
-            } else {
+            begin_status(P, w.b, w.h, w.rt, w.tile0, status);
+            if (!w.whole) {
                 part[(size_t)T.MR * D + 2 * T.MR] = __int_as_float(status);
                 if (w.tile0 == 0) P.joins[blockIdx.x] = {parts_of(at.total, blockIdx.x, at.ctas, w.u + w.rq.n), w.b, w.h, w.rt, w.rq.rows};
             }
@@ -1208,7 +1215,7 @@ attn_tc_kernel(const __grid_constant__ TcParams T, const __grid_constant__ CUten
     const AttnParams& P = T.A;
     const int tid = threadIdx.x, w = tid >> 5;
     if (tid == 0) {
-        P.joins[blockIdx.x].parts = 0;
+        P.joins[blockIdx.x] = {};
         for (int i = 0; i < T.stages; ++i) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.info[i], 1);
@@ -1223,6 +1230,7 @@ attn_tc_kernel(const __grid_constant__ TcParams T, const __grid_constant__ CUten
         mbar_init(&sh.qfull, 4 * NG);
         mbar_init(&sh.done, 1);
         sh.fail = 0;
+        for (int g = 0; g < NG; ++g) sh.lost[g][1] = 0;
         fence_mbar_init();
     }
     launch_dependents();
@@ -1248,6 +1256,15 @@ attn_tc_kernel(const __grid_constant__ TcParams T, const __grid_constant__ CUten
     else if (w >= SMW0) role_softmax<DT, D>(T, sh, at, smem, tmem);
     tc_fence_before();
     __syncthreads();
+    if (tid == 0) {
+        int lo = P.B, hi = 0;
+        for (int g = 0; g < NG; ++g)
+            if (sh.lost[g][1] > 0) lo = min(lo, sh.lost[g][0]), hi = max(hi, sh.lost[g][1]);
+        if (hi > 0) {
+            P.joins[blockIdx.x].lost0 = lo;
+            P.joins[blockIdx.x].lost1 = hi;
+        }
+    }
     if (w == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem));

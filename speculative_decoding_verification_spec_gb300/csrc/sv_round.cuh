@@ -134,7 +134,8 @@ constexpr int ATTN_MAX_TC_CTAS = 256;  // and of the kernel for many rows
 // a group of rows that starts in one streaming CTA and ends in a later one (parts == 0: none starts there)
 struct AttnJoin {
     int parts, b, h, rt, rows;
-    int pad[3];
+    int lost0, lost1;  // requests [lost0, lost1) of the CTA are without some of their outputs: a wait ran out
+    int pad;
 };
 
 struct AttnParams {

@@ -19,6 +19,37 @@ def copies(p, n):
     p.dtable, p.dlens = p.dtable.repeat(n, 1), p.dlens.repeat(n)
 
 
+# ------------------------------------------------------------------ waits that run out
+
+@pytest.mark.parametrize("T,hq,hkv,lens", [(6, 16, 4, [900, 3, 0, 2100]), (40, 8, 8, [600] * 24), (6, 32, 8, [70] * 90)])
+def test_attention_time_outs_of_any_head_are_reported(T, hq, hkv, lens):
+    """Limits under which waits run out in some CTAs and not in others: a request without a status holds what it held before, and one
+    with the status holds nothing else but NaN."""
+    g = torch.Generator().manual_seed(51)
+    p = Pool(g, lens, hkv, 64, 128)
+    q, kn, vn = (x.cuda() for x in round_inputs(g, len(lens), T, hq, hkv, 128, "bf16"))
+    call = lambda: sv.verify_attention(q, p.cache, p.dtable, p.dlens, k=kn, v=vn, lse=True)
+    clean = call()
+    seen = set()
+    for limit in [1, 2, 3, 4, 6, 8, 12] * 12:
+        old = sv.set_wait_limit(limit)
+        try:
+            r = call()
+        finally:
+            sv.set_wait_limit(old)
+        status = r["row_status"].tolist()
+        seen.update(status)
+        for name in ("out", "lse"):
+            x, y = r[name].flatten(1), clean[name].flatten(1)
+            gone = x.isnan()
+            assert bool(((x == y) | gone).all()), (limit, name)
+            lost = gone.any(1).tolist()
+            assert all(s == B_.ROW_TIMEOUT for s, l in zip(status, lost) if l), (limit, name, status, lost)
+    assert seen <= {B_.ROW_OK, B_.ROW_TIMEOUT}
+    again = call()
+    assert torch.equal(again["out"], clean["out"]) and torch.equal(again["lse"], clean["lse"])
+
+
 # ------------------------------------------------------------------ scores past 2^24
 
 def in_hull(out, v):
