@@ -138,128 +138,148 @@ __device__ int write_status(const CacheWriteParams& P, int b, int len, int count
     return bad;
 }
 
-// NV: 16-byte source vectors per thread, at most (a page's worth over NT threads, rounded up to a power of two)
-template <int DT, int NV, bool ALIGNED>
-__global__ void __launch_bounds__(NT, NV <= 4 ? 6 : 1) cache_write_kernel(CacheWriteParams P)
+// NV: 16-byte source vectors per thread, at most (a page's worth over NT threads, rounded up to a power of two).  LONG: a CTA takes
+// several pages; of its own, as the loop costs registers that the kernel for one page has not.
+template <int DT, int NV, bool ALIGNED, bool LONG>
+__global__ void __launch_bounds__(NT, NV <= 4 ? (LONG ? 4 : 6) : 1) cache_write_kernel(CacheWriteParams P)
 {
     constexpr int VEC = Elem<DT>::VEC;
     __shared__ uint32_t red[WARPS];
     const int which = blockIdx.y & 1, h = blockIdx.y >> 1, b = blockIdx.z, t = threadIdx.x;
     const int len = __ldg(P.lens + b);
     const int count = P.accepted_len ? min(max(__ldg(P.accepted_len + b), -1), P.T) + 1 : P.T;
-    const int j = len / P.page + blockIdx.x;                       // page of the request
-    const int first = max((int)(len - (long long)j * P.page), 0);  // slots the request held before
-    const long long r0 = (long long)j * P.page + first - len;      // the first row that goes into this page
-    const int rows = len < 0 ? 0 : (int)max(0LL, min(min((long long)count, (long long)P.T) - r0, (long long)(P.page - first)));
+    for (int at_page = blockIdx.x; at_page < P.span; at_page += gridDim.x) {
+        if (LONG && at_page != (int)blockIdx.x) __syncthreads();  // `red` has been read
+        const int j = len / P.page + at_page;                          // page of the request
+        const int first = max((int)(len - (long long)j * P.page), 0);  // slots the request held before
+        const long long r0 = (long long)j * P.page + first - len;      // the first row that goes into this page
+        const int rows = len < 0 ? 0 : (int)max(0LL, min(min((long long)count, (long long)P.T) - r0, (long long)(P.page - first)));
 
-    // The rows are on their way while the request is looked over: a prompt's CTAs spend their time in that chain of loads.
-    // (A node that is out of range is clamped here and refused below.)
-    const int vshift = 31 - __clz(P.D / VEC), vpr = 1 << vshift;  // vectors per row
-    uint4 x[NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int i = t + k * NT;
-        x[k] = make_uint4(0, 0, 0, 0);
-        if (i < rows * vpr) {
-            const int at = (int)r0 + (i >> vshift);
-            int row = at;
-            if (P.out_nodes && at > 0)
-                row = at - 1 < P.nodes_width ? min(max(__ldg(P.out_nodes + (size_t)b * P.nodes_width + at - 1), -1), P.T - 2) + 1 : 0;
-            x[k] = load16<DT, ALIGNED>(P.src[which], b * P.sb[which] + row * P.st[which] + h * P.sh[which] + (i & (vpr - 1)) * VEC);
-        }
-    }
-    const int page = rows > 0 && j < P.table_width ? __ldg(P.page_table + (size_t)b * P.table_width + j) : 0;
-    const int status = write_status(P, b, len, count);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) {
-        if (P.row_status) P.row_status[b] = status;
-        if (P.lens_out) P.lens_out[b] = status == ROW_OK ? len + count : len;
-    }
-    if (status != ROW_OK || rows <= 0) return;
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) top = fold_magnitude<DT>(top, x[k]);
-    top = __reduce_max_sync(0xffffffffu, __float_as_uint(magnitude<DT>(top)));
-    if ((t & 31) == 0) red[t >> 5] = top;
-    float* sp = P.scale[which] + (size_t)page * P.Hkv + h;
-    const float old = first > 0 ? *sp : 0.0f;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) top = max(top, red[w]);
-    float amax = __uint_as_float(top);
-    const bool plain = amax <= CACHE_MAX_CODE * 0x1p60f;
-    if (!plain) {
-        // something that no scale holds (or an infinity, or NaN): it becomes NaN and sets no scale
-        amax = 0.0f;
+        // The rows are on their way while the request is looked over: a prompt's CTAs spend their time in that chain of loads.
+        // (A node that is out of range is clamped here and refused below.)
+        const int vshift = 31 - __clz(P.D / VEC), vpr = 1 << vshift;  // vectors per row
+        uint4 x[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            float f[VEC];
-            widen<DT>(x[k], f);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (fabsf(f[e]) <= CACHE_MAX_CODE * 0x1p60f) amax = fmaxf(amax, fabsf(f[e]));
-        }
-        amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-        __syncthreads();
-        if ((t & 31) == 0) red[t >> 5] = __float_as_uint(amax);
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) amax = fmaxf(amax, __uint_as_float(red[w]));
-    }
-    const int e = cache_scale_exp(amax);
-    float s = exp2_int(e);
-    float inv = exp2_int(-e);
-    uint8_t* dst = P.codes[which] + ((size_t)page * P.Hkv + h) * P.page * P.D;
-    if (old >= s) {
-        s = old;
-        inv = 1.0f / old;
-    } else if (first > 0) {
-        // the page's earlier codes move to the larger scale: exact but for subnormals
-        const float ratio = old * inv;
-        for (int i = t; i < first * P.D / 16; i += NT) {
-            uint4 w = reinterpret_cast<uint4*>(dst)[i];
-            uint32_t* u = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t lo = e4m3x2_to_half2((uint16_t)u[k]), hi = e4m3x2_to_half2((uint16_t)(u[k] >> 16));
-                const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-                const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-                u[k] = (uint32_t)e4m3x2_from(a.x * ratio, a.y * ratio) |
-                       (uint32_t)e4m3x2_from(c.x * ratio, c.y * ratio) << 16;
+            const int i = t + k * NT;
+            x[k] = make_uint4(0, 0, 0, 0);
+            if (i < rows * vpr) {
+                const int at = (int)r0 + (i >> vshift);
+                int row = at;
+                if (P.out_nodes && at > 0)
+                    row = at - 1 < P.nodes_width ? min(max(__ldg(P.out_nodes + (size_t)b * P.nodes_width + at - 1), -1), P.T - 2) + 1 : 0;
+                x[k] = load16<DT, ALIGNED>(P.src[which], b * P.sb[which] + row * P.st[which] + h * P.sh[which] + (i & (vpr - 1)) * VEC);
             }
-            reinterpret_cast<uint4*>(dst)[i] = w;
         }
-    }
-    if (t == 0) *sp = s;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int i = t + k * NT;
-        if (i < rows * vpr) {
-            float f[VEC];
-            widen<DT>(x[k], f);
-            uint16_t c[VEC / 2];
-#pragma unroll
-            for (int q = 0; q < VEC / 2; ++q)
-                c[q] = plain ? e4m3x2_plain(f[2 * q] * inv, f[2 * q + 1] * inv) : e4m3x2_from(f[2 * q] * inv, f[2 * q + 1] * inv);
-            uint8_t* o = dst + first * P.D + i * VEC;
-            if constexpr (VEC == 8)
-                *reinterpret_cast<uint2*>(o) = make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
-            else
-                *reinterpret_cast<uint32_t*>(o) = c[0] | (uint32_t)c[1] << 16;
+        const int page = rows > 0 && j < P.table_width ? __ldg(P.page_table + (size_t)b * P.table_width + j) : 0;
+        if (!LONG || at_page == (int)blockIdx.x) {
+            const int status = write_status(P, b, len, count);
+            if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) {
+                if (P.row_status) P.row_status[b] = status;
+                if (P.lens_out) P.lens_out[b] = status == ROW_OK ? len + count : len;
+            }
+            if (status != ROW_OK) return;
         }
+        if (rows <= 0) return;  // and the pages after this one have none
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) top = fold_magnitude<DT>(top, x[k]);
+        top = __reduce_max_sync(0xffffffffu, __float_as_uint(magnitude<DT>(top)));
+        if ((t & 31) == 0) red[t >> 5] = top;
+        float* sp = P.scale[which] + (size_t)page * P.Hkv + h;
+        const float old = first > 0 ? *sp : 0.0f;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) top = max(top, red[w]);
+        float amax = __uint_as_float(top);
+        const bool plain = amax <= CACHE_MAX_CODE * 0x1p60f;
+        if (!plain) {
+            // something that no scale holds (or an infinity, or NaN): it becomes NaN and sets no scale
+            amax = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float f[VEC];
+                widen<DT>(x[k], f);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (fabsf(f[e]) <= CACHE_MAX_CODE * 0x1p60f) amax = fmaxf(amax, fabsf(f[e]));
+            }
+            amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+            __syncthreads();
+            if ((t & 31) == 0) red[t >> 5] = __float_as_uint(amax);
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) amax = fmaxf(amax, __uint_as_float(red[w]));
+        }
+        const int e = cache_scale_exp(amax);
+        float s = exp2_int(e);
+        float inv = exp2_int(-e);
+        uint8_t* dst = P.codes[which] + ((size_t)page * P.Hkv + h) * P.page * P.D;
+        if (old >= s) {
+            s = old;
+            inv = 1.0f / old;
+        } else if (first > 0) {
+            // the page's earlier codes move to the larger scale: exact but for subnormals
+            const float ratio = old * inv;
+            for (int i = t; i < first * P.D / 16; i += NT) {
+                uint4 w = reinterpret_cast<uint4*>(dst)[i];
+                uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t lo = e4m3x2_to_half2((uint16_t)u[k]), hi = e4m3x2_to_half2((uint16_t)(u[k] >> 16));
+                    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+                    const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                    u[k] = (uint32_t)e4m3x2_from(a.x * ratio, a.y * ratio) |
+                           (uint32_t)e4m3x2_from(c.x * ratio, c.y * ratio) << 16;
+                }
+                reinterpret_cast<uint4*>(dst)[i] = w;
+            }
+        }
+        if (t == 0) *sp = s;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int i = t + k * NT;
+            if (i < rows * vpr) {
+                float f[VEC];
+                widen<DT>(x[k], f);
+                uint16_t c[VEC / 2];
+#pragma unroll
+                for (int q = 0; q < VEC / 2; ++q)
+                    c[q] = plain ? e4m3x2_plain(f[2 * q] * inv, f[2 * q + 1] * inv) : e4m3x2_from(f[2 * q] * inv, f[2 * q + 1] * inv);
+                uint8_t* o = dst + first * P.D + i * VEC;
+                if constexpr (VEC == 8)
+                    *reinterpret_cast<uint2*>(o) = make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
+                else
+                    *reinterpret_cast<uint32_t*>(o) = c[0] | (uint32_t)c[1] << 16;
+            }
+        }
+        if (!LONG) break;
     }
 }
 
-template <int DT, bool ALIGNED>
-cudaError_t write_launch(const CacheWriteParams& P, cudaStream_t st)
+template <int DT, bool ALIGNED, bool LONG>
+cudaError_t write_grid(const CacheWriteParams& P, dim3 grid, cudaStream_t st)
 {
-    const int pages = (P.T + P.page - 2) / P.page + 1;  // pages that T rows can touch
-    const dim3 grid((unsigned)pages, (unsigned)(2 * P.Hkv), (unsigned)P.B);
     const int vecs = (min(P.page, P.T) * P.D / Elem<DT>::VEC + NT - 1) / NT;
-    if (vecs <= 1) cache_write_kernel<DT, 1, ALIGNED><<<grid, NT, 0, st>>>(P);
-    else if (vecs <= 4) cache_write_kernel<DT, 4, ALIGNED><<<grid, NT, 0, st>>>(P);
-    else if (vecs <= 8) cache_write_kernel<DT, 8, ALIGNED><<<grid, NT, 0, st>>>(P);
-    else cache_write_kernel<DT, 16, ALIGNED><<<grid, NT, 0, st>>>(P);
+    if (vecs <= 1) cache_write_kernel<DT, 1, ALIGNED, LONG><<<grid, NT, 0, st>>>(P);
+    else if (vecs <= 4) cache_write_kernel<DT, 4, ALIGNED, LONG><<<grid, NT, 0, st>>>(P);
+    else if (vecs <= 8) cache_write_kernel<DT, 8, ALIGNED, LONG><<<grid, NT, 0, st>>>(P);
+    else cache_write_kernel<DT, 16, ALIGNED, LONG><<<grid, NT, 0, st>>>(P);
     return cudaGetLastError();
+}
+
+template <int DT, bool ALIGNED>
+cudaError_t write_launch(CacheWriteParams& P, cudaStream_t st)
+{
+    // Every CTA looks at all of its request's page-table entries: with up to SCAN of them (four loads a thread) it takes one page,
+    // in a longer request as many more, so that the entries read grow with the tokens and not with their square.  One request of 131072
+    // tokens, eight heads of 128 channels: 369 us with pages of 16 and 168 with 64 (740 and 188 with one page a CTA throughout; 461 and
+    // 190 with 16 NT, 437 and 244 at 4 NT with three CTAs an SM).
+    constexpr int SCAN = 4 * NT;
+    P.span = (P.T + P.page - 2) / P.page + 1;  // pages that T rows can touch
+    const int per = (P.span + SCAN - 1) / SCAN;
+    const dim3 grid((unsigned)((P.span + per - 1) / per), (unsigned)(2 * P.Hkv), (unsigned)P.B);
+    return per == 1 ? write_grid<DT, ALIGNED, false>(P, grid, st) : write_grid<DT, ALIGNED, true>(P, grid, st);
 }
 
 // ---------------------------------------------------------------- read
@@ -360,7 +380,7 @@ __global__ void __launch_bounds__(NT) cache_read_kernel(CacheReadParams P)
 
 }  // namespace
 
-cudaError_t launch_cache_write(const CacheWriteParams& P, int dtype, cudaStream_t st)
+cudaError_t launch_cache_write(CacheWriteParams& P, int dtype, cudaStream_t st)
 {
     const int vec = dtype == DT_F32 ? 4 : 8;
     bool aligned = true;

@@ -108,9 +108,10 @@ struct CacheWriteParams {
     int32_t* lens_out;
     int32_t* row_status;
     int B, T, Hkv, D, page, pages, table_width;
+    int span;                      // pages that a request's rows may touch
 };
 
-cudaError_t launch_cache_write(const CacheWriteParams& P, int dtype, cudaStream_t st);
+cudaError_t launch_cache_write(CacheWriteParams& P, int dtype, cudaStream_t st);
 
 struct CacheReadParams {
     const uint8_t* codes[2];

@@ -9,7 +9,7 @@ import speculative_decoding_verification_spec_gb300 as sv
 from speculative_decoding_verification_spec_gb300 import binding as B_
 
 import round_ref as R
-from test_gpu_round import DT, Pool, check_attention, round_inputs, run_attention, same
+from test_gpu_round import DT, Pool, check_attention, check_write, round_inputs, run_attention, same
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +128,47 @@ def test_attention_huge_scores(T, hq, dtype, e):
             assert bool(((r["lse"][c].double() - lse).abs() <= 2 * ds + 2.0 ** -22 * lse.abs() + 1e-3).all()), c
             assert bool(((r["out"][c].double() - out).abs() <= tol)[ok].all()), c
     assert clear >= T * hq
+
+
+# ------------------------------------------------------------------ long prompts
+
+@pytest.mark.parametrize("T,page,D,accepted", [(17000, 16, 64, [16999, 9001, -1]), (33000, 32, 128, None)])
+def test_write_of_a_long_prompt(T, page, D, accepted):
+    """More pages than a CTA's share: a CTA takes several."""
+    g = torch.Generator().manual_seed(61)
+    B = 3 if accepted else 1
+    p = Pool(g, [0, page - 3, 2 * page][:B], 1, page, D, spare=T)
+    mag = torch.exp2(torch.randint(-6, 7, (B, T, 1, 1), generator=g).float())
+    k, v = ((torch.randn(B, T, 1, D, generator=g) * mag).bfloat16().cuda() for _ in range(2))
+    check_write(p, k, v, accepted)
+
+
+def test_write_of_a_long_prompt_refuses_it_whole():
+    g = torch.Generator().manual_seed(62)
+    T = 17000
+    p = Pool(g, [5, 9], 1, 16, 64, spare=T)
+    k, v = (torch.randn(2, T, 1, 64, generator=g).bfloat16().cuda() for _ in range(2))
+    p.table[0, 1062] = p.codes[0].shape[0]
+    p.dtable = p.table.cuda()
+    r = check_write(p, k, v, bad=(0,))
+    assert r["row_status"].tolist() == [B_.ROW_BAD_PAGE, 0]
+
+
+def test_write_time_grows_with_the_tokens():
+    """Four times the tokens take about four times as long, not sixteen."""
+    def time(T):
+        cache = sv.kv_cache(T // 16, 1, 16, 64)
+        table = torch.randperm(T // 16, device="cuda").to(torch.int32)[None]
+        lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+        k = torch.randn(1, T, 1, 64, device="cuda").bfloat16()
+        out = sv.kv_cache_write(k, k, cache, table, lens)
+        best = math.inf
+        for _ in range(10):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            sv.kv_cache_write(k, k, cache, table, lens, out=out)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+    assert time(1 << 19) < 7 * time(1 << 17)
