@@ -475,10 +475,12 @@ def _new(shape, dtype, device, stream):
     return t
 
 
-def _raw_stream(stream, device) -> int:
+def _raw_stream(stream, at) -> int:
     if stream is not None:
+        if stream.device_index != at:
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{at}")
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return torch._C._cuda_getCurrentRawStream(at)
 
 
 _round_ws = {}
@@ -518,41 +520,61 @@ def _strides(t, n):
     return (ctypes.c_int64 * n)(*[t.stride(i) if t.shape[i] > 1 else dense[i] for i in range(n)])
 
 
-def _not_cuda():
-    raise SpecVerifyError("inputs must be CUDA tensors (there is no CPU path)")
+def _not_at(t, at):
+    if t.get_device() < 0:
+        raise SpecVerifyError("the tensors of a call must be CUDA tensors (there is no CPU path)")
+    raise ValueError(f"a tensor is on cuda:{t.get_device()}, the others on cuda:{at}")
 
 
-def _arg(t, dtype, shape, what):
-    """The pointer of an optional argument: a contiguous CUDA tensor of this dtype and shape."""
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _at(t) -> int:
+    """The device of a call, which launches on the current one."""
+    at = t.get_device()
+    if at < 0:
+        _not_at(t, at)
+    if at != _current_device():
+        raise ValueError(f"the tensors are on cuda:{at}, the current device is cuda:{_current_device()}")
+    return at
+
+
+def _arg(t, dtype, shape, what, at):
+    """The pointer of an optional argument: a contiguous tensor of this dtype and shape on device `at`."""
     if t is None:
         return None
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-    if not t.is_cuda:
-        _not_cuda()
+    if t.get_device() != at:
+        _not_at(t, at)
     return t.data_ptr()
 
 
 _I32, _F32 = torch.int32, torch.float32
 
 
-def _cache_args(cache, page_table, lens, B):
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _cache_args(cache, page_table, lens, B, at):
     k, v, ks, vs = cache
     shape = k.shape
     if len(shape) != 4 or v.shape != shape or not (k.is_contiguous() and v.is_contiguous()):
         raise ValueError("the cache's codes must be contiguous [pages, heads, page_size, head_dim]")
-    if k.element_size() != 1 or v.element_size() != 1:
-        raise TypeError("the cache's codes must be e4m3 (one byte each)")
-    if not (k.is_cuda and v.is_cuda):
-        _not_cuda()
+    if k.dtype not in _CODES or v.dtype not in _CODES:
+        raise TypeError("the cache's codes must be float8_e4m3fn (or their bytes as uint8)")
+    for t in (k, v):
+        if t.get_device() != at:
+            _not_at(t, at)
     pages, heads, page, dim = shape
     if page_table is None or page_table.dim() != 2 or page_table.shape[0] != B or lens is None:
         raise ValueError(f"page_table must be [{B}, width], with lens [{B}]")
     width = page_table.shape[1]
     scales = (pages, heads)
     return (pages, heads, page, dim, width,
-            (k.data_ptr(), v.data_ptr(), _arg(ks, _F32, scales, "k_scale"), _arg(vs, _F32, scales, "v_scale")),
-            _arg(page_table, _I32, (B, width), "page_table"), _arg(lens, _I32, (B,), "lens"))
+            (k.data_ptr(), v.data_ptr(), _arg(ks, _F32, scales, "k_scale", at), _arg(vs, _F32, scales, "v_scale", at)),
+            _arg(page_table, _I32, (B, width), "page_table", at), _arg(lens, _I32, (B,), "lens", at))
 
 
 def process_logits(logits, *, tokens=None, parents=None, history=None, prompt_len=None, history_len=None,
@@ -569,8 +591,7 @@ def process_logits(logits, *, tokens=None, parents=None, history=None, prompt_le
     Returns that dict.
     """
     lib = load()
-    if not logits.is_cuda:
-        _not_cuda()
+    at = _at(logits)
     if logits.dim() != 3:
         raise ValueError("logits must be [B, R, V]")
     B, R, V = logits.shape
@@ -590,25 +611,27 @@ def process_logits(logits, *, tokens=None, parents=None, history=None, prompt_le
         out = {"logits": y, "row_status": _new(B, _I32, dev, stream)}
     else:
         y = out["logits"]
-        if y.shape != logits.shape or y.dtype is not logits.dtype or not y.is_cuda:
+        if y.shape != logits.shape or y.dtype is not logits.dtype:
             raise ValueError("out['logits'] must have the logits' shape and dtype")
+        if y.get_device() != at:
+            _not_at(y, at)
     if allowed is not None:
         W = (V + 31) // 32
-        if not allowed.is_cuda:
-            _not_cuda()
+        if allowed.get_device() != at:
+            _not_at(allowed, at)
         if tuple(allowed.shape) != (B, R, W) or allowed.element_size() != 4 or not allowed.is_contiguous():
             raise ValueError(f"allowed must be a contiguous 32-bit [B, R, {W}] tensor")
     one = (B,)
     rc = lib.process_logits(
         logits.data_ptr(), y.data_ptr(), dt, B, R, V, _strides(logits, 2), _strides(y, 2),
-        _arg(tokens, _I32, (B, N), "tokens") if N else None, _arg(parents, _I32, (B, N), "parents") if N else None, N,
-        _arg(history, _I32, (B, H), "history") if H else None, H, _arg(prompt_len, _I32, one, "prompt_len"),
-        _arg(history_len, _I32, one, "history_len"), _arg(repetition, _F32, one, "repetition"),
-        _arg(presence, _F32, one, "presence"), _arg(frequency, _F32, one, "frequency"),
-        _arg(bias_tokens, _I32, (B, nb), "bias_tokens") if nb else None,
-        _arg(bias_values, _F32, (B, nb), "bias_values") if nb else None, nb,
-        None if allowed is None else allowed.data_ptr(), _arg(out.get("row_status"), _I32, one, "row_status"),
-        _raw_stream(stream, dev))
+        _arg(tokens, _I32, (B, N), "tokens", at) if N else None, _arg(parents, _I32, (B, N), "parents", at) if N else None, N,
+        _arg(history, _I32, (B, H), "history", at) if H else None, H, _arg(prompt_len, _I32, one, "prompt_len", at),
+        _arg(history_len, _I32, one, "history_len", at), _arg(repetition, _F32, one, "repetition", at),
+        _arg(presence, _F32, one, "presence", at), _arg(frequency, _F32, one, "frequency", at),
+        _arg(bias_tokens, _I32, (B, nb), "bias_tokens", at) if nb else None,
+        _arg(bias_values, _F32, (B, nb), "bias_values", at) if nb else None, nb,
+        None if allowed is None else allowed.data_ptr(), _arg(out.get("row_status"), _I32, one, "row_status", at),
+        _raw_stream(stream, at))
     if rc:
         _check(rc)
     return out
@@ -623,14 +646,15 @@ def kv_cache_write(k, v, cache, page_table, lens, *, accepted_len=None, out_node
     all T rows are written.  Returns dict(lens, row_status): the lengths after the write.
     """
     lib = load()
-    if not (k.is_cuda and v.is_cuda):
-        _not_cuda()
+    at = _at(k)
+    if v.get_device() != at:
+        _not_at(v, at)
     if k.dim() != 4 or k.shape != v.shape or k.dtype is not v.dtype:
         raise ValueError("k and v must be [B, T, heads, head_dim] of one dtype")
     B, T, heads, dim = k.shape
     dev = k.device
     dt = _round_dtype(k.dtype, "k", (SPEC_F32, SPEC_BF16, SPEC_F16))
-    pages, h, page, d, width, ptrs, table, ln = _cache_args(cache, page_table, lens, B)
+    pages, h, page, d, width, ptrs, table, ln = _cache_args(cache, page_table, lens, B, at)
     if h != heads or d != dim:
         raise ValueError(f"the cache holds {h} heads of {d}, the rows {heads} of {dim}")
     if out_nodes is not None and accepted_len is None:
@@ -641,9 +665,9 @@ def kv_cache_write(k, v, cache, page_table, lens, *, accepted_len=None, out_node
     one = (B,)
     rc = lib.kv_cache_write(
         k.data_ptr(), _strides(k, 3), v.data_ptr(), _strides(v, 3), dt, B, T, heads, dim, *ptrs, pages, page, table, width,
-        ln, _arg(accepted_len, _I32, one, "accepted_len"),
-        _arg(out_nodes, _I32, (B, nw), "out_nodes") if nw else None, nw, _arg(out.get("lens"), _I32, one, "lens"),
-        _arg(out.get("row_status"), _I32, one, "row_status"), _raw_stream(stream, dev))
+        ln, _arg(accepted_len, _I32, one, "accepted_len", at),
+        _arg(out_nodes, _I32, (B, nw), "out_nodes", at) if nw else None, nw, _arg(out.get("lens"), _I32, one, "lens", at),
+        _arg(out.get("row_status"), _I32, one, "row_status", at), _raw_stream(stream, at))
     if rc:
         _check(rc)
     return out
@@ -654,7 +678,8 @@ def kv_cache_read(cache, page_table, lens, *, max_len: int, start=None, dtype=to
     head_dim], row_status).  Tokens past a request's length read as zero."""
     lib = load()
     B = lens.shape[0]
-    pages, heads, page, dim, width, ptrs, table, ln = _cache_args(cache, page_table, lens, B)
+    at = _at(cache[0])
+    pages, heads, page, dim, width, ptrs, table, ln = _cache_args(cache, page_table, lens, B, at)
     dev = cache[0].device
     shape = (B, max_len, heads, dim)
     if out is None:
@@ -663,9 +688,9 @@ def kv_cache_read(cache, page_table, lens, *, max_len: int, start=None, dtype=to
     y, z = out["k"], out["v"]
     dt = _round_dtype(y.dtype, "out", (SPEC_F32, SPEC_BF16, SPEC_F16))
     one = (B,)
-    rc = lib.kv_cache_read(*ptrs, pages, page, heads, dim, table, width, ln, _arg(start, _I32, one, "start"), B, max_len,
-                           _arg(y, y.dtype, shape, "out['k']"), _arg(z, y.dtype, shape, "out['v']"), dt,
-                           _arg(out.get("row_status"), _I32, one, "row_status"), _raw_stream(stream, dev))
+    rc = lib.kv_cache_read(*ptrs, pages, page, heads, dim, table, width, ln, _arg(start, _I32, one, "start", at), B, max_len,
+                           _arg(y, y.dtype, shape, "out['k']", at), _arg(z, y.dtype, shape, "out['v']", at), dt,
+                           _arg(out.get("row_status"), _I32, one, "row_status", at), _raw_stream(stream, at))
     if rc:
         _check(rc)
     return out
@@ -686,14 +711,13 @@ def verify_attention(q, cache, page_table, lens, *, k=None, v=None, parents=None
     with ``lse``, lse [B, T, Hq] in fp32).
     """
     lib = load()
-    if not q.is_cuda:
-        _not_cuda()
+    at = _at(q)
     if q.dim() != 4:
         raise ValueError("q must be [B, T, Hq, D]")
     B, T, hq, dim = q.shape
     dev = q.device
     dt = _round_dtype(q.dtype, "q", (SPEC_BF16, SPEC_F16))
-    pages, hkv, page, d, width, ptrs, table, ln = _cache_args(cache, page_table, lens, B)
+    pages, hkv, page, d, width, ptrs, table, ln = _cache_args(cache, page_table, lens, B, at)
     if d != dim or hq % hkv:
         raise ValueError(f"q has {hq} heads of {dim}, the cache {hkv} of {d}")
     if k is None and v is None:
@@ -703,8 +727,9 @@ def verify_attention(q, cache, page_table, lens, *, k=None, v=None, parents=None
     else:
         if k.shape != (B, T, hkv, dim) or v.shape != k.shape or k.dtype is not q.dtype or v.dtype is not q.dtype:
             raise ValueError("k and v must be [B, T, Hkv, D] of q's dtype")
-        if not (k.is_cuda and v.is_cuda):
-            _not_cuda()
+        for t in (k, v):
+            if t.get_device() != at:
+                _not_at(t, at)
         kp, vp, kst, vst = k.data_ptr(), v.data_ptr(), _strides(k, 3), _strides(v, 3)
     if out is None:
         out = {"out": _new(q.shape, q.dtype, dev, stream), "row_status": _new(B, _I32, dev, stream)}
@@ -713,17 +738,21 @@ def verify_attention(q, cache, page_table, lens, *, k=None, v=None, parents=None
     y = out["out"]
     if y.shape != q.shape or y.dtype is not q.dtype or not y.is_contiguous():
         raise ValueError("out['out'] must be contiguous, with q's shape and dtype")
+    if y.get_device() != at:
+        _not_at(y, at)
     key = (T, hq, hkv, dim)
     nbytes = _attn_bytes.get(key)
     if nbytes is None:
         nbytes = _attn_bytes[key] = int(lib.verify_attention_workspace_bytes(1, *key))
-    raw = _raw_stream(stream, dev)
+    raw = _raw_stream(stream, at)
     ws = _round_workspace(workspace, dev, stream, raw, max(nbytes, 256))
+    if ws.get_device() != at:
+        _not_at(ws, at)
     rc = lib.verify_attention(
         q.data_ptr(), _strides(q, 3), kp, kst, vp, vst, dt, B, T, hq, hkv, dim, *ptrs, pages, page, table, width, ln,
-        _arg(parents, _I32, (B, T - 1), "parents") if T > 1 else None, _arg(n_rows, _I32, (B,), "n_rows"),
-        dim ** -0.5 if scale is None else scale, y.data_ptr(), _arg(out.get("lse"), _F32, (B, T, hq), "lse"),
-        _arg(out.get("row_status"), _I32, (B,), "row_status"), ws.data_ptr(), ws.numel(), raw)
+        _arg(parents, _I32, (B, T - 1), "parents", at) if T > 1 else None, _arg(n_rows, _I32, (B,), "n_rows", at),
+        dim ** -0.5 if scale is None else scale, y.data_ptr(), _arg(out.get("lse"), _F32, (B, T, hq), "lse", at),
+        _arg(out.get("row_status"), _I32, (B,), "row_status", at), ws.data_ptr(), ws.numel(), raw)
     if rc:
         _check(rc)
     return out
