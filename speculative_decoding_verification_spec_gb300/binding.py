@@ -461,6 +461,9 @@ def kv_cache(pages: int, heads: int, page_size: int, head_dim: int, device="cuda
                    *(torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2)))
 
 
+# With `stream` a call runs there instead of on the current stream: the caller orders it after the work on its inputs, and keeps
+# them until it has run.
+#
 # A round's calls are short and many, so their marshalling avoids what costs microseconds: pointers go as plain ints,
 # dense tensors pass no strides, and the current stream's handle comes without a Stream object.
 
@@ -468,10 +471,13 @@ _EMPTY = torch.empty
 
 
 def _new(shape, dtype, device, stream):
-    """A new output, safe to be written on `stream` when that is not the current one."""
-    t = _EMPTY(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
+    """A new tensor for a call on `stream`.  It is allocated on that stream: a block freed on the current one may still be in
+    use there.  The current stream, where the caller goes on, is noted as its second user."""
+    if stream is None:
+        return _EMPTY(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = _EMPTY(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 

@@ -172,3 +172,59 @@ def test_write_time_grows_with_the_tokens():
             best = min(best, a.elapsed_time(b))
         return best
     assert time(1 << 19) < 7 * time(1 << 17)
+
+
+# ------------------------------------------------------------------ streams and captures
+
+def busy_block(nbytes, value):
+    """A block that the caching allocator hands out next on the current stream, while that still has to write `value` to it."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    x = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    torch.cuda._sleep(400_000_000)  # some 0.2 s
+    x.fill_(value)
+    return x.data_ptr()
+
+
+@pytest.mark.parametrize("what", ["attention", "logits", "write", "read"])
+def test_new_outputs_on_another_stream_are_the_calls_own(what):
+    """The current stream still has work on a block that was freed there; a call on another stream does not take it."""
+    g = torch.Generator().manual_seed(71)
+    p = Pool(g, [70, 130], 2, 32, 64, spare=5)
+    q, kn, vn = (x.cuda() for x in round_inputs(g, 2, 5, 4, 2, 64, "bf16"))
+    logits = torch.randn(2, 3, 400, generator=g).cuda()
+    tokens = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+    calls = dict(attention=lambda **kw: sv.verify_attention(q, p.cache, p.dtable, p.dlens, k=kn, v=vn, lse=True, **kw),
+                 logits=lambda **kw: sv.process_logits(logits, tokens=tokens, **kw),
+                 write=lambda **kw: sv.kv_cache_write(kn, vn, p.cache, p.dtable, p.dlens, **kw),
+                 read=lambda **kw: sv.kv_cache_read(p.cache, p.dtable, p.dlens, max_len=90, dtype=torch.float32, **kw))
+    call = calls[what]
+    want = call()
+    st = torch.cuda.Stream()
+    call(stream=st)  # its workspace is there from now on
+    for name, t in want.items():
+        busy_block(t.numel() * t.element_size(), 77)
+        got = call(stream=st)
+        torch.cuda.synchronize()
+        for n in want:
+            assert torch.equal(got[n], want[n]), (name, n)
+
+
+def test_a_new_workspace_on_another_stream_is_the_calls_own():
+    g = torch.Generator().manual_seed(72)
+    p = Pool(g, [3000, 130], 2, 32, 64)
+    q, kn, vn = (x.cuda() for x in round_inputs(g, 2, 5, 4, 2, 64, "bf16"))
+    call = lambda **kw: sv.verify_attention(q, p.cache, p.dtable, p.dlens, k=kn, v=vn, lse=True, **kw)
+    out = {n: torch.empty_like(t) for n, t in call().items()}
+    n = B_.load().verify_attention_workspace_bytes(2, 5, 4, 2, 64)
+    old = dict(B_._round_ws)
+    B_._round_ws.clear()
+    try:
+        st = torch.cuda.Stream()
+        at = busy_block(n, 77)
+        call(stream=st, out=out)
+        (buf,) = B_._round_ws.values()
+        assert buf.data_ptr() + buf.numel() <= at or at + n <= buf.data_ptr()
+        torch.cuda.synchronize()
+    finally:
+        B_._round_ws.update(old)
