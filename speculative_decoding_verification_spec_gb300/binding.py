@@ -489,13 +489,24 @@ def _raw_stream(stream, at) -> int:
     return torch._C._cuda_getCurrentRawStream(at)
 
 
+def _capturing(stream) -> bool:
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 _round_ws = {}
 
 
 def _round_workspace(ws, device, stream, raw, nbytes):
-    """The call's workspace; by default one per device and stream, as calls on two streams may overlap."""
+    """The call's workspace; by default one per device and stream, as calls on two streams may overlap.  A captured call has one
+    of its own, from its graph's memory: graphs captured on one stream may be replayed on two, and a kept workspace may be
+    replaced by a larger one."""
     if ws is not None:
         return ws.get(nbytes)
+    if _capturing(stream):
+        return _new(nbytes, torch.uint8, device, stream)
     key = (device, raw)
     buf = _round_ws.get(key)
     if buf is None or buf.numel() < nbytes:

@@ -228,3 +228,95 @@ def test_a_new_workspace_on_another_stream_is_the_calls_own():
         torch.cuda.synchronize()
     finally:
         B_._round_ws.update(old)
+
+
+class Spy:
+    """The library, noting the workspace of every verify_attention."""
+
+    def __init__(self, lib):
+        self.lib, self.seen = lib, []
+
+    def __getattr__(self, name):
+        f = getattr(self.lib, name)
+        if name != "verify_attention":
+            return f
+
+        def call(*a):
+            self.seen.append((a[-3], a[-2]))
+            return f(*a)
+        return call
+
+
+@pytest.mark.parametrize("T,hq,other", [(3, 8, False), (6, 16, False), (6, 16, True)])
+def test_captured_attention_has_a_workspace_of_its_own(monkeypatch, T, hq, other):
+    """Two graphs captured without a workspace, replayed at the same time on two streams while eager calls run."""
+    g = torch.Generator().manual_seed(73)
+    spy = Spy(B_.load())
+    monkeypatch.setattr(B_, "load", lambda *a: spy)
+    cases, graphs = [], []
+    for seed in range(2):
+        p = Pool(g, [5000 + 900 * seed, 100], 2, 64, 128)
+        q, kn, vn = (x.cuda() for x in round_inputs(g, 2, T, hq, 2, 128, "bf16"))
+        cases.append(lambda p=p, q=q, kn=kn, vn=vn, **kw: sv.verify_attention(q, p.cache, p.dtable, p.dlens, k=kn, v=vn, lse=True, **kw))
+    want = [c() for c in cases]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for c in cases:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            if other:  # a branch of the capture
+                side.wait_stream(torch.cuda.current_stream())
+                r = c(stream=side)
+                torch.cuda.current_stream().wait_stream(side)
+            else:
+                r = c()
+        graphs.append((graph, r))
+    eager, a, b = ((x, x + n) for x, n in spy.seen[1:4])
+    for x, y in ((eager, a), (eager, b), (a, b)):
+        assert x[1] <= y[0] or y[1] <= x[0], spy.seen
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for st, (graph, r) in zip(streams, graphs):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                for t in r.values():
+                    t.zero_()
+                graph.replay()
+        now = [c() for c in cases]
+        torch.cuda.synchronize()
+        for w, (_, r), e in zip(want, graphs, now):
+            for n in w:
+                assert torch.equal(r[n], w[n]) and torch.equal(e[n], w[n]), n
+
+
+def test_a_larger_workspace_leaves_captured_calls_alone():
+    """64 channels captured, then 128 channels eagerly on the same stream, whose workspace is larger."""
+    g = torch.Generator().manual_seed(74)
+    st = torch.cuda.Stream()
+    calls = []
+    for D in (64, 128):
+        p = Pool(g, [4000, 100], 2, 64, D)
+        q, kn, vn = (x.cuda() for x in round_inputs(g, 2, 6, 16, 2, D, "bf16"))
+        calls.append(lambda p=p, q=q, kn=kn, vn=vn, **kw: sv.verify_attention(q, p.cache, p.dtable, p.dlens, k=kn, v=vn, lse=True, **kw))
+    want = calls[0]()
+    old = dict(B_._round_ws)
+    B_._round_ws.clear()
+    try:
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            calls[0]()
+            graph = torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph, stream=st):
+                r = calls[0]()
+            calls[1]()
+            torch.cuda.synchronize()
+            n = B_.load().verify_attention_workspace_bytes(2, 6, 16, 2, 64)
+            held = torch.full((n,), 0x7f, dtype=torch.uint8, device="cuda")  # takes what the smaller one left
+            graph.replay()
+            torch.cuda.synchronize()
+            assert bool((held == 0x7f).all())
+        for n in want:
+            assert torch.equal(r[n], want[n]), n
+    finally:
+        B_._round_ws.update(old)
