@@ -691,7 +691,8 @@ cudaError_t launch_rows(AttnParams& P, int sms, cudaStream_t st)
     const size_t smem = (size_t)AW * ASTAGES * 2 * SLICE * D;
     static_assert((size_t)AW * ASTAGES * 2 * SLICE * D >= (size_t)AW * MR * D * 4, "the ring holds the warps' sums");
     auto* k = attn_rows_kernel<DT, D>;
-    static int per_sm = 0;
+    static PerDevice kept;
+    int& per_sm = kept.here();
     if (per_sm == 0) {
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;

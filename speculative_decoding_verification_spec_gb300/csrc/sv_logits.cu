@@ -409,7 +409,8 @@ cudaError_t launch_chunks(LogitsParams& P, int sms, cudaStream_t st)
     const auto smem = [&](int chunk) {
         return ((size_t)chunk + 32 + (chunk + 32) / 32 + P.N) * 4 + ((size_t)chunk + 32 + P.N + P.nb + 1) / 2 * 4;
     };
-    static int per_sm = 0;  // CTAs that the registers allow
+    static PerDevice kept;
+    int& per_sm = kept.here();  // CTAs that the registers allow
     if (per_sm == 0) {
         cudaFuncAttributes a;
         const cudaError_t e = cudaFuncGetAttributes(&a, K);

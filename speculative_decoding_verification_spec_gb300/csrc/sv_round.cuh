@@ -23,6 +23,18 @@ enum { ROW_BAD_PAGE = 9, ROW_BAD_LENGTH = 10, ROW_BAD_NODE = 11 };
 constexpr int CACHE_E_MIN = -60, CACHE_E_MAX = 60;  // a scale's exponent
 constexpr float CACHE_MAX_CODE = 448.0f;            // the largest e4m3 value
 
+// What a launcher keeps for each device (0: nothing yet): attributes of a kernel belong to the device that was current when they
+// were set.  On a device past the last slot it is found anew by every call.
+struct PerDevice {
+    int slot[65] = {0};
+    int& here()
+    {
+        int dev = 64;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) slot[dev = 64] = 0;
+        return slot[dev];
+    }
+};
+
 // 2^e for a normal result
 __host__ __device__ __forceinline__ float exp2_int(int e)
 {

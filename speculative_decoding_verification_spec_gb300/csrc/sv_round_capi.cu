@@ -11,15 +11,12 @@ namespace sv {
 
 static int round_sm_count()
 {
-    static int cache[64] = {0};
+    static PerDevice cache;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-    if (cache[dev] == 0) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
-        cache[dev] = n;
-    }
-    return cache[dev];
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    int& n = cache.here();
+    if (n == 0 && (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)) n = 152;
+    return n;
 }
 
 static bool on(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
