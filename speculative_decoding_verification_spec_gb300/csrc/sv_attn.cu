@@ -131,14 +131,14 @@ __device__ __forceinline__ void slice_step(RowState<D>& S, const uint32_t (&qf)[
                 }
             }
             const float ref = m == NEG_INF ? 0.0f : m;
-            float p[2][2];
+            float p[2][2], l[2];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+            for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    p[nt][j] = ex2(u[nt][j] - ref);
-                    S.l[mt][hi] = fmaf(p[nt][j], l_scale(nt, j), S.l[mt][hi]);
-                }
+                for (int j = 0; j < 2; ++j) p[nt][j] = ex2(u[nt][j] - ref);
+                l[nt] = fmaf(p[nt][0], l_scale(nt, 0), p[nt][1] * l_scale(nt, 1));
+            }
+            S.l[mt][hi] += l[0] + l[1];  // one rounding a slice beside a large sum, where small weights may be many
             pf[mt][hi] = pack_half2(p[0][0], p[0][1]);
             pf[mt][2 + hi] = pack_half2(p[1][0], p[1][1]);
         }

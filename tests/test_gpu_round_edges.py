@@ -130,6 +130,34 @@ def test_attention_huge_scores(T, hq, dtype, e):
     assert clear >= T * hq
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,hq", [(1, 4)])
+def test_attention_small_weights_beside_a_large_one(T, hq, dtype):
+    """One token holds nearly all of the weight and a value near zero, 32767 others share the rest and make the output."""
+    D, page, n = 128, 64, 32768
+    g = torch.Generator().manual_seed(43)
+    p = Pool(g, [n], 1, page, D)
+    for which, (one, rest) in enumerate(((1.5, 0.125), (2.0 ** -9, 1.0))):
+        p.codes[which] = torch.full(p.codes[which].shape, rest).to(R.FP8)
+        p.codes[which][int(p.table[0, 0]), 0, 0] = torch.full((D,), one).to(R.FP8)
+        p.scales[which].fill_(1.0)
+        p.cache[which].view(torch.uint8).copy_(p.codes[which].view(torch.uint8).cuda())
+        p.cache[2 + which].copy_(p.scales[which])
+    q = (1.0 - 2.0 ** -8 * (torch.arange(T * hq) % 8).view(1, T, hq, 1)).expand(1, T, hq, D).to(DT[dtype])
+    copies(p, 320)
+    r = run_attention(p, q.repeat(320, 1, 1, 1), None, None)
+    kc, vc = p.line(0, 0), p.line(1, 0)
+    out, lse, absv, seen, size = R.attention_ref(q[0], kc, vc, None, None, None, T, D ** -0.5)
+    assert float(out.max()) < 0.05 and bool((out > 0.003).all())
+    # weights: 2^-11 of each, or 2^-32 of the largest; sums of n tokens, 16 a step, and two scores that fp32 holds but for their last
+    # places: 2^-11; the output's own rounding
+    tol = n * 2.0 ** -32 + (2 * 2.0 ** -11 + torch.finfo(q.dtype).eps / 2) * out
+    for b in range(320):
+        err = (r["out"][b].double() - out).abs()
+        assert bool((err <= tol).all()), (b, float((err / out).max()), float((tol / out).min()))
+        assert bool(((r["lse"][b].double() - lse).abs() <= 2.0 ** -14).all())
+
+
 # ------------------------------------------------------------------ long prompts
 
 @pytest.mark.parametrize("T,page,D,accepted", [(17000, 16, 64, [16999, 9001, -1]), (33000, 32, 128, None)])
