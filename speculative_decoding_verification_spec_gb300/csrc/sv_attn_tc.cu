@@ -9,7 +9,7 @@
 //       most 2^-17 of it below) and three for halfs, whose products accumulate.
 //   O^T [D, rows] += V^T [D, 128] P^T:   halfs; six warps widen the codes of V into shared memory, and the weights are
 //       rounded to halfs (half a step, 2^-11, under the output's own rounding; a weight below 2^-14 is off by 2^-25
-//       absolute, 2^-28 of the row's largest, as HEAD says).
+//       absolute, 2^-32 of the row's largest, as HEAD says).
 // The round's own rows come last, as tiles of their own: keys and values as halfs scaled by a power of two per token, and a
 // copy of q as halfs.
 //
@@ -20,7 +20,7 @@
 //   2 - 7  values: the next tile's codes from L2 into registers while this tile's are widened into shared memory
 //   8 - 15 softmax, two groups of four warps; a thread is a token, a group takes half of the columns.  The sums l stay in
 //          tensor memory beside S^T and O^T, one per token lane and column, so a thread holds 16 columns at a time.  The
-//          weights are taken against the reference as it stands; only when one passes 2^15 (the first tile of a group, and
+//          weights are taken against the reference as it stands; only when one passes 2^15.9 (the first tile of a group, and
 //          rarely after) does the group find the columns' maxima, move the reference, rescale its part of O^T and l and
 //          repeat the tile.
 // What bounds it: neither memory nor the tensor cores, but the chain that each tile goes through (S^T, softmax, P, O^T): some
@@ -49,11 +49,13 @@ constexpr int TNT = (SMW0 + 4 * NG) * 32;
 constexpr int MAXR = 128;        // rows of a group: S^T twice, O^T and the sums l take four times as many columns
 constexpr int MAXC = (MAXR / 16 + NG - 1) / NG * 16;  // columns of a softmax group
 constexpr int MAXSTAGES = 6;
-constexpr float WINDOW = 15.0f;  // a weight may reach 2^WINDOW (the largest half is near 2^16)
-constexpr float HEAD = 3.0f;     // a moved reference leaves the maximum at 2^HEAD: a move repeats a tile, so the room above
-                                 // is kept large; a weight 2^-28 of the largest is then the least that a half still holds
-constexpr float LATE = 5.0f;     // where a move is due, columns past 2^LATE move with it: later repeats are fewer (B = 32, T = 65:
-                                 // 362 us, 386 with 14; T = 6, eight query heads a head: 169 and 187).  Under WINDOW by more than the
+constexpr float WINDOW = 15.9f;  // a weight may reach 2^WINDOW (the largest half is just under 2^16)
+constexpr float HEAD = 7.0f;     // a moved reference leaves the maximum at 2^HEAD, so a weight 2^-32 of the largest is the least that a
+                                 // half still holds, as on the few-rows path.  More room above means fewer repeated tiles: with 3
+                                 // (and 2^-28) B = 32, T = 6, T = 65 and eight query heads a head took 134, 362 and 169 us, with 7
+                                 // 137, 384 and 186; but a row whose weight lies on one token loses a percent of the others
+constexpr float LATE = 7.0f;     // where a move is due, columns past 2^LATE move with it: later repeats are fewer (B = 32, T = 65:
+                                 // 384 us, 417 with 11; T = 6, eight query heads a head: 186 and 209).  Under WINDOW by more than the
                                  // two passes' roundings differ, so that a weight past it does move
 constexpr float HOLD = 14.0f;    // where a weight is put that no reference brings under the window
 constexpr size_t TC_SMEM = 214 * 1024;  // dynamic shared memory; the static arrays take the rest of the SM's 227 KB

@@ -131,7 +131,7 @@ def test_attention_huge_scores(T, hq, dtype, e):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("T,hq", [(1, 4)])
+@pytest.mark.parametrize("T,hq", [(1, 4), (4, 16)])
 def test_attention_small_weights_beside_a_large_one(T, hq, dtype):
     """One token holds nearly all of the weight and a value near zero, 32767 others share the rest and make the output."""
     D, page, n = 128, 64, 32768
