@@ -107,7 +107,7 @@ __device__ __forceinline__ uint4 masked_vec(uint4 w, uint32_t ok)
 // what a CTA knows of its request and run
 struct Run {
     int b, v0, ndraft, nbias;
-    float rep, inv_rep, pres, freq;
+    float rep, pres, freq;
     const uint32_t* words;
     const uint16_t* draft;
     const uint16_t* bias;
@@ -116,11 +116,10 @@ struct Run {
     const uint64_t* row_path;  // which of them lie on each row's path
 };
 
-// the penalties of an entry that was generated c times; the division is a product with the reciprocal: one more
-// fp32 rounding
+// the penalties of an entry that was generated c times
 __device__ __forceinline__ float penalised(const Run& q, float x, int c, bool seen)
 {
-    if (c > 0 || seen) x = x > 0.0f ? x * q.inv_rep : x * q.rep;
+    if (c > 0 || seen) x = x > 0.0f ? x / q.rep : x * q.rep;
     if (c > 0) x -= fmaf(q.freq, (float)c, q.pres);
     return x;
 }
@@ -369,7 +368,6 @@ __global__ void __launch_bounds__(NT, 5) process_logits_kernel(LogitsParams P)
     q.same = masks ? same : nullptr;
     q.row_path = row_path;
     q.rep = P.repetition ? __ldg(P.repetition + b) : 1.0f;
-    q.inv_rep = 1.0f / q.rep;
     q.pres = P.presence ? __ldg(P.presence + b) : 0.0f;
     q.freq = P.frequency ? __ldg(P.frequency + b) : 0.0f;
     const int touched_n = nlist;

@@ -348,3 +348,25 @@ def test_a_larger_workspace_leaves_captured_calls_alone():
             assert torch.equal(r[n], want[n]), n
     finally:
         B_._round_ws.update(old)
+
+
+# ------------------------------------------------------------------ logits
+
+@pytest.mark.parametrize("rep", [1.3, 0.7, 1.1754944e-38, 1e-40, 2.9387359e-39, 3e38])
+def test_logits_are_divided_by_the_repetition_penalty(rep):
+    """The quotient rounded once, also where the reciprocal is no normal number."""
+    g = torch.Generator().manual_seed(81)
+    V = 4099
+    x = torch.randn(1, 2, V, generator=g) * torch.exp2(torch.randint(-60, 4, (V,), generator=g).float())
+    hist = torch.randperm(V, generator=g).to(torch.int32)[None, :4000].contiguous()
+    r = torch.tensor([rep])
+    y = sv.process_logits(x.cuda(), tokens=torch.zeros(1, 1, dtype=torch.int32, device="cuda"), history=hist.cuda(),
+                          repetition=r.cuda())["logits"].cpu()
+    hit = torch.zeros(V, dtype=torch.bool)
+    hit[hist[0].long()] = True
+    for row in range(2):
+        seen = hit.clone()
+        if row:
+            seen[0] = True
+        want = torch.where(seen, torch.where(x[0, row] > 0, x[0, row] / r, x[0, row] * r), x[0, row])
+        assert torch.equal(y[0, row], want)
