@@ -658,7 +658,7 @@ def kv_cache_write(k, v, cache, page_table, lens, *, accepted_len=None, out_node
     """Appends rows to the requests' 8-bit caches, one scale per page and head.
 
     k, v [B, T, Hkv, D] (fp32, bf16 or fp16; any strides but the last), ``cache`` a KVCache (written in place),
-    page_table [B, width] and lens [B] int32.  ``accepted_len`` [B] and ``out_nodes`` [B, >= T-1], as a verify call
+    page_table [B, width] and lens [B] int32.  ``accepted_len`` [B] and ``out_nodes`` [B, width], as a verify call
     returns them, choose the rows: 0 .. accepted_len, or row 0 and the accepted path's nodes; without them
     all T rows are written.  Returns dict(lens, row_status): the lengths after the write.
     """
@@ -680,10 +680,12 @@ def kv_cache_write(k, v, cache, page_table, lens, *, accepted_len=None, out_node
     if out is None:
         out = {"lens": _new(B, _I32, dev, stream), "row_status": _new(B, _I32, dev, stream)}
     one = (B,)
+    acc, nodes = _arg(accepted_len, _I32, one, "accepted_len", at), _arg(out_nodes, _I32, (B, nw), "out_nodes", at)
+    if out_nodes is not None and not nw:
+        nodes = acc  # no node is read; a null pointer would say that the rows are a chain's
     rc = lib.kv_cache_write(
         k.data_ptr(), _strides(k, 3), v.data_ptr(), _strides(v, 3), dt, B, T, heads, dim, *ptrs, pages, page, table, width,
-        ln, _arg(accepted_len, _I32, one, "accepted_len", at),
-        _arg(out_nodes, _I32, (B, nw), "out_nodes", at) if nw else None, nw, _arg(out.get("lens"), _I32, one, "lens", at),
+        ln, acc, nodes, nw, _arg(out.get("lens"), _I32, one, "lens", at),
         _arg(out.get("row_status"), _I32, one, "row_status", at), _raw_stream(stream, at))
     if rc:
         _check(rc)

@@ -202,6 +202,16 @@ def test_write_time_grows_with_the_tokens():
     assert time(1 << 19) < 7 * time(1 << 17)
 
 
+def test_write_of_a_path_without_room_for_nodes():
+    """A tree call with room for one token gives out_nodes of width 0: row 0 may be written, and nothing that a path would name."""
+    g = torch.Generator().manual_seed(63)
+    T = 4
+    p = Pool(g, [3, 5, 17], 2, 16, 64, spare=T)
+    k, v = (torch.randn(3, T, 2, 64, generator=g).bfloat16().cuda() for _ in range(2))
+    r = check_write(p, k, v, [0, 2, -1], torch.empty(3, 0, dtype=torch.int32), bad=(1,))
+    assert r["row_status"].tolist() == [0, B_.ROW_BAD_LENGTH, 0]
+
+
 # ------------------------------------------------------------------ streams and captures
 
 def busy_block(nbytes, value):
