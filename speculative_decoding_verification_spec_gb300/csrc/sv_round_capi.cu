@@ -235,7 +235,7 @@ spec_status verify_attention(const void* q, const int64_t* q_strides, const void
     P.vs = v_scale;
     P.page_table = page_table;
     P.lens = lens;
-    P.parents = T > 1 ? parents : nullptr;
+    P.parents = T > 1 && k ? parents : nullptr;  // of rows that are there
     P.n_rows = n_rows;
     P.out = out;
     P.lse = lse;

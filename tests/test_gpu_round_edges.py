@@ -19,6 +19,19 @@ def copies(p, n):
     p.dtable, p.dlens = p.dtable.repeat(n, 1), p.dlens.repeat(n)
 
 
+# ------------------------------------------------------------------ both kernels, T hq / hkv up to 16 and more
+
+@pytest.mark.parametrize("T,hq", [(3, 4), (9, 8)])
+def test_attention_without_rows_of_the_round_has_no_use_for_parents(T, hq):
+    g = torch.Generator().manual_seed(40)
+    p = Pool(g, [0, 40], 2, 16, 64)
+    q, _, _ = round_inputs(g, 2, T, hq, 2, 64, "bf16")
+    want = run_attention(p, q, None, None)
+    r = run_attention(p, q, None, None, parents=torch.full((2, T - 1), 9, dtype=torch.int32))
+    assert r["row_status"].tolist() == [0, 0]
+    assert all(torch.equal(r[n], want[n]) for n in r)
+
+
 # ------------------------------------------------------------------ waits that run out
 
 @pytest.mark.parametrize("T,hq,hkv,lens", [(6, 16, 4, [900, 3, 0, 2100]), (40, 8, 8, [600] * 24), (6, 32, 8, [70] * 90)])
