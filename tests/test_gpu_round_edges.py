@@ -32,6 +32,134 @@ def test_attention_without_rows_of_the_round_has_no_use_for_parents(T, hq):
     assert all(torch.equal(r[n], want[n]) for n in r)
 
 
+BOTH = [(1, 8, 2), (3, 8, 2), (5, 8, 2), (9, 16, 2)]
+
+
+@pytest.mark.parametrize("T,hq,hkv", BOTH)
+def test_attention_bad_requests_on_both_paths(T, hq, hkv):
+    """A bad page in the middle and at the end of a context whose parts are joined, a bad length, a bad parent."""
+    g = torch.Generator().manual_seed(44)
+    lens = [9001, 40, 64, 10, 4097, 9001]
+    p = Pool(g, lens, hkv, 16, 128)
+    q, kn, vn = round_inputs(g, len(lens), T, hq, hkv, 128, "bf16")
+    p.dtable[0, 300] = -1
+    p.dtable[4, 256] = p.codes[0].shape[0]
+    p.dlens[2] = -1
+    bad = {0: B_.ROW_BAD_PAGE, 2: B_.ROW_BAD_LENGTH, 4: B_.ROW_BAD_PAGE}
+    parents = None
+    if T > 2:
+        parents = torch.stack([R.random_parents(g, T - 1) for _ in lens])
+        parents[3, T - 2] = T - 2
+        parents[5, 1] = -2
+        bad.update({3: B_.ROW_BAD_PARENT, 5: B_.ROW_BAD_PARENT})
+    r = check_attention(p, q, kn, vn, parents, skip=tuple(bad))
+    assert r["row_status"].tolist() == [bad.get(b, 0) for b in range(len(lens))]
+    for b in bad:
+        assert bool(r["out"][b].isnan().all()) and bool(r["lse"][b].isnan().all())
+
+
+@pytest.mark.parametrize("lens", [[0, 33], [5000, 9]])
+@pytest.mark.parametrize("T,hq", [(8, 4), (8, 8)])
+def test_attention_unseen_values_on_both_paths(T, hq, lens):
+    """NaN and infinities in rows that a row does not see, in the cache and in q."""
+    g = torch.Generator().manual_seed(45)
+    p = Pool(g, lens, 2, 16, 64)
+    q, kn, vn = round_inputs(g, 2, T, hq, 2, 64, "bf16")
+    parents = torch.full((2, T - 1), -1, dtype=torch.int32)  # every node a child of the frontier
+    clean = run_attention(p, q, kn, vn, parents)
+    k2, v2 = kn.clone(), vn.clone()
+    k2[:, 3], v2[:, 3] = math.nan, math.inf
+    v2[:, 5, 0, 3] = math.nan
+    v2[:, 6, 1, 60] = -math.inf
+    r = run_attention(p, q, k2, v2, parents)
+    for t in range(T):
+        if t not in (3, 5, 6):
+            assert torch.equal(r["out"][:, t], clean["out"][:, t]) and torch.equal(r["lse"][:, t], clean["lse"][:, t])
+    G = hq // 2
+    assert bool(r["out"][:, 3].isnan().all()) and bool(r["lse"][:, 3].isnan().all())
+    assert bool(r["out"][:, 5, :G, 3].isnan().all()) and torch.equal(r["out"][:, 5, G:], clean["out"][:, 5, G:])
+    assert bool(torch.isneginf(r["out"][:, 6, G:, 60]).all()) and torch.equal(r["out"][:, 6, :G], clean["out"][:, 6, :G])
+    b = lens.index(min(x for x in lens if x > 0))
+    p.cache.v.view(torch.uint8)[int(p.table[b, 0]), 1, 2, 9] = 0x7F
+    r = run_attention(p, q, kn, vn, parents)
+    assert bool(r["out"][b, :, G:, 9].isnan().all()) and not bool(r["out"][b, :, :G].isnan().any())
+    assert torch.equal(r["out"][1 - b], clean["out"][1 - b])
+    q2 = q.clone()
+    q2[1, 2, 1, 0] = math.inf
+    q2[0, 1, 0, 7] = math.nan
+    p.cache.v.view(torch.uint8)[int(p.table[b, 0]), 1, 2, 9] = 0
+    p.codes[1].view(torch.uint8)[int(p.table[b, 0]), 1, 2, 9] = 0
+    r, want = run_attention(p, q2, kn, vn, parents), run_attention(p, q, kn, vn, parents)
+    assert bool(r["out"][1, 2, 1].isnan().all()) and bool(r["out"][0, 1, 0].isnan().all())
+    gone = r["lse"].isnan()
+    assert int(gone.sum()) == 2 and torch.equal(r["out"][~gone], want["out"][~gone])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,hq,hkv,D", [(2, 8, 2, 64), (9, 8, 2, 64), (9, 8, 2, 128), (70, 4, 1, 128)])
+def test_attention_unaligned_rows_on_both_paths(T, hq, hkv, D, dtype):
+    """q, k and v cut out of one buffer at odd offsets, with row strides that allow no wide load."""
+    g = torch.Generator().manual_seed(46)
+    p = Pool(g, [100, 3], hkv, 32, D)
+    qkv = torch.randn(2, T, (hq + 2 * hkv) * D + 3, generator=g).to(DT[dtype]).cuda()
+    cut = lambda at, h: qkv[..., at:at + h * D].unflatten(-1, (h, D))
+    q, kn, vn = cut(1, hq), cut(1 + hq * D, hkv), cut(3 + (hq + hkv) * D, hkv)
+    assert not q.is_contiguous() and q.data_ptr() % 4 and vn.data_ptr() % 4
+    check_attention(p, q.cpu(), kn.cpu(), vn.cpu())
+    dense = sv.verify_attention(q.contiguous(), p.cache, p.dtable, p.dlens, k=kn.contiguous(), v=vn.contiguous(), lse=True)
+    r = sv.verify_attention(q, p.cache, p.dtable, p.dlens, k=kn, v=vn, lse=True)
+    assert all(torch.equal(r[n], dense[n]) for n in r)
+    # heads before rows, and one batch stride for all
+    qt, kt, vt = (x.contiguous().transpose(1, 2).contiguous().transpose(1, 2) for x in (q, kn, vn))
+    r = sv.verify_attention(qt, p.cache, p.dtable, p.dlens, k=kt, v=vt, lse=True)
+    assert all(torch.equal(r[n], dense[n]) for n in r)
+    one = [x[:1].expand(2, *x.shape[1:]) for x in (q, kn, vn)]
+    r = sv.verify_attention(one[0], p.cache, p.dtable, p.dlens, k=one[1], v=one[2], lse=True)
+    assert all(torch.equal(r[n][0], dense[n][0]) for n in ("out", "lse"))
+
+
+@pytest.mark.parametrize("T,hq,hkv,D", [(4, 8, 2, 64), (17, 8, 2, 64), (65, 8, 2, 128), (130, 4, 2, 64)])
+def test_attention_tree_f16(T, hq, hkv, D):
+    g = torch.Generator().manual_seed(T)
+    p = Pool(g, [0, 5, 300], hkv, 32, D)
+    q, kn, vn = round_inputs(g, 3, T, hq, hkv, D, "f16")
+    parents = torch.stack([R.random_parents(g, T - 1) for _ in range(3)])
+    check_attention(p, q, kn, vn, parents)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,hq", [(3, 4), (9, 4), (20, 6)])
+def test_attention_scales_far_apart(T, hq, dtype):
+    """Pages whose values differ by 2^40 in scale, the heavy tokens on those with the smallest: what a weight may be off by is counted
+    against the largest p 2^e of the row, not against the largest value."""
+    g = torch.Generator().manual_seed(47)
+    D, page, n = 64, 16, 640
+    p = Pool(g, [n], 1, page, D)
+    e = torch.zeros(n)
+    for j in range(n // page):
+        i = int(p.table[0, j])
+        p.scales[1][i] = 2.0 ** (-30 + 10 * (j % 5))
+        p.scales[0][i] = 2.0 ** (-4 if j % 5 == 0 else -6)
+        e[j * page:(j + 1) * page] = -30 + 10 * (j % 5)
+    p.cache.k_scale.copy_(p.scales[0])
+    p.cache.v_scale.copy_(p.scales[1])
+    q, _, _ = round_inputs(g, 1, T, hq, 1, D, dtype)
+    copies(p, 320)
+    r = run_attention(p, q.repeat(320, 1, 1, 1), None, None)
+    kc, vc = p.line(0, 0), p.line(1, 0)
+    out, lse, absv, seen, size = R.attention_ref(q[0], kc, vc, None, None, None, T, D ** -0.5)
+    w = torch.exp(torch.einsum("thd,jd->thj", q[0].double(), kc[:, 0]) * D ** -0.5 - lse[..., None])
+    top = (w * torch.exp2(e.double())).amax(-1, keepdim=True)
+    tol, tl = R.attention_tolerance(out, lse, absv, seen, size, 0.0, D, q.dtype)
+    tol = tol + n * 2.0 ** -32 * top * 448
+    if dtype == "f16":
+        assert float(out.abs().max()) < 60000
+    for b in range(320):
+        err = (r["out"][b].double() - out).abs()
+        assert bool((err <= tol).all()), (b, float((err / tol).max()))
+        assert bool(((r["lse"][b].double() - lse).abs() <= tl).all()), b
+
+
 # ------------------------------------------------------------------ waits that run out
 
 @pytest.mark.parametrize("T,hq,hkv,lens", [(6, 16, 4, [900, 3, 0, 2100]), (40, 8, 8, [600] * 24), (6, 32, 8, [70] * 90)])
