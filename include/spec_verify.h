@@ -498,8 +498,13 @@ size_t verify_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
  *   ancestors of row t and row t itself
  *   out [B, T, Hq, D] = sum_j softmax(s)_j v_j, dense, 16-byte aligned;  lse [B, T, Hq] (nullable, fp32) = log sum_j exp(s_j)
  * A row that sees nothing gives zeros and -inf.  What a row does not see has no effect on it, whatever it
- * holds.  Scores, softmax and sums are fp32; out is rounded once.  A row of q that holds a NaN or an infinity gives
- * NaN, and so does a key of the round that does, for the rows that see it.
+ * holds.  A row of q that holds a NaN or an infinity gives NaN, and so does a key of the round that does, for the rows
+ * that see it.
+ * Precision: scores, the softmax's references and all sums are fp32; codes are exact.  An element of q enters the
+ * scores to 2^-17 of its row's largest (bf16 elements over 2^-10 of that are exact, fp16 ones over 2^-6; with up to 16 rows a
+ * key/value head to 2^-39 of it), an element of the round's k and v to 2^-39 of its row's largest.  For the product with
+ * the values a weight p_j 2^(e_j), 2^(e_j) the scale of v_j, is rounded to a half: 2^-11 of itself, or 2^-32 of the row's
+ * largest; lse and the denominator take it unrounded.  The quotient is formed in fp32 and rounded to out's type.
  * row_status [B] (nullable): SPEC_ROW_BAD_LENGTH, BAD_PAGE, BAD_PARENT: the request's out and lse are NaN.
  * SPEC_ROW_TIMEOUT where more than 16 rows share a key/value head (T Hq / Hkv; that path waits on mbarriers): what the wait
  * that ran out kept from being computed, of any head, is NaN.

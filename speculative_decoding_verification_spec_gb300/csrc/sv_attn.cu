@@ -13,8 +13,8 @@
 // u, and sums p'_j = 2^(u_j - m):
 //   o = (sum_j p'_j c_j) / (sum_j p'_j 2^(-e_j)),   c_j the codes of v_j,
 // so pages with different scales need no second scaling of the sums.  p' <= 2^15 is rounded to a half for the
-// product (half a step, 2^-11, under the output's own rounding; what lies under 2^-14 is off by 2^-25 absolute, 2^-32 of
-// the row's largest term); the denominator takes it in fp32.
+// product (half a step, 2^-11: under a bf16 output's own rounding, as much as an fp16 output's; what lies under 2^-14 is off by
+// 2^-25 absolute, 2^-32 of the row's largest term); the denominator takes it in fp32.
 //
 // Schedule.  The work is cut into tiles of 64 tokens; every CTA takes an equal run of the tiles of all (request,
 // head, row tile) groups in a row, so ragged lengths balance and one long request spreads over the GPU.  A
@@ -713,7 +713,7 @@ template <int DT, int D>
 cudaError_t launch_dim(AttnParams& P, int sms, cudaStream_t st)
 {
     // Rows that fill one 16-row tile of mma.sync stay below the memory's pace there.  More rows take the tensor cores' own path:
-    // with 24 rows (B = 32, T = 6, contexts to 8192) two such tiles took 181 us where it took 139 (now 129); with 20 or 24 rows of one short
+    // with 24 rows (B = 32, T = 6, contexts to 8192) two such tiles took 181 us where it took 139 (now 132); with 20 or 24 rows of one short
     // context both are launch and latency.  With 8 to 16 rows it cannot pay, its tiles cost the same from one row to 48.
     return P.R <= MR ? launch_rows<DT, D>(P, sms, st) : launch_attention_tc(P, DT, sms, st);
 }

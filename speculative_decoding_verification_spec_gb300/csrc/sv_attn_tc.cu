@@ -6,10 +6,11 @@
 //   S^T [128 tokens, rows] = K [128, D] Q^T:   the codes of K go from memory to the product as they are (e4m3 x e4m3);
 //       a row of q, scaled by a power of two to a largest element in [128, 256), is split into e4m3 terms that sum to it,
 //       two for bf16 (4 bits each, the residual's sign the ninth: exact for elements above 2^-10 of the largest, off by at
-//       most 2^-17 of it below) and three for halfs, whose products accumulate.
+//       most 2^-17 of it below) and three for halfs (exact above 2^-6, and the same below), whose products accumulate.
 //   O^T [D, rows] += V^T [D, 128] P^T:   halfs; six warps widen the codes of V into shared memory, and the weights are
-//       rounded to halfs (half a step, 2^-11, under the output's own rounding; a weight below 2^-14 is off by 2^-25
-//       absolute, 2^-32 of the row's largest, as HEAD says).
+//       rounded to halfs (half a step, 2^-11: under a bf16 output's own rounding, as much as an fp16 output's; a weight below
+//       2^-14 is off by 2^-25 absolute, 2^-32 of the row's largest, as HEAD says).  The product needs 16-bit operands, and a
+//       bf16 weight would be off by 2^-9.
 // The round's own rows come last, as tiles of their own: keys and values as halfs scaled by a power of two per token, and a
 // copy of q as halfs.
 //
@@ -26,8 +27,8 @@
 // What bounds it: neither memory nor the tensor cores, but the chain that each tile goes through (S^T, softmax, P, O^T): some
 // 2000 to 2800 cycles up to 48 rows and 3600 at 87, of which a product takes about 100 whatever its columns, and some 12000
 // to 20000 more where a CTA changes the group (q, the first reference, the round's own rows, the outputs).  The issue slots are
-// 44% used, DRAM 27%.  B = 32, contexts to 8192, T = 6, four query heads a head: 129 us for 347 MB (2.7 TB/s); to 4096, T = 65
-// (three row tiles of 87): 375 us for 89 GFLOP (238 TFLOP/s).  A third softmax group (spills), S^T fetched a chunk ahead, and
+// 44% used, DRAM 25%.  B = 32, contexts to 8192, T = 6, four query heads a head: 132 us for 347 MB (2.6 TB/s); to 4096, T = 65
+// (three row tiles of 87): 382 us for 89 GFLOP (233 TFLOP/s).  A third softmax group (spills), S^T fetched a chunk ahead, and
 // both terms of q stacked into one product of twice the columns were slower: 202, 142 and 147 us where this took 139.
 // Every wait on an mbarrier is bounded; when one runs out the CTA's remaining groups report SPEC_ROW_TIMEOUT.  Between named
 // barriers the threads of a softmax group never part: what a wait returned is agreed on before anyone acts on it.

@@ -19,8 +19,9 @@
 // vectors start at its own first boundary, the few entries before it and after its last whole vector go one by one.
 //
 // Measured: 59 us for the 197 MB of (B, R, V) = (64, 6, 128256) bf16 (3.4 TB/s), 290 us for the 1.1 GB of (32, 65, 128256) under
-// a mask (3.8 TB/s).  What keeps it from a copy's rate is a CTA's own chain (history, barriers, first loads, touched entries)
-// against the few rows that follow it, and in the large case the writes.
+// a mask (3.8 TB/s, where a copy moves 6.8).  What keeps it from a copy's rate are a CTA's phases: history, barriers, first loads,
+// copy and touched entries follow one another, and the touched entries are read and written a second time after their
+// lines have gone out.
 #include <type_traits>
 
 #include "sv_round.cuh"
