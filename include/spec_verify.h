@@ -479,7 +479,7 @@ spec_status kv_cache_read(const void* k_cache, const void* v_cache, const float*
                           const int32_t* lens, const int32_t* start, int B, int max_len, void* k_out, void* v_out,
                           spec_dtype dtype, int32_t* row_status, void* stream);
 
-/* Bytes of workspace of a verify_attention call; 0 for sizes that it refuses. */
+/* Bytes of workspace of a verify_attention call; 0 for sizes that it refuses, and never less for a larger T. */
 size_t verify_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
 
 /*

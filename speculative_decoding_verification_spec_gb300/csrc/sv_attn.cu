@@ -727,9 +727,10 @@ cudaError_t launch_attn_merge(const AttnParams& P, int dtype, int ctas, int MR, 
     return P.D == 128 ? launch_merge<DT_F16, 128>(P, ctas, MR, st) : launch_merge<DT_F16, 64>(P, ctas, MR, st);
 }
 
-size_t attn_workspace_bytes(int D)
+// Never less for more rows, so that a workspace for the longest round serves the shorter ones.
+size_t attn_workspace_bytes(int rows, int D)
 {
-    const size_t few = ATTN_MAX_CTAS * part_floats(16, D), many = ATTN_MAX_TC_CTAS * part_floats(128, D);
+    const size_t few = ATTN_MAX_CTAS * part_floats(MR, D), many = rows > MR ? ATTN_MAX_TC_CTAS * part_floats(rows, D) : 0;
     return ATTN_MAX_CTAS * sizeof(AttnJoin) + 2 * (few > many ? few : many) * sizeof(float);
 }
 

@@ -141,8 +141,8 @@ cudaError_t launch_cache_read(const CacheReadParams& P, int dtype, int sms, cuda
 // ---------------------------------------------------------------- attention
 
 constexpr int ATTN_MAX_ROWS = 256;   // rows of a round (T)
-constexpr int ATTN_MAX_CTAS = 1024;  // CTAs of one launch (few rows): the workspace holds two parts for each
-constexpr int ATTN_MAX_TC_CTAS = 256;  // and of the kernel for many rows
+constexpr int ATTN_MAX_CTAS = 512;   // CTAs of one launch (few rows; three an SM): the workspace holds two parts for each
+constexpr int ATTN_MAX_TC_CTAS = 160;  // and of the kernel for many rows (one an SM)
 
 // a group of rows that starts in one streaming CTA and ends in a later one (parts == 0: none starts there)
 struct AttnJoin {
@@ -181,7 +181,7 @@ struct AttnParams {
 // polls of a bounded wait (spec_set_wait_limit)
 int wait_limit_polls();
 
-size_t attn_workspace_bytes(int D);
+size_t attn_workspace_bytes(int rows, int D);  // rows: of a row tile, at most 128
 cudaError_t launch_attention(AttnParams& P, int dtype, int sms, cudaStream_t st);
 
 }  // namespace sv

@@ -190,7 +190,8 @@ spec_status kv_cache_read(const void* k_cache, const void* v_cache, const float*
 size_t verify_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D)
 {
     if (B < 0 || T < 1 || T > ATTN_MAX_ROWS || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
-    return attn_workspace_bytes(D);
+    const long long rows = (long long)T * (Hq / Hkv);
+    return attn_workspace_bytes(rows < 128 ? (int)rows : 128, D);
 }
 
 spec_status verify_attention(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import speculative_decoding_verification_spec_gb300 as sv
-from speculative_decoding_verification_spec_gb300 import binding
+from speculative_decoding_verification_spec_gb300 import binding, build_ext
 
 
 class On(torch.Tensor):
@@ -123,6 +123,17 @@ def test_codes_have_to_be_e4m3(i):
                 f(dict(args, **{name: args[name].to(dtype)}))
         with pytest.raises(Reached):
             f(dict(args, **{name: args[name].view(torch.float8_e4m3fn)}))
+
+
+def test_the_workspace_is_that_of_the_rows(monkeypatch):
+    monkeypatch.undo()
+    build_ext.build()
+    need = lambda T, hq, hkv, D: sv.load().verify_attention_workspace_bytes(1, T, hq, hkv, D)
+    for D in (64, 128):
+        assert need(1, 32, 8, D) <= 9 << 20 and need(256, 64, 1, D) <= 22 << 20
+        for hq, hkv in ((1, 1), (8, 2), (40, 8), (64, 4)):
+            sizes = [need(T, hq, hkv, D) for T in range(1, 257)]
+            assert sizes == sorted(sizes) and all(n % 16 == 0 for n in sizes)
 
 
 def test_the_stream_has_to_be_on_the_call_s_device(monkeypatch):
