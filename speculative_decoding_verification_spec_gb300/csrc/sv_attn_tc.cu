@@ -54,7 +54,8 @@ constexpr float WINDOW = 15.9f;  // a weight may reach 2^WINDOW (the largest hal
 constexpr float HEAD = 7.0f;     // a moved reference leaves the maximum at 2^HEAD, so a weight 2^-32 of the largest is the least that a
                                  // half still holds, as on the few-rows path.  More room above means fewer repeated tiles: with 3
                                  // (and 2^-28) B = 32, T = 6, T = 65 and eight query heads a head took 134, 362 and 169 us, with 7
-                                 // 137, 384 and 186; but a row whose weight lies on one token loses a percent of the others
+                                 // 137, 384 and 186; but with 3 a row whose weight lies nearly all on one token has the others'
+                                 // weights off by up to 2%, with 7 by 0.13% at 32768 of them
 constexpr float LATE = 7.0f;     // where a move is due, columns past 2^LATE move with it: later repeats are fewer (B = 32, T = 65:
                                  // 384 us, 417 with 11; T = 6, eight query heads a head: 186 and 209).  Under WINDOW by more than the
                                  // two passes' roundings differ, so that a weight past it does move
