@@ -609,11 +609,15 @@ struct Row {
                 if (lane >= o) upto += y;
             }
             if (lane == 31) sh.warp32[w] = __float_as_uint(upto);
-            if (tid == 0) sh.from = -1, sh.to = BINS - 1, sh.count = 0;
+            if (tid == 0) sh.from = BINS, sh.to = -1, sh.count = 0;
             __syncthreads();
-            float before = upto - s;
+            float before = 0.0f;  // up to this warp's bins
 #pragma unroll 1
             for (int i = 0; i < w; ++i) before += __uint_as_float(sh.warp32[i]);
+            // A thread's sums go on from the very number at which its neighbour's end: summed in another order the two would differ
+            // in their last bits, and a level between them be met by two threads or by none.
+            const float end = before + upto, prev = __shfl_up_sync(0xffffffffu, end, 1);
+            if (lane > 0) before = prev;
             // bins' masses are right to 2^-13 together; counts are exact
             const float left = (float)(want - over0), tol = count ? 0.0f : left * 0x1p-12f;
             // (of the mass in the middle of bin 0)
@@ -621,14 +625,15 @@ struct Row {
             const float lo = (left - tol) * unit, hi = (left + tol) * unit;
 #pragma unroll
             for (int k = 0; k < BPT; ++k) {
-                const float after = before + m[k];
-                if (before < lo && after >= lo) sh.from = tid * BPT + k;
-                if (before < hi && after >= hi) sh.to = tid * BPT + k;
+                const float after = k < BPT - 1 ? before + m[k] : end;
+                // (sums of rounded terms may fall by their last bits and meet a level twice; all CTAs have the same ones, and go the same way)
+                if (before < lo && after >= lo) atomicMin(&sh.from, tid * BPT + k);
+                if (before < hi && after >= hi) atomicMax(&sh.to, tid * BPT + k);
                 before = after;
             }
             __syncthreads();
-            const int from = sh.from, to = sh.to;
-            if (from < 0 || to < from) return false;
+            const int from = sh.from, to = sh.to < 0 ? BINS - 1 : sh.to;
+            if (from == BINS) return false;
             // What lies above the bracket, and the bracket's logits.  (A quarter of a bin more on either side: at a bin's border the
             // two roundings may differ.)
             const float x1 = from == 0 && level == 0 ? __int_as_float(0x7f800000) : upper - ((float)from - 0.75f) / per;
