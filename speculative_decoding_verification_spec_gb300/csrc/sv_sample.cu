@@ -173,7 +173,12 @@ struct Vec<DT_F32> {
 };
 
 // A row's scale: c = log2(e) / T as a pair, K, and the origin that logits are taken from: 0, or the largest where |max c| is so
-// large that it has to be (what counts then lies near it, and the difference is exact).
+// large that it has to be (what counts then lies near it, and the difference is exact).  The product with c's second part comes behind J
+// (see Mass): of a c of 16 bits that part is up to 2^-15 of it, and from 128 octaves (with the 46 that matter, 2^-7.5 at most) bf16 logits
+// are taken from the largest.  (From 16384 octaves on, as in fp32, masses were off by up to 2^-15.)  A logit that has 2^-14 of the largest mass then
+// lies within a ninth of it: the difference has 7 bits, and its product with 16 is exact.
+template <int DT>
+constexpr float FAR_OCTAVES = DT == DT_BF16 ? 128.0f : 16384.0f;
 struct Scale {
     float hi, lo, origin;
     int K;
@@ -1246,7 +1251,7 @@ __global__ void __launch_bounds__(SNT, 2) sample_kernel(const __grid_constant__ 
         R.c.hi = __fdiv_rn(E_HI, T);
         if (DT == DT_BF16) R.c.hi = __uint_as_float(__float_as_uint(R.c.hi) & 0xffffff00u);  // 16 bits: see Mass
         R.c.lo = __fdiv_rn(__fadd_rn(fmaf(-R.c.hi, T, E_HI), E_LO), T);
-        R.c.origin = fabsf(top * R.c.hi) < 16384.0f ? 0.0f : top;
+        R.c.origin = fabsf(top * R.c.hi) < FAR_OCTAVES<DT> ? 0.0f : top;
         R.c.K = (int)rintf((top - R.c.origin) * R.c.hi);
         float g = NEG_INF;
         if (mp > 0.0f) {  // min-p
