@@ -558,7 +558,7 @@ spec_status verify_attention_window(const void* q, const int64_t* q_strides, con
  *   out_tokens [N]          the smallest v with u * Z < C(v), C the cumulated mass of the kept tokens in ascending order;
  *                           tokens without mass are never drawn
  *   logprob [N] (nullable)  ln of its probability among the kept tokens, fp32
- * Masses are whole numbers of 2^-44 of the largest, right to 2^-30 of themselves; what is kept and drawn follows from exact sums
+ * Masses are whole numbers of 2^-44 of the largest, right to 2^-28 of themselves; what is kept and drawn follows from exact sums
  * of them.  row_status [N] (nullable), each with token -1 and logprob NaN: SPEC_ROW_NONFINITE (a NaN, +inf, or no finite logit),
  * SPEC_ROW_BAD_UNIFORM, SPEC_ROW_BAD_PARAM (a setting outside the ranges above).
  */

@@ -11,7 +11,7 @@
 // cluster barrier and take the same decisions from the same records.  With many rows a row is one CTA, which reads it again from
 // L2 for each of its sweeps (RMEM): two rows an SM, no cluster barriers.  launch_type() has the rule and both sides' times.
 //
-// Arithmetic.  With c = log2(e) / T a token's mass is 2^(44 + x c - K), K the whole number nearest to max c, right to 2^-30 of
+// Arithmetic.  With c = log2(e) / T a token's mass is 2^(44 + x c - K), K the whole number nearest to max c, right to 2^-28 of
 // itself (Mass) and rounded to a whole number, so sums do not depend on their order, a border is crossed by one token or the other,
 // and a uniform falls as near to one as the masses are off once in some 10^4 draws among 50000 tokens.  Sums of 2^18 masses stay under
 // 2^63.  The exponential unit alone is right to 2^-22: a kernel that summed with it, and drew the rows again whose decisions that left in
@@ -184,8 +184,15 @@ struct Scale {
     int K;
 };
 
-// Masses as A 2^22 + B, each in the low bits of a float next to a power of two: sums of n of them, n <= 2^9, in 32 bits.
+// units of 512 vectors of a row that begins anywhere in its first vector
+constexpr int units_of(int V, int epv) { return ((V + 2 * epv - 2) / epv + UNIT - 1) / UNIT; }
+
+// Masses as A 2^22 + B, each in the low bits of a float next to a power of two: sums of n of them in 32 bits.  A thread meets a
+// vector a unit, of the widest row as one CTA 520 logits (516 in fp32), and a mass is 2^(44 + 1/2) at most, and what K misses (FAR_OCTAVES):
+// 2^-8 of an octave in bf16, less in fp32.
 struct Part {
+    static constexpr int MOST = units_of(SAMPLE_MAX_V, 8) * 8;
+    static_assert(MOST >= units_of(SAMPLE_MAX_V, 4) * 4 && MOST * 1.42 * (1 << 22) < 0x1p32 && MOST * 0x1p21 < 0x1p31, "A's sum, and B's, which has a sign");
     uint32_t a, b, n;
     __device__ __forceinline__ void add(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1)
     {
@@ -197,8 +204,9 @@ struct Part {
 };
 
 // The masses of two logits: x c as a pair of floats, J / 32 next to it, 2^(J / 32) from the table and e^z - 1 of the rest
-// (|z| < 2^-6.5) as its series to z^4, whose fp32 roundings are 2^-24 of it.  Logits 80 octaves down are held there: no part of 2^-44.
-// The table stands in shared memory once a lane, so that a warp's loads meet no bank twice.
+// (|z| < 2^-6.1, with c's second part) as its series to z^4.  Of a mass that leaves the roundings of z, up to 2^-30 together, and of its
+// product with the table's value, 2^-30: of 400,000 masses followed step by step the worst is off by 2^-28.5, the root of the mean square is 2^-31.
+// Logits 80 octaves down are held there: no part of 2^-44.  The table stands in shared memory once a lane, so that a warp's loads meet no bank twice.
 template <int DT>
 struct Mass {
     u64 origin, hi, lo;
@@ -271,7 +279,7 @@ __device__ __forceinline__ u64 scaled_floor(float u, u64 z, bool& more)
     const int s = 150 - (e ? e : 1);  // u = m 2^-s, s >= 24
     const u64 hi = __umul64hi(m, z), lo = m * z;
     const u64 q = s < 64 ? hi << (64 - s) | lo >> s : s < 128 ? hi >> (s - 64) : 0ull;
-    more = s < 64 ? (lo << (64 - s)) != 0 : (lo | hi) != 0;  // (u < 2^-40: no product is whole but zero)
+    more = (s < 64 ? lo << (64 - s) : lo | (s < 128 ? hi & ((1ull << (s - 64)) - 1) : hi)) != 0;
     return q;
 }
 
@@ -1282,8 +1290,7 @@ template <int DT>
 cudaError_t launch_type(SampleParams& P, int sms, cudaStream_t st)
 {
     constexpr int EPV = Vec<DT>::N;
-    // units of 512 vectors of a row that begins anywhere in its first vector
-    const int units = ((P.V + 2 * EPV - 2) / EPV + UNIT - 1) / UNIT;
+    const int units = units_of(P.V, EPV);
     // with few rows as many CTAs as the GPU has room for
     const int room = sms / P.N;
     const int most_units = SAMPLE_UNITS - (DT == DT_BF16);  // beside the counts
@@ -1315,7 +1322,7 @@ cudaError_t launch_type(SampleParams& P, int sms, cudaStream_t st)
     const size_t smem = (size_t)P.units * UNIT * 16;
     auto* kern = sample_kernel<DT, false>;
     // (set once, to what the widest row takes: threads that call at once do not lower each other's)
-    constexpr int WIDEST = ((SAMPLE_MAX_V + 2 * EPV - 2) / EPV + UNIT - 1) / UNIT, EACH = (WIDEST + MAX_CL - 1) / MAX_CL;
+    constexpr int WIDEST = units_of(SAMPLE_MAX_V, EPV), EACH = (WIDEST + MAX_CL - 1) / MAX_CL;
     constexpr int MOST = (EACH > SAMPLE_UNITS ? EACH : SAMPLE_UNITS) * UNIT * 16;
     static PerDevice kept;
     int& done = kept.here();
