@@ -608,6 +608,13 @@ def _arg(t, dtype, shape, what, at):
 _I32, _F32 = torch.int32, torch.float32
 
 
+def _int(x, what):
+    """A whole number for the C ABI's int, which would drop the bits above 32 without a word."""
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{what} is out of range: {x}")
+    return x
+
+
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 
 
@@ -775,7 +782,7 @@ def verify_attention_window(q, cache, page_table, lens, *, window: int, sinks: i
     """verify_attention under a sliding window: a row at position p (lens[b] plus its depth in the round) sees the tokens j with
     p - j < ``window``, and those with j < ``sinks``; of the round's rows those of its path that this leaves it.  Pages without
     a token that any row sees are not read and may have been given back.  Arguments and result as there."""
-    return _attention(q, cache, page_table, lens, k, v, parents, n_rows, (window, sinks), scale, lse, out, workspace, stream)
+    return _attention(q, cache, page_table, lens, k, v, parents, n_rows, (_int(window, "window"), _int(sinks, "sinks")), scale, lse, out, workspace, stream)
 
 
 def _attention(q, cache, page_table, lens, k, v, parents, n_rows, window, scale, lse, out, workspace, stream):
@@ -921,10 +928,11 @@ def kv_pages_reserve(page_table, held, lens, free_pages, free_count, *, page_siz
     lib = load()
     at = _at(page_table)
     B, width, cap, table, hold, ln, free, count = _pages_args(page_table, held, lens, free_pages, free_count, at)
+    _int(max_new, "max_new")
     if out is None:
         out = {"slots": _new((B, max_new), torch.int64, page_table.device, stream), "row_status": _like(held, stream)}
     rc = lib.kv_pages_reserve(
-        table, width, hold, ln, _arg(n_new, _I32, (B,), "n_new", at), B, max_new, page_size, free, cap, count,
+        table, width, hold, ln, _arg(n_new, _I32, (B,), "n_new", at), B, max_new, _int(page_size, "page_size"), free, cap, count,
         _arg(out.get("slots"), torch.int64, (B, max_new), "slots", at), _arg(out.get("row_status"), _I32, (B,), "row_status", at),
         _raw_stream(stream, at))
     if rc:
@@ -941,7 +949,7 @@ def kv_pages_release(page_table, held, lens, free_pages, free_count, *, page_siz
     B, width, cap, table, hold, ln, free, count = _pages_args(page_table, held, lens, free_pages, free_count, at)
     if out is None:
         out = {"row_status": _like(held, stream)}
-    rc = lib.kv_pages_release(table, width, hold, ln, B, page_size, free, cap, count,
+    rc = lib.kv_pages_release(table, width, hold, ln, B, _int(page_size, "page_size"), free, cap, count,
                               _arg(out.get("row_status"), _I32, (B,), "row_status", at), _raw_stream(stream, at))
     if rc:
         _check(rc)
