@@ -533,7 +533,8 @@ spec_status verify_attention(const void* q, const int64_t* q_strides, const void
  *   window >= 1, sinks >= 0     at most 2^30
  *   k, v                        needed
  * Every other argument, the workspace, the statuses and the precision are verify_attention's.  Only the pages that hold a token
- * that row 0 sees are read: the others may have been given back, their entries in the table and their contents may be anything.
+ * that row 0 sees are read: the entries of the others in the table and their contents may be anything.  (Pages that have left a
+ * window are the caller's to use again: kv_pages_release gives back a request's last pages, not these.)
  */
 spec_status verify_attention_window(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
                                     const void* v, const int64_t* v_strides, spec_dtype dtype, int B, int T, int Hq,
@@ -560,7 +561,8 @@ spec_status verify_attention_window(const void* q, const int64_t* q_strides, con
  *   logprob [N] (nullable)  ln of its probability among the kept tokens, fp32
  * Masses are whole numbers of 2^-44 of the largest, right to 2^-28 of themselves; what is kept and drawn follows from exact sums
  * of them.  row_status [N] (nullable), each with token -1 and logprob NaN: SPEC_ROW_NONFINITE (a NaN, +inf, or no finite logit),
- * SPEC_ROW_BAD_UNIFORM, SPEC_ROW_BAD_PARAM (a setting outside the ranges above).
+ * SPEC_ROW_BAD_UNIFORM, SPEC_ROW_BAD_PARAM (a setting outside the ranges above).  Tokens are masked best with -inf: with top_k, a finite mask that
+ * leaves fewer than k tokens costs fp32 rows several times as much.
  */
 spec_status sample_logits(const void* logits, int64_t row_stride, spec_dtype dtype, int N, int V, const float* uniforms,
                           const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
@@ -612,8 +614,9 @@ spec_status qk_norm_rope(const void* q, const int64_t* q_strides, const void* k,
  * no room.  held and free_count are updated; the table is left as it is.
  *
  * SPEC_ROW_BAD_LENGTH, and nothing of the request changes: a negative length or n_new, n_new over max_new, more pages than the
- * table is wide; in a release a length past the pages held.  A free_count outside 0 .. capacity serves nobody and stays.  Pages' numbers are
- * passed on as they are.  Both calls read and write held and free_count: calls on one free list belong on one stream.
+ * table is wide; in a release a length past the pages held.  A free_count outside 0 .. capacity serves nobody who needs pages (or gives
+ * some back) and stays.  Pages' numbers are passed on as they are; what a page holds is not looked at.  The time grows with the square
+ * of B past 1024: some 7 ms at 65535.  Both calls read and write held and free_count: calls on one free list belong on one stream.
  */
 spec_status kv_pages_reserve(int32_t* page_table, int table_width, int32_t* held, const int32_t* lens, const int32_t* n_new,
                              int B, int max_new, int page_size, const int32_t* free_pages, int capacity, int32_t* free_count,

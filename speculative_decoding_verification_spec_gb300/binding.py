@@ -781,8 +781,10 @@ def verify_attention_window(q, cache, page_table, lens, *, window: int, sinks: i
                             stream=None):
     """verify_attention under a sliding window: a row at position p (lens[b] plus its depth in the round) sees the tokens j with
     p - j < ``window``, and those with j < ``sinks``; of the round's rows those of its path that this leaves it.  Pages without
-    a token that any row sees are not read and may have been given back.  Arguments and result as there."""
-    return _attention(q, cache, page_table, lens, k, v, parents, n_rows, (_int(window, "window"), _int(sinks, "sinks")), scale, lse, out, workspace, stream)
+    a token that any row sees are not read: their entries in the table may be anything.  (kv_pages_release gives back a request's last
+    pages, not those that have left a window.)  Arguments and result as there."""
+    reach = (_int(window, "window"), _int(sinks, "sinks"))
+    return _attention(q, cache, page_table, lens, k, v, parents, n_rows, reach, scale, lse, out, workspace, stream)
 
 
 def _attention(q, cache, page_table, lens, k, v, parents, n_rows, window, scale, lse, out, workspace, stream):
@@ -962,9 +964,9 @@ def sample_logits(logits, uniforms, *, temperature=None, top_k=None, top_p=None,
 
     logits [N, V] (bf16 or fp32; any row stride, so one row expanded to N will do), ``uniforms`` [N] fp32 in [0, 1).  Settings per row, each [N] or None
     (off): ``temperature`` fp32 (0: the largest logit's token, otherwise 1e-30 to 1e30), ``top_k`` int32 (0: off; ties are kept), ``top_p`` fp32
-    (>= 1: off; whole groups of equal logits, inclusive), ``min_p`` fp32 (0: off), applied in this order.  Returns
-    dict(tokens [N] int32, row_status and, with ``logprob``, logprob [N]: the ln of the token's probability among the
-    kept ones).
+    (>= 1: off; whole groups of equal logits, inclusive), ``min_p`` fp32 (0: off), applied in this order.  Mask tokens with -inf: a large
+    finite number is right too, but slower with ``top_k`` in fp32.  Returns dict(tokens [N] int32, row_status and, with ``logprob``,
+    logprob [N]: the ln of the token's probability among the kept ones).
     """
     lib = load()
     at = _at(logits)

@@ -11,7 +11,9 @@
 // all of them have read.
 //
 // What bounds it: latency, dependent reads and a prefix sum over the batch; with long prompts the slot map's writes.  On the GPU a
-// reservation for 256 requests of a round and the release after it take 8 us, for 64 prompts (524,000 rows) and their release 14.
+// reservation for 256 requests of a round and the release after it take 8 us, for 64 prompts (524,000 rows) and their release 14.  Past 1024
+// requests every request's CTAs sum what stands before it, together half a square of the batch: 1024 requests take 21 us, 3000 40,
+// 8192 161, 16384 516 and 65535 7 ms.
 #include "sv_round.cuh"
 
 namespace sv {

@@ -21,13 +21,17 @@
 // top-k up to 512 those at or above a bound that the threads' maxima give, for min-p those that it keeps.  Otherwise a row of bf16 is
 // counted by value (counted()).  In fp32 a histogram of masses (with the sum of all, in one sweep) or of counts brackets the threshold
 // to a bin or so, whose logits are listed; a bracket with more of them gets bins of its own, and a group of ties is taken as one.
-// Bisection over the row where that fails: a threshold under the bins.
+// Bisection over the row where that fails: a threshold under the bins.  Top-k's bins reach 32 under the largest logit, so it is what a
+// row in fp32 gets whose mask, a large finite number, leaves fewer than k tokens: 64 rows of 50257 with k = 50 and three tokens left take
+// 102 us, 13 without a mask and 11 with -inf, which the list leaves out (in bf16 29, 12 and 10).
 //
 // What bounds it.  With top-p the shared memory's atomics and lookups, one of each a logit at random places, and that SMs get
 // three rows or four: 512 rows of 152064 take 108 us on the GPU (23 are the copy rate's), a row some 50 of which 18 are the first sweep, with the
-// counts, and 15 the one that draws.  In fp32 the issue slots: 30 to 45 instructions a logit in the sweep that forms the masses and the bins, 25
-// in the one that sums what lies over the bracket.  With top-k the chain of a row's steps: 64 rows of 128256 take 15 us on the
-// GPU, 5 for the loads, 3 for the bound and the exchange, 3 for the list and 4 for what rank 0 does with it.
+// counts, and 15 the one that draws.  In fp32 the chain of a row's sweeps and steps behind the cluster's barriers, and
+// clusters that last as long as their slowest row: 96 rows of 50257 with settings by row use 33% of the issue slots (30 to 45 instructions a
+// logit in the sweep that forms the masses and the bins, 25 in the one that sums what lies over the bracket) and 6% of the
+// memory's pace.  With top-k the chain of a row's steps: 64 rows of 128256 take 15 us on the GPU, 5 for the loads, 3 for the bound and the
+// exchange, 3 for the list and 4 for what rank 0 does with it.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -188,11 +192,12 @@ struct Scale {
 constexpr int units_of(int V, int epv) { return ((V + 2 * epv - 2) / epv + UNIT - 1) / UNIT; }
 
 // Masses as A 2^22 + B, each in the low bits of a float next to a power of two: sums of n of them in 32 bits.  A thread meets a
-// vector a unit, of the widest row as one CTA 520 logits (516 in fp32), and a mass is 2^(44 + 1/2) at most, and what K misses (FAR_OCTAVES):
-// 2^-8 of an octave in bf16, less in fp32.
+// vector a unit, of the widest row as one CTA 520 logits (516 in fp32), and a mass is 2^(44 + 1/2) at most, but for what K, rounded
+// from c's first part, misses: 2^-8 of an octave (FAR_OCTAVES).
 struct Part {
     static constexpr int MOST = units_of(SAMPLE_MAX_V, 8) * 8;
-    static_assert(MOST >= units_of(SAMPLE_MAX_V, 4) * 4 && MOST * 1.42 * (1 << 22) < 0x1p32 && MOST * 0x1p21 < 0x1p31, "A's sum, and B's, which has a sign");
+    static_assert(MOST >= units_of(SAMPLE_MAX_V, 4) * 4 && MOST * 1.42 * (1 << 22) < 0x1p32 && MOST * 0x1p21 < 0x1p31,
+                  "A's sum, and B's, which has a sign");
     uint32_t a, b, n;
     __device__ __forceinline__ void add(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1)
     {
@@ -1299,7 +1304,9 @@ cudaError_t launch_type(SampleParams& P, int sms, cudaStream_t st)
     cl = cl < units ? cl : units;
     cl = cl < MAX_CL ? cl : MAX_CL;
     // A row as one CTA: from three quarters of a row an SM on (96 rows of 50257 in fp32 with mixed settings take 37 us as clusters, 54 as a
-    // CTA each; 100 of 152064 in bf16 without top-k and top-p 45 and 40).  Of bf16, where top-k or top-p may need the counts, also where the
+    // CTA each; 100 of 152064 in bf16 without top-k and top-p 45 and 40).  In fp32 that border is too late for the widest rows, whose clusters
+    // come in waves: with top-p 32, 64 and 113 rows of 152064, one CTA an SM, take 103, 172 and 280 us and 114 as a CTA each 100; of 128256
+    // 53, 96 and 152, and 85; of 50257 26, 36 and 56, and 41.  Of bf16, where top-k or top-p may need the counts, also where the
     // clusters would come in two waves (64 rows of 152064 with top-p 44 us as clusters and 36 as a CTA each, 48 rows 30 and 43, one row 17
     // and 34), and some short rows, over which a cluster's steps are long (of 32000 48 rows 21 and 16, 32 rows 15 and 16, one row 13 and 15).
     const bool one = P.N >= sms - sms / 4 ||
