@@ -948,7 +948,7 @@ __device__ __forceinline__ void draw(Row<DT, RMEM>& R, int row, float u, float p
 // mass and place MAGS - 1.  The sweep for the largest logit counts by the way (`done`), as if it were 64; what does not fit is counted
 // again.  Ranks go through them from the largest value on: rank r is place MAGS - 1 - r, or r; the zero of the second half is taken with
 // the first's.  The CTAs of a cluster share the groups of 32 ranks out, each of which sums the counts of all for its own.  False, and nothing,
-// where a logit in place 0 is no zero.  `mass`: 2 MAGS of them, for the sweep that draws where a row is one CTA.
+// where a logit in place 0 is no zero and may have mass.  `mass`: 2 MAGS of them, for the sweep that draws where a row is one CTA.
 //
 // (512 rows of 152064 with top-p: 111 us; 118 with loads that L1 may not keep, 132 with the counts as a sweep of their own and the
 // loads of the drawing sweep one ahead, 300 with a mass a logit and the bracket of bins.  One row, by eight CTAs: 17 us; 35 where each
@@ -1002,7 +1002,8 @@ __device__ __forceinline__ bool counted(Row<DT_BF16, RMEM>& R, int row, float u,
     }
     const uint32_t zeros = sh.v.n[0] + sh.v.n[MAGS];
     bool tiny = false;
-    if (zeros && low <= 0.0f && base > 0) {
+    // (of place 0, magnitudes up to 2^16 base's: where the first sweep's places are for larger logits, all of the mass may lie in it)
+    if (zeros && base > 0 && low <= __uint_as_float((uint32_t)base << 16)) {
         u64 all = 0;
         R.sweep([&](const uint4& v, int) {
             const uint32_t q[4] = {v.x, v.y, v.z, v.w};
